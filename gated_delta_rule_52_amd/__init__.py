@@ -21,6 +21,12 @@ respect to the raw rows, and a training pair must pass the same value to both
 calls.  The numerical-safety options of the chunked calls (wy_eps damping of
 the WY solve, clip at the stage boundaries, diag stage counters read back with
 gdn_diag_read) follow include/gdn.h.
+
+The operators that stand around the layer in a stack with softmax-attention
+layers (norms before and after a block, packed attention with its gradients, a
+paged cache) are in block.py and are names of this package too: gdn_norm_block,
+gdn_norm_gate, gdn_attn_forward, gdn_attn_append, gdn_attn_paged and the
+backward calls.
 """
 from __future__ import annotations
 
@@ -43,7 +49,11 @@ EXPORTS = ("gdn_new_state", "gdn_workspace_bytes", "gdn_forward", "gdn_forward_n
            "gdn_backward",
            "gdn_forward_train", "gdn_backward_train", "gdn_decode_step", "gdn_diag_read",
            "gdn_replay_buffer_bytes", "gdn_replay_reset", "gdn_replay_step", "gdn_replay_fold",
-           "gdn_status_string")
+           "gdn_status_string",
+           # the operators around the layer (block.py)
+           "gdn_norm_workspace_bytes", "gdn_norm_block", "gdn_norm_block_backward", "gdn_norm_gate",
+           "gdn_norm_gate_backward", "gdn_attn_workspace_bytes", "gdn_attn_forward",
+           "gdn_attn_backward", "gdn_attn_append", "gdn_attn_paged")
 # include/gdn_profile.h: exported by the measurement build only
 PROFILE_EXPORTS = ("gdn_profile_begin", "gdn_profile_end", "gdn_profile_launch_name")
 
@@ -117,6 +127,7 @@ def lib():
         L.gdn_replay_fold.restype = i
         L.gdn_status_string.argtypes = [i]
         L.gdn_status_string.restype = ctypes.c_char_p
+        block.declare(L)
         _lib = L
     return _lib
 
@@ -427,3 +438,9 @@ def gdn_replay_fold(ckpt, buf, depth, *, per_channel=True):
         raise ValueError("buf is smaller than gdn_replay_buffer_bytes for this shape and depth")
     _call(lib().gdn_replay_fold, "gdn_replay_fold", ctypes.byref(sh), _ptr(ckpt), _ptr(buf),
           int(depth), _stream())
+
+
+from . import block  # noqa: E402  (it takes the names above)
+from .block import (GDN_ATTN_BACKWARD, GDN_ATTN_PAGED, GdnAttnShape, GdnNormShape,  # noqa: E402,F401
+                    gdn_attn_append, gdn_attn_backward, gdn_attn_forward, gdn_attn_paged, gdn_norm_block,
+                    gdn_norm_block_backward, gdn_norm_gate, gdn_norm_gate_backward)

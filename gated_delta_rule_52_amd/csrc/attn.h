@@ -1,0 +1,249 @@
+// attn.h -- what the softmax-attention kernels share: 32 x 32 tiles on the
+// matrix cores, row tables in LDS, and the way a workgroup finds its rows.
+//
+// Fragments.  An operand fragment holds 8 values a lane: lane l (m = l % 32,
+// h = l / 32), element j, is operand row (A) or column (B) m at contraction
+// index kappa(h, j) of a 16-long block.  Any kappa gives the same product as
+// long as A and B agree on it; two are used:
+//   plain:    kappa = 8 h + j                      (operands read along their rows)
+//   permuted: kappa = 8 (j / 4) + 4 h + j % 4      (accumulators fed back as operands)
+// bf16 takes one v_mfma_f32_32x32x16_bf16 a fragment pair, fp32 eight
+// v_mfma_f32_32x32x2_f32, the j-th over element j of both.
+// Accumulator: lane l holds column l % 32, rows 8 (r / 4) + 4 h + r % 4 in
+// acc[r], r = 0..15: registers 8 b .. 8 b + 7 are, in the permuted order, the
+// 16 rows from 16 b.  So with scores computed as S^T = K Q^T (a lane is one
+// query, its registers are keys) a lane's probabilities are the next product's
+// operand as they stand, and a row's maximum and sum need one exchange between
+// the lane halves.
+#pragma once
+
+#include "common.h"
+#include "attn_plan.h"
+
+namespace gdn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+template <typename T> struct FragOf;
+template <> struct FragOf<bf16> { typedef bf16x8 type; };
+template <> struct FragOf<float> { typedef f32x8 type; };
+template <typename T> using Frag = typename FragOf<T>::type;
+
+__device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(f32x8 a, f32x8 b, f32x16 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x16 zero16()
+{
+    return f32x16{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+}
+
+// registers 8 b .. 8 b + 7 of an accumulator as an operand (permuted order)
+template <typename T> __device__ __forceinline__ Frag<T> acc_frag(const f32x16& s, int b);
+template <> __device__ __forceinline__ bf16x8 acc_frag<bf16>(const f32x16& s, int b)
+{
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = cvt2_bf16(s[8 * b + 2 * i], s[8 * b + 2 * i + 1]);
+    return __builtin_bit_cast(bf16x8, w);
+}
+template <> __device__ __forceinline__ f32x8 acc_frag<float>(const f32x16& s, int b)
+{
+    f32x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = s[8 * b + i];
+    return v;
+}
+
+// a fragment in plain order from 8 values in memory, 16-byte aligned
+template <typename T> __device__ __forceinline__ Frag<T> load_frag(const T* p);
+template <> __device__ __forceinline__ bf16x8 load_frag<bf16>(const bf16* p)
+{
+    return *reinterpret_cast<const bf16x8*>(p);
+}
+template <> __device__ __forceinline__ f32x8 load_frag<float>(const float* p)
+{
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// four accumulator rows of one column, stored as four neighbours
+template <typename T> __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d);
+template <> __device__ __forceinline__ void store4<bf16>(bf16* p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<uint2*>(p) = uint2{cvt2_bf16(a, b), cvt2_bf16(c, d)};
+}
+template <> __device__ __forceinline__ void store4<float>(float* p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+}
+
+// the value of lane l and of lane l ^ 32, the same pair in both
+__device__ __forceinline__ float2 half_pair(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return float2{__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ float half_max(float x)
+{
+    const float2 p = half_pair(x);
+    return fmaxf(p.x, p.y);
+}
+__device__ __forceinline__ float half_add(float x)
+{
+    const float2 p = half_pair(x);
+    return p.x + p.y;
+}
+
+// ---------------------------------------------------------------------------
+// row tables in LDS: rows of D elements, U = D sizeof(T) / 16 words of 16
+// bytes; word u of row r sits at word r U + (u ^ f(r)).  f is a permutation of
+// the row bits that decide a bank group, so that both reads below meet every
+// bank group once: 16-byte reads of 16 of 32 consecutive rows (a phase is the
+// lanes with equal bit 5 and equal parity of bits 2..4), and transposing reads
+// of four consecutive rows.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+struct Rows {
+    static constexpr int U = D * (int)sizeof(T) / 16;
+    static constexpr int BYTES = U * 16;
+    static constexpr int PER = 64 / U;  // rows a wave's 64 words hold
+    static_assert(U == 8 || U == 16 || U == 32, "head size");
+    static __device__ __forceinline__ int f(int r)
+    {
+        return U == 8 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3);
+    }
+    static __device__ __forceinline__ int word(int r, int u) { return r * U + (u ^ f(r)); }
+
+    // operand rows r0 .. r0 + 31 along their own values 16 kk .. + 15, plain order
+    static __device__ __forceinline__ Frag<T> along(const void* tab, int r0, int kk)
+    {
+        const int l = lane_id(), r = r0 + (l & 31), h = l >> 5;
+        const u32x4* t = reinterpret_cast<const u32x4*>(tab);
+        if constexpr (sizeof(T) == 2) {
+            return __builtin_bit_cast(bf16x8, t[word(r, 2 * kk + h)]);
+        } else {
+            const f32x4 a = __builtin_bit_cast(f32x4, t[word(r, 4 * kk + 2 * h)]);
+            const f32x4 b = __builtin_bit_cast(f32x4, t[word(r, 4 * kk + 2 * h + 1)]);
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+
+    // operand columns d0 .. d0 + 31 down rows k0 .. k0 + 15, permuted order.
+    // bf16: two transposing loads; in one, lane i of a group of 16 receives
+    // element i % 4 of what lanes 4 e + i / 4 read, e = 0..3, so lane i reads
+    // row i / 4 at columns 4 (i % 4) and gets column i of the four rows.
+    static __device__ __forceinline__ Frag<T> down(const void* tab, int k0, int d0)
+    {
+        const int l = lane_id(), h = l >> 5;
+        if constexpr (sizeof(T) == 2) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            const int i = l & 15, c = d0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
+            s16x4 v[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int r = k0 + 8 * t + 4 * h + (i >> 2);
+                const char* p = reinterpret_cast<const char*>(tab) + word(r, c >> 3) * 16 + (c & 7) * 2;
+                v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+            }
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int c = d0 + (l & 31);
+            const float* t = reinterpret_cast<const float*>(tab);
+            f32x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = k0 + 8 * (j >> 2) + 4 * h + (j & 3);
+                v[j] = t[word(r, c >> 2) * 4 + (c & 3)];
+            }
+            return v;
+        }
+    }
+
+    // Rows r0 .. r0 + N - 1 of a table from global memory, by direct loads of the
+    // calling wave (N / PER of them): row r comes from `base` + min(r - r0, last)
+    // * stride bytes.  r0 is a multiple of N, N of PER.
+    template <int N>
+    static __device__ __forceinline__ void fetch(void* tab, int r0, const void* base, uint32_t stride, int last)
+    {
+        const int l = lane_id();
+#pragma unroll
+        for (int i = 0; i < N / PER; ++i) {
+            const int rr = i * PER + l / U;
+            const int u = (l % U) ^ f(r0 + rr);
+            const uint32_t off = (uint32_t)(rr < last ? rr : last) * stride + (uint32_t)u * 16;
+            dma16(reinterpret_cast<const char*>(base) + off, reinterpret_cast<char*>(tab) + (r0 + i * PER) * BYTES);
+        }
+    }
+    // zeros in the same places
+    template <int N>
+    static __device__ __forceinline__ void clear(void* tab, int r0)
+    {
+        u32x4* t = reinterpret_cast<u32x4*>(tab) + r0 * U;
+#pragma unroll
+        for (int i = 0; i < N / PER; ++i) t[i * 64 + lane_id()] = u32x4{0, 0, 0, 0};
+    }
+};
+
+// 4-byte direct load into LDS: lane i's word lands at lds_wave_base + 4 i
+__device__ __forceinline__ void dma4(const void* gptr, const void* lds_wave_base)
+{
+    warm_line(gptr, lds_wave_base);
+}
+
+// value of a wave-uniform integer in a scalar register
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// ---------------------------------------------------------------------------
+// Packed sequences: sequence b has the rows cu[b] .. cu[b + 1] - 1.  The bounds
+// are device data: they are clamped to 0 <= start <= end <= T, so that no value
+// of theirs reaches outside the buffers.
+// ---------------------------------------------------------------------------
+struct Span {
+    int b, start, n, blk;
+};
+
+// Block `id` of all sequences' blocks of BR rows, a sequence of n tokens having
+// n * G rows; every wave finds it by itself.  False: there is no such block.
+__device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, int T, int G, int BR, int id, Span& s)
+{
+    const int l = lane_id();
+    int before = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        const int b = b0 + l < B ? b0 + l : B - 1;
+        int st = cu[b], en = cu[b + 1];
+        st = st < 0 ? 0 : st > T ? T : st;
+        en = en < st ? st : en > T ? T : en;
+        const int nb = b0 + l < B ? (int)(((long long)(en - st) * G + BR - 1) / BR) : 0;
+        int inc = nb;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(inc, d);
+            if (l >= d) inc += up;
+        }
+        const uint64_t hit = __ballot(before + inc > id);
+        if (hit) {
+            const int first = __builtin_ctzll(hit);
+            s.b = b0 + first;
+            s.start = __builtin_amdgcn_readlane(st, first);
+            s.n = __builtin_amdgcn_readlane(en, first) - s.start;
+            s.blk = id - (before + __builtin_amdgcn_readlane(inc - nb, first));
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(inc, 63);
+    }
+    return false;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace gdn

@@ -1,0 +1,319 @@
+// attn_bwd.hip -- gradients of causal softmax attention over packed prompts.
+//
+//   p_ij = exp(scale q_i . k_j - lse_i),   delta_i = do_i . o_i
+//   dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
+//
+// The probabilities are formed again from the saved log-sums.  Two passes, one
+// over the queries of a block of keys (dk, dv: a key's sum runs over all query
+// heads of its group inside one workgroup) and one over the keys of a block of
+// queries (dq): seven products where five would do, and in return no sum ever
+// crosses workgroups, so there are no atomics and the order is the same in every
+// run.  Both products that sum over an accumulator's rows take it as their
+// operand without leaving the registers (attn.h).
+#include "attn.h"
+
+namespace gdn {
+
+namespace {
+
+struct BwdArgs {
+    const void *q, *k, *v, *o, *dO;
+    const float* lse;
+    const int* cu;
+    void *dq, *dk, *dv;
+    float *lse2, *delta;  // [Hq][T]: lse * log2 e, and do . o
+    long long q_stride;
+    uint32_t q_bytes, k_bytes, v_bytes, o_bytes;  // bytes between tokens
+    int B, T, Hq, Hkv, G;
+    float scale;
+};
+
+// delta and the log-sums in base 2, by query head.  A row of D values is held by
+// D / VE lanes.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_delta_kernel(BwdArgs a)
+{
+    constexpr int VE = 16 / (int)sizeof(T), L = D / VE;
+    const size_t rows = (size_t)a.T * a.Hq;
+    const size_t row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int c = (threadIdx.x % L) * VE;
+    const size_t at = (row < rows ? row : rows - 1) * D + c;
+    float sum = 0.f;
+    const T* o = (const T*)a.o + at;
+    const T* d = (const T*)a.dO + at;
+    if constexpr (sizeof(T) == 2) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(o), y = *reinterpret_cast<const u32x4*>(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16);
+            sum += __uint_as_float(x[i] & 0xffff0000u) * __uint_as_float(y[i] & 0xffff0000u);
+        }
+    } else {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(o), y = *reinterpret_cast<const f32x4*>(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += x[i] * y[i];
+    }
+    if (L == 8) {
+        sum = lane8_sum(sum);
+    } else {
+        sum = lane16_sum(sum);
+        if (L == 32) sum += __shfl_xor(sum, 16);
+    }
+    if (c == 0 && row < rows) {
+        const size_t t = row / a.Hq, h = row % a.Hq;
+        a.delta[h * a.T + t] = sum;
+        a.lse2[h * a.T + t] = a.lse[row] * kLog2e;
+    }
+}
+
+// dk, dv of 128 keys: four waves of 32 keys, whose keys and values stay in
+// registers; tiles of QT tokens of one query head after the other go through
+// two LDS buffers.
+template <typename T, int D>
+__global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(BwdArgs a)
+{
+    constexpr int KK = D / 16, DT = D / 32;
+    constexpr int QT = sizeof(T) == 2 ? 64 : 32, RW = QT / 4;
+    constexpr int TAB = QT * Rows<T, D>::BYTES;
+    __shared__ __align__(1024) char lds[2][2][TAB];
+    __shared__ __align__(256) float ld[2][2][64];  // lse2, delta of a tile (64 lanes' words; QT are read)
+
+    const int hk = blockIdx.x % a.Hkv;
+    Span s;
+    if (!find_block(a.cu, a.B, a.T, 1, 128, blockIdx.x / a.Hkv, s)) return;
+    const int key0 = s.blk * 128;  // the first keys have the most queries: they come first
+    const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
+    const int wkey = key0 + 32 * w;
+    const int key = wkey + (l & 31);
+    const int kc = key < s.n ? key : s.n - 1;
+
+    Frag<T> kf[KK], vf[KK];
+    {
+        const T* kp = (const T*)((const char*)a.k + (size_t)(s.start + kc) * a.k_bytes) + (size_t)hk * D;
+        const T* vp = (const T*)((const char*)a.v + (size_t)(s.start + kc) * a.v_bytes) + (size_t)hk * D;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            kf[kk] = load_frag<T>(kp + 16 * kk + 8 * h);
+            vf[kk] = load_frag<T>(vp + 16 * kk + 8 * h);
+        }
+    }
+    f32x16 dk[DT], dv[DT];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) dk[dt] = dv[dt] = zero16();
+
+    const float sl2 = a.scale * kLog2e;
+    const int tq0 = key0 / QT, ntq = (s.n + QT - 1) / QT - tq0;  // query tiles at or after the block
+    const int total = ntq * a.G;
+    auto fetch = [&](int it, int buf) {
+        const int g = it / ntq, q0 = (tq0 + it - g * ntq) * QT;
+        const int hq = hk * a.G + g;
+        const int at = q0 + w * RW < s.n ? q0 + w * RW : s.n - 1;
+        const int last = s.n - 1 - at;
+        const size_t tok = (size_t)(s.start + at);
+        Rows<T, D>::template fetch<RW>(lds[buf][0], w * RW, (const char*)a.q + tok * a.q_bytes + (size_t)hq * D * sizeof(T),
+                                       a.q_bytes, last);
+        Rows<T, D>::template fetch<RW>(lds[buf][1], w * RW, (const char*)a.dO + tok * a.o_bytes + (size_t)hq * D * sizeof(T),
+                                       a.o_bytes, last);
+        const int t = q0 + l < s.n ? q0 + l : s.n - 1;
+        if (w == 0) dma4(a.lse2 + (size_t)hq * a.T + s.start + t, ld[buf][0]);
+        if (w == 1) dma4(a.delta + (size_t)hq * a.T + s.start + t, ld[buf][1]);
+    };
+    fetch(0, 0);
+    for (int it = 0; it < total; ++it) {
+        const int buf = it & 1;
+        wait_vm<0>();
+        __syncthreads();
+        if (it + 1 < total) fetch(it + 1, buf ^ 1);
+        const int q0 = (tq0 + it % ntq) * QT;
+#pragma unroll
+        for (int sub = 0; sub < QT / 32; ++sub) {
+            const int qs = q0 + 32 * sub;
+            if (qs + 31 < wkey || qs >= s.n) continue;  // every query stands before the wave's keys
+            const void* qt = lds[buf][0];
+            const void* dt_ = lds[buf][1];
+            f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(qt, 32 * sub, kk), kf[kk], sc);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) dp = mma32(Rows<T, D>::along(dt_, 32 * sub, kk), vf[kk], dp);
+            const bool edge = qs < wkey + 31 || qs + 32 > s.n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(&ld[buf][0][32 * sub + 8 * i + 4 * h]);
+                const f32x4 de = *reinterpret_cast<const f32x4*>(&ld[buf][1][32 * sub + 8 * i + 4 * h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 4 * i + e;
+                    sc[r] = exp2_hw(sc[r] * sl2 - ls[e]);
+                    dp[r] = sc[r] * (dp[r] - de[e]);
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int q = qs + 8 * (r >> 2) + 4 * h + (r & 3);
+                    const bool in = key <= q && q < s.n;
+                    sc[r] = in ? sc[r] : 0.f;
+                    dp[r] = in ? dp[r] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                // both operands are rounded to the inputs' type, as in the forward
+                const Frag<T> p = acc_frag<T>(sc, b), ds = acc_frag<T>(dp, b);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    dv[dt] = mma32(Rows<T, D>::down(dt_, 32 * sub + 16 * b, 32 * dt), p, dv[dt]);
+                    dk[dt] = mma32(Rows<T, D>::down(qt, 32 * sub + 16 * b, 32 * dt), ds, dk[dt]);
+                }
+            }
+        }
+    }
+    if (key < s.n) {
+        const size_t at = ((size_t)(s.start + key) * a.Hkv + hk) * D;
+        T* kp = (T*)a.dk + at;
+        T* vp = (T*)a.dv + at;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = 32 * dt + 8 * i + 4 * h;
+                store4<T>(kp + c, dk[dt][4 * i] * a.scale, dk[dt][4 * i + 1] * a.scale, dk[dt][4 * i + 2] * a.scale,
+                          dk[dt][4 * i + 3] * a.scale);
+                store4<T>(vp + c, dv[dt][4 * i], dv[dt][4 * i + 1], dv[dt][4 * i + 2], dv[dt][4 * i + 3]);
+            }
+    }
+}
+
+// dq of 128 rows (token * G + head): four waves of 32 rows; tiles of KT keys go
+// through two LDS buffers.
+template <typename T, int D>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdArgs a)
+{
+    constexpr int KK = D / 16, DT = D / 32;
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32, RW = KT / 4;
+    constexpr int TAB = KT * Rows<T, D>::BYTES;
+    __shared__ __align__(1024) char lds[2][2][TAB];
+
+    const int hk = blockIdx.x % a.Hkv;
+    Span s;
+    if (!find_block(a.cu, a.B, a.T, a.G, 128, blockIdx.x / a.Hkv, s)) return;
+    const int R = s.n * a.G, nblk = (R + 127) / 128;
+    const int row0 = (nblk - 1 - s.blk) * 128;
+    const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
+    const int row = row0 + 32 * w + (l & 31);
+    const int rr = row < R ? row : R - 1;
+    const int tok = rr / a.G, hq = hk * a.G + (rr - tok * a.G);
+    const size_t at = (size_t)(s.start + tok);
+    Frag<T> qf[KK], df[KK];
+    {
+        const T* qp = (const T*)a.q + at * a.q_stride + (size_t)hq * D;
+        const T* dp = (const T*)a.dO + (at * a.Hq + hq) * D;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            qf[kk] = load_frag<T>(qp + 16 * kk + 8 * h);
+            df[kk] = load_frag<T>(dp + 16 * kk + 8 * h);
+        }
+    }
+    const float lse2 = a.lse2[(size_t)hq * a.T + at], delta = a.delta[(size_t)hq * a.T + at];
+    f32x16 dq[DT];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
+    const float sl2 = a.scale * kLog2e;
+
+    const int limit = tok + 1;
+    const int wmin = __builtin_amdgcn_readlane(limit, 0), wmax = __builtin_amdgcn_readlane(limit, 31);
+    const int end = row0 + 127 < R ? row0 + 127 : R - 1;
+    const int tiles = (end / a.G + 1 + KT - 1) / KT;
+    const char* kb = (const char*)a.k + (size_t)s.start * a.k_bytes + (size_t)hk * D * sizeof(T);
+    const char* vb = (const char*)a.v + (size_t)s.start * a.v_bytes + (size_t)hk * D * sizeof(T);
+    auto fetch = [&](int t, int buf) {
+        const int k0 = t * KT + w * RW;
+        const int kat = k0 < s.n ? k0 : s.n - 1;
+        Rows<T, D>::template fetch<RW>(lds[buf][0], w * RW, kb + (size_t)kat * a.k_bytes, a.k_bytes, s.n - 1 - kat);
+        Rows<T, D>::template fetch<RW>(lds[buf][1], w * RW, vb + (size_t)kat * a.v_bytes, a.v_bytes, s.n - 1 - kat);
+    };
+    fetch(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+        const int buf = t & 1;
+        wait_vm<0>();
+        __syncthreads();
+        if (t + 1 < tiles) fetch(t + 1, buf ^ 1);
+#pragma unroll
+        for (int sub = 0; sub < KT / 32; ++sub) {
+            const int key0 = t * KT + 32 * sub;
+            if (key0 >= wmax) continue;
+            f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(lds[buf][0], 32 * sub, kk), qf[kk], sc);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) dp = mma32(Rows<T, D>::along(lds[buf][1], 32 * sub, kk), df[kk], dp);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] = exp2_hw(sc[r] * sl2 - lse2) * (dp[r] - delta);
+            if (key0 + 32 > wmin) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    dp[r] = key0 + 8 * (r >> 2) + 4 * h + (r & 3) < limit ? dp[r] : 0.f;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const Frag<T> ds = acc_frag<T>(dp, b);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+                    dq[dt] = mma32(Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt), ds, dq[dt]);
+            }
+        }
+    }
+    if (row < R) {
+        T* p = (T*)a.dq + (at * a.Hq + hq) * D;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                store4<T>(p + 32 * dt + 8 * i + 4 * h, dq[dt][4 * i] * a.scale, dq[dt][4 * i + 1] * a.scale,
+                          dq[dt][4 * i + 2] * a.scale, dq[dt][4 * i + 3] * a.scale);
+    }
+}
+
+template <typename T, int D>
+gdn_status launch(const BwdArgs& a, hipStream_t st)
+{
+    constexpr int RPB = 256 / (D * (int)sizeof(T) / 16);
+    const size_t rows = (size_t)a.T * a.Hq;
+    GDN_LAUNCH("attn_delta", (attn_delta_kernel<T, D>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
+    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv;
+    GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
+    const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv;
+    GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3((unsigned)qblocks), dim3(256), st, a);
+    return GDN_OK;
+}
+
+size_t half_ws(const gdn_attn_shape& s) { return ((size_t)s.T * s.Hq * sizeof(float) + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t attn_backward_ws(const gdn_attn_shape& s) { return 2 * half_ws(s); }
+
+gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const void* k, const void* v, const int* cu,
+                                  const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                                  void* ws, hipStream_t st)
+{
+    const uint32_t e = s.dtype == GDN_BF16 ? 2 : 4;
+    BwdArgs a{};
+    a.q = q; a.k = k; a.v = v; a.o = o; a.dO = dO; a.lse = lse; a.cu = cu;
+    a.dq = dq; a.dk = dk; a.dv = dv;
+    a.lse2 = (float*)ws;
+    a.delta = (float*)((char*)ws + half_ws(s));
+    a.q_stride = s.q_stride;
+    a.q_bytes = (uint32_t)(s.q_stride * e);
+    a.k_bytes = (uint32_t)(s.k_stride * e);
+    a.v_bytes = (uint32_t)(s.v_stride * e);
+    a.o_bytes = (uint32_t)(s.Hq * s.D * e);
+    a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
+    a.scale = s.scale;
+    if (s.dtype == GDN_BF16) return s.D == 64 ? launch<bf16, 64>(a, st) : launch<bf16, 128>(a, st);
+    return s.D == 64 ? launch<float, 64>(a, st) : launch<float, 128>(a, st);
+}
+
+}  // namespace gdn

@@ -1,0 +1,514 @@
+// norm.hip -- the norms around a block: residual add with a residual scale and
+// RMS norm before it (gdn_norm_block), RMS norm of every head with weight and
+// silu gate after it (gdn_norm_gate), each with its gradients.
+//
+//   h = x + a o y,   r = 1 / sqrt(mean(h^2) + eps),   n = r h o w
+//   dh' = dh + r (g - xh mean(g o xh)),  g = dn o w,  xh = r h
+//   dx = dh',  dy = a o dh',  dw = sum_rows dn o xh,  da = sum_rows y o dh'
+//
+//   y = oh o w o s(z),  oh = r o_,  s(z) = z / (1 + exp(-z))
+//   do = r (g - oh mean(g o oh)),  g = dy o s(z) o w
+//   dz = dy o oh o w o s'(z),  dw = sum_rows dy o s(z) o oh
+//
+// Everything is computed in fp32 and rounded once, when stored; h enters the
+// norm unrounded (the backward forms it again from x and y, which it reads
+// anyway for da).  All of these are bound by HBM: each value is read once and
+// written once, as 16-byte words.
+#include "common.h"
+#include "norm.h"
+
+namespace gdn {
+
+namespace {
+
+// VE elements in one 16-byte word
+template <typename T> struct Vec;
+template <> struct Vec<bf16> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ void load(const bf16* p, float (&v)[8])
+    {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(bf16* p, const float (&v)[8])
+    {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = cvt2_bf16(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x4*>(p) = w;
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int VE = 4;
+    static __device__ __forceinline__ void load(const float* p, float (&v)[4])
+    {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[4])
+    {
+        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+};
+
+template <int VE> __device__ __forceinline__ void load_f32(const float* p, float (&v)[VE])
+{
+#pragma unroll
+    for (int i = 0; i < VE; i += 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(p + i);
+        v[i] = w[0], v[i + 1] = w[1], v[i + 2] = w[2], v[i + 3] = w[3];
+    }
+}
+template <int VE> __device__ __forceinline__ void store_f32(float* p, const float (&v)[VE])
+{
+#pragma unroll
+    for (int i = 0; i < VE; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+}
+
+// sum over aligned groups of L lanes, the same bits in every lane of the group;
+// L = 256 is the whole workgroup of four waves (one LDS word a wave; `slot`
+// alternates between two sets so that one barrier a sum is enough)
+template <int L> __device__ __forceinline__ float group_sum(float x, float (*red)[4], int slot)
+{
+    if (L >= 2) x += dpp_mov<0xB1>(x);
+    if (L >= 4) x += dpp_mov<0x4E>(x);
+    if (L >= 8) x += dpp_mov<0x141>(x);
+    if (L >= 16) x += dpp_mov<0x140>(x);
+    if (L >= 32) x += __shfl_xor(x, 16);
+    if (L >= 64) x += __shfl_xor(x, 32);
+    if (L == 256) {
+        if (lane_id() == 0) red[slot][wave_id()] = x;
+        __syncthreads();
+        x = (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+    }
+    return x;
+}
+
+// ---------------------------------------------------------------------------
+// residual add and norm.  A row is held by L lanes, N words each.
+// ---------------------------------------------------------------------------
+template <typename T, int L, int N>
+__global__ __launch_bounds__(256) void norm_block_kernel(const T* __restrict__ x, const T* __restrict__ y,
+                                                         const float* __restrict__ a, const float* __restrict__ w,
+                                                         T* h, T* n, float* __restrict__ rstd, int rows, int width,
+                                                         float eps)
+{
+    constexpr int VE = Vec<T>::VE, R = 256 / L;
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+    const float inv = 1.0f / (float)width;
+    int slot = 0;
+    // the row index is the same for all lanes of a group and, at L = 256, for the workgroup
+    for (int row0 = blockIdx.x * R; row0 < rows; row0 += gridDim.x * R, slot ^= 1) {
+        const int row = row0 + sub;
+        const bool live = row < rows;
+        const size_t base = (size_t)(live ? row : rows - 1) * width;
+        float v[N][VE];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * L + lane) * VE;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] = 0.f;
+            if (c < width) {
+                Vec<T>::load(x + base + c, v[i]);
+                if (y) {
+                    float u[VE], s[VE];
+                    Vec<T>::load(y + base + c, u);
+                    if (a) load_f32<VE>(a + c, s);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) v[i][e] += a ? s[e] * u[e] : u[e];
+                }
+#pragma unroll
+                for (int e = 0; e < VE; ++e) ss += v[i][e] * v[i][e];
+            }
+        }
+        ss = group_sum<L>(ss, red, slot);
+        const float r = 1.0f / sqrtf(ss * inv + eps);
+        if (live) {
+            if (rstd && lane == 0) rstd[row] = r;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (i * L + lane) * VE;
+                if (c < width) {
+                    float s[VE], out[VE];
+                    load_f32<VE>(w + c, s);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) out[e] = v[i][e] * r * s[e];
+                    if (h) Vec<T>::store(h + base + c, v[i]);
+                    Vec<T>::store(n + base + c, out);
+                }
+            }
+        }
+    }
+}
+
+// The rows are dealt to a fixed number of workgroups; each lane sums its
+// columns' dw and da over its rows in registers, the workgroup's row groups are
+// added in LDS, and one row of partial sums a workgroup goes to `part`
+// ([2][gridDim.x][width], dw then da), added up by norm_finish_kernel: the same
+// order in every run.
+template <typename T, int L, int N>
+__global__ __launch_bounds__(256) void norm_block_bwd_kernel(const T* __restrict__ dn, const T* __restrict__ dh,
+                                                             const T* __restrict__ x, const T* __restrict__ y,
+                                                             const float* __restrict__ a, const float* __restrict__ w,
+                                                             const float* __restrict__ rstd, T* dx, T* dy,
+                                                             float* __restrict__ part, int rows, int width)
+{
+    constexpr int VE = Vec<T>::VE, R = 256 / L;
+    __shared__ float red[2][4];
+    __shared__ __align__(16) float tot[R > 1 ? 256 * VE : 4];
+    const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+    const float inv = 1.0f / (float)width;
+    float dw[N][VE] = {}, da[N][VE] = {};
+    int slot = 0;
+    for (int row0 = blockIdx.x * R; row0 < rows; row0 += gridDim.x * R, slot ^= 1) {
+        const int row = row0 + sub;
+        const bool live = row < rows;
+        const size_t base = (size_t)(live ? row : rows - 1) * width;
+        const float r = rstd[live ? row : rows - 1];
+        float xh[N][VE], g[N][VE], u[N][VE], d[N][VE];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * L + lane) * VE;
+            if (c < width) {
+                float s[VE], t[VE];
+                Vec<T>::load(x + base + c, xh[i]);
+                Vec<T>::load(dn + base + c, t);
+                if (y) Vec<T>::load(y + base + c, u[i]);
+                if (dh) Vec<T>::load(dh + base + c, d[i]);
+                if (y) {
+                    if (a) load_f32<VE>(a + c, s);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) xh[i][e] += a ? s[e] * u[i][e] : u[i][e];
+                }
+                load_f32<VE>(w + c, s);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    xh[i][e] *= r;
+                    g[i][e] = t[e] * s[e];
+                    dot += g[i][e] * xh[i][e];
+                    if (live) dw[i][e] += t[e] * xh[i][e];
+                }
+            }
+        }
+        dot = group_sum<L>(dot, red, slot) * inv;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (i * L + lane) * VE;
+                if (c < width) {
+                    float o[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        o[e] = r * (g[i][e] - xh[i][e] * dot);
+                        if (dh) o[e] += d[i][e];
+                    }
+                    if (a) {
+                        float s[VE], q[VE];
+                        load_f32<VE>(a + c, s);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            da[i][e] += u[i][e] * o[e];
+                            q[e] = s[e] * o[e];
+                        }
+                        Vec<T>::store(dy + base + c, q);
+                    }
+                    Vec<T>::store(dx + base + c, o);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k == 1 && !a) break;
+        float* out = part + ((size_t)k * gridDim.x + blockIdx.x) * width;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * L + lane) * VE;
+            float s[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) s[e] = k ? da[i][e] : dw[i][e];
+            if (R > 1) {  // add the row groups' sums, in order
+                __syncthreads();
+                store_f32<VE>(tot + threadIdx.x * VE, s);
+                __syncthreads();
+                if (sub == 0)
+                    for (int q = 1; q < R; ++q) {
+                        float t[VE];
+                        load_f32<VE>(tot + (q * L + lane) * VE, t);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) s[e] += t[e];
+                    }
+            }
+            if (sub == 0 && c < width) store_f32<VE>(out + c, s);
+        }
+    }
+}
+
+// out[c] = sum over the nb rows of part[.][c]: 16 columns a workgroup, 16 row
+// strips, then the strips in order
+__global__ __launch_bounds__(256) void norm_finish_kernel(const float* __restrict__ part, float* __restrict__ out0,
+                                                          float* __restrict__ out1, int nb, int width)
+{
+    __shared__ float tot[16][17];
+    const int c = blockIdx.x * 16 + (threadIdx.x & 15), strip = threadIdx.x >> 4;
+    const float* p = part + (size_t)blockIdx.y * nb * width;
+    float s = 0.f;
+    if (c < width)
+        for (int r = strip; r < nb; r += 16) s += p[(size_t)r * width + c];
+    tot[strip][threadIdx.x & 15] = s;
+    __syncthreads();
+    if (strip == 0 && c < width) {
+#pragma unroll
+        for (int q = 1; q < 16; ++q) s += tot[q][threadIdx.x];
+        (blockIdx.y ? out1 : out0)[c] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gated norm of every head: a row of D values is held by L = D / VE lanes, one
+// word each.  The gate's tokens are gate_stride elements apart.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + fast_exp(-z)); }
+
+template <typename T, int L>
+__global__ __launch_bounds__(256) void norm_gate_kernel(const T* __restrict__ o, const T* __restrict__ z,
+                                                        const float* __restrict__ w, T* y, float* __restrict__ rstd,
+                                                        int rows, int heads, long long gate_stride, float eps)
+{
+    constexpr int VE = Vec<T>::VE, R = 256 / L, D = L * VE;
+    const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+    float wv[VE];
+    load_f32<VE>(w + lane * VE, wv);
+    for (int row0 = blockIdx.x * R; row0 < rows; row0 += gridDim.x * R) {
+        const int row = row0 + sub;
+        const bool live = row < rows;
+        const unsigned rr = live ? row : rows - 1;
+        const unsigned tok = rr / (unsigned)heads;
+        const size_t at = (size_t)rr * D + lane * VE;
+        float v[VE], g[VE];
+        Vec<T>::load(o + at, v);
+        Vec<T>::load(z + (size_t)tok * gate_stride + (size_t)(rr - tok * heads) * D + lane * VE, g);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) ss += v[e] * v[e];
+        ss = group_sum<L>(ss, nullptr, 0);
+        const float r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[e] = v[e] * r * wv[e] * (g[e] * sigmoid(g[e]));
+        if (live) {
+            if (rstd && lane == 0) rstd[row] = r;
+            Vec<T>::store(y + at, v);
+        }
+    }
+}
+
+template <typename T, int L>
+__global__ __launch_bounds__(256) void norm_gate_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ o,
+                                                            const T* __restrict__ z, const float* __restrict__ w,
+                                                            const float* __restrict__ rstd, T* dO, T* dz,
+                                                            float* __restrict__ part, int rows, int heads,
+                                                            long long gate_stride)
+{
+    constexpr int VE = Vec<T>::VE, R = 256 / L, D = L * VE;
+    __shared__ __align__(16) float tot[256 * VE];
+    const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+    float wv[VE], dw[VE] = {};
+    load_f32<VE>(w + lane * VE, wv);
+    for (int row0 = blockIdx.x * R; row0 < rows; row0 += gridDim.x * R) {
+        const int row = row0 + sub;
+        const bool live = row < rows;
+        const unsigned rr = live ? row : rows - 1;
+        const unsigned tok = rr / (unsigned)heads;
+        const size_t at = (size_t)rr * D + lane * VE;
+        float v[VE], g[VE], d[VE], p[VE];
+        Vec<T>::load(o + at, v);
+        Vec<T>::load(z + (size_t)tok * gate_stride + (size_t)(rr - tok * heads) * D + lane * VE, g);
+        Vec<T>::load(dy + at, d);
+        const float r = rstd[rr];
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            v[e] *= r;
+            const float s = sigmoid(g[e]), act = g[e] * s;
+            const float t = d[e] * v[e];               // dy oh
+            if (live) dw[e] += t * act;
+            p[e] = d[e] * act * wv[e];                 // g of the norm
+            dot += p[e] * v[e];
+            g[e] = t * wv[e] * (s + act * (1.0f - s)); // dz
+        }
+        dot = group_sum<L>(dot, nullptr, 0) * (1.0f / D);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) p[e] = r * (p[e] - v[e] * dot);
+        if (live) {
+            Vec<T>::store(dO + at, p);
+            Vec<T>::store(dz + at, g);
+        }
+    }
+    store_f32<VE>(tot + threadIdx.x * VE, dw);
+    __syncthreads();
+    // thread c < D adds its column over the row groups, in order
+    for (int c = threadIdx.x; c < D; c += 256) {
+        float s = 0.f;
+        for (int q = 0; q < R; ++q) s += tot[q * D + c];
+        part[(size_t)blockIdx.x * D + c] = s;
+    }
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// Lanes and words a row of norm_block: the pair that wastes the fewest words;
+// among equals the widest group when the rows are few (a whole workgroup a row
+// ends sooner) and the narrowest when they are many (no barrier).
+struct Split {
+    int L, N;
+};
+Split pick_split(int words, int rows)
+{
+    static const Split all[] = {{16, 1}, {16, 2}, {16, 3}, {16, 4}, {64, 1}, {64, 2}, {64, 3}, {64, 4},
+                                {256, 1}, {256, 2}, {256, 3}, {256, 4}, {256, 8}};
+    const bool few = rows <= 2048;
+    Split best{0, 0};
+    for (const Split& s : all) {
+        if (s.L * s.N < words) continue;
+        const int have = best.L * best.N, now = s.L * s.N;
+        if (!best.L || now < have || (now == have && (few ? s.L > best.L : s.L < best.L))) best = s;
+    }
+    return best;
+}
+
+// Call f(L, N) as compile-time constants.
+template <typename F> gdn_status with_split(Split s, F&& f)
+{
+#define GDN_SPLIT(l, n) \
+    if (s.L == l && s.N == n) return f(std::integral_constant<int, l>{}, std::integral_constant<int, n>{})
+    GDN_SPLIT(16, 1); GDN_SPLIT(16, 2); GDN_SPLIT(16, 3); GDN_SPLIT(16, 4);
+    GDN_SPLIT(64, 1); GDN_SPLIT(64, 2); GDN_SPLIT(64, 3); GDN_SPLIT(64, 4);
+    GDN_SPLIT(256, 1); GDN_SPLIT(256, 2); GDN_SPLIT(256, 3); GDN_SPLIT(256, 4); GDN_SPLIT(256, 8);
+#undef GDN_SPLIT
+    return GDN_ERR_UNSUPPORTED;
+}
+
+template <typename F> gdn_status with_lanes(int L, F&& f)
+{
+    switch (L) {
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    case 16: return f(std::integral_constant<int, 16>{});
+    case 32: return f(std::integral_constant<int, 32>{});
+    }
+    return GDN_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+gdn_status block_fwd(const gdn_norm_shape& s, const void* x, const void* y, const float* a, const float* w, void* h,
+                     void* n, float* rstd, hipStream_t st)
+{
+    const Split sp = pick_split(s.width / Vec<T>::VE, s.tokens);
+    return with_split(sp, [&](auto L, auto N) -> gdn_status {
+        const int blocks = ceil_div(s.tokens, 256 / L());
+        GDN_LAUNCH("norm_block", (norm_block_kernel<T, L(), N()>), dim3(blocks < 4096 ? blocks : 4096), dim3(256), st,
+                   (const T*)x, (const T*)y, a, w, (T*)h, (T*)n, rstd, s.tokens, s.width, s.eps);
+        return GDN_OK;
+    });
+}
+
+template <typename T>
+gdn_status block_bwd(const gdn_norm_shape& s, const void* dn, const void* dh, const void* x, const void* y,
+                     const float* a, const float* w, const float* rstd, void* dx, void* dy, float* dw, float* da,
+                     float* part, hipStream_t st)
+{
+    const Split sp = pick_split(s.width / Vec<T>::VE, s.tokens);
+    const int nb = norm_partials(s, false);
+    gdn_status r = with_split(sp, [&](auto L, auto N) -> gdn_status {
+        if (!nb) return GDN_OK;  // no rows: the sums are zeros
+        GDN_LAUNCH("norm_block_bwd", (norm_block_bwd_kernel<T, L(), N()>), dim3(nb), dim3(256), st, (const T*)dn,
+                   (const T*)dh, (const T*)x, (const T*)y, a, w, rstd, (T*)dx, (T*)dy, part, s.tokens, s.width);
+        return GDN_OK;
+    });
+    if (r != GDN_OK) return r;
+    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), a ? 2 : 1), dim3(256), st, part, dw, da,
+               nb, s.width);
+    return GDN_OK;
+}
+
+template <typename T>
+gdn_status gate_fwd(const gdn_norm_shape& s, const void* o, const void* z, const float* w, void* y, float* rstd,
+                    hipStream_t st)
+{
+    const int rows = s.tokens * s.heads;
+    return with_lanes(s.width / Vec<T>::VE, [&](auto L) -> gdn_status {
+        const int blocks = ceil_div(rows, 256 / L());
+        GDN_LAUNCH("norm_gate", (norm_gate_kernel<T, L()>), dim3(blocks < 8192 ? blocks : 8192), dim3(256), st,
+                   (const T*)o, (const T*)z, w, (T*)y, rstd, rows, s.heads, s.gate_stride, s.eps);
+        return GDN_OK;
+    });
+}
+
+template <typename T>
+gdn_status gate_bwd(const gdn_norm_shape& s, const void* dy, const void* o, const void* z, const float* w,
+                    const float* rstd, void* dO, void* dz, float* dw, float* part, hipStream_t st)
+{
+    const int rows = s.tokens * s.heads;
+    const int nb = norm_partials(s, true);
+    gdn_status r = with_lanes(s.width / Vec<T>::VE, [&](auto L) -> gdn_status {
+        if (!nb) return GDN_OK;  // no rows: the sums are zeros
+        GDN_LAUNCH("norm_gate_bwd", (norm_gate_bwd_kernel<T, L()>), dim3(nb), dim3(256), st, (const T*)dy,
+                   (const T*)o, (const T*)z, w, rstd, (T*)dO, (T*)dz, part, rows, s.heads, s.gate_stride);
+        return GDN_OK;
+    });
+    if (r != GDN_OK) return r;
+    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), 1), dim3(256), st, part, dw,
+               (float*)nullptr, nb, s.width);
+    return GDN_OK;
+}
+
+}  // namespace
+
+// Workgroups of the backward, each leaving one row of partial sums.
+int norm_partials(const gdn_norm_shape& s, bool gate)
+{
+    const int ve = s.dtype == GDN_BF16 ? 8 : 4;
+    const int L = gate ? s.width / ve : pick_split(s.width / ve, s.tokens).L;
+    const int blocks = ceil_div((long long)s.tokens * s.heads, 256 / L);
+    return blocks < 1024 ? blocks : 1024;
+}
+
+gdn_status norm_block_dispatch(const gdn_norm_shape& s, const void* x, const void* y, const float* a, const float* w,
+                               void* h, void* n, float* rstd, hipStream_t st)
+{
+    return s.dtype == GDN_BF16 ? block_fwd<bf16>(s, x, y, a, w, h, n, rstd, st)
+                               : block_fwd<float>(s, x, y, a, w, h, n, rstd, st);
+}
+
+gdn_status norm_block_bwd_dispatch(const gdn_norm_shape& s, const void* dn, const void* dh, const void* x,
+                                   const void* y, const float* a, const float* w, const float* rstd, void* dx,
+                                   void* dy, float* dw, float* da, float* part, hipStream_t st)
+{
+    return s.dtype == GDN_BF16 ? block_bwd<bf16>(s, dn, dh, x, y, a, w, rstd, dx, dy, dw, da, part, st)
+                               : block_bwd<float>(s, dn, dh, x, y, a, w, rstd, dx, dy, dw, da, part, st);
+}
+
+gdn_status norm_gate_dispatch(const gdn_norm_shape& s, const void* o, const void* z, const float* w, void* y,
+                              float* rstd, hipStream_t st)
+{
+    return s.dtype == GDN_BF16 ? gate_fwd<bf16>(s, o, z, w, y, rstd, st) : gate_fwd<float>(s, o, z, w, y, rstd, st);
+}
+
+gdn_status norm_gate_bwd_dispatch(const gdn_norm_shape& s, const void* dy, const void* o, const void* z,
+                                  const float* w, const float* rstd, void* dO, void* dz, float* dw, float* part,
+                                  hipStream_t st)
+{
+    return s.dtype == GDN_BF16 ? gate_bwd<bf16>(s, dy, o, z, w, rstd, dO, dz, dw, part, st)
+                               : gate_bwd<float>(s, dy, o, z, w, rstd, dO, dz, dw, part, st);
+}
+
+}  // namespace gdn

@@ -263,6 +263,144 @@ gdn_status gdn_replay_fold(const gdn_shape *shape, float *ckpt, void *buf, int d
 gdn_status gdn_diag_read(const gdn_shape *shape, const void *ws, unsigned int *counts,
                          void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the layer: what a stack of gated delta-rule layers and softmax
+ * attention layers needs next to the recurrence.  The conventions above hold:
+ * device pointers that the caller owns, 16-byte alignment (4-byte for the int
+ * arrays and for rstd and lse), the caller's stream, no allocation, no host
+ * synchronisation, deterministic results, statuses before any launch.
+ * Everything is computed in float32 and rounded to the stored type once; the
+ * operands of the matrix products after a softmax take the inputs' type.
+ * ---------------------------------------------------------------------------
+ *
+ * Norms before and after a block.
+ *
+ * gdn_norm_block: h = x + res_scale o y, n = h o weight / sqrt(mean(h^2) + eps)
+ * over rows of `width` values: the residual stream x takes the last block's
+ * output y, scaled per channel (y NULL: h = x; res_scale NULL: 1), and the
+ * next block gets n.  x, y, h, n [tokens, width] (dtype); res_scale, weight
+ * [width], rstd [tokens] float32 (1 / sqrt(...), for the backward).  h and
+ * rstd may be NULL (not written); h may be x or y themselves.  n is computed
+ * from the unrounded h.  width: a multiple of 8 (bf16, at most 16384) or of 4
+ * (float32, at most 8192).
+ *
+ * gdn_norm_block_backward: with dn, and dh the gradient that arrives at h from
+ * behind (NULL = zero), dx = dL/dx, dy = res_scale o dx, dweight, dres_scale.
+ * It reads x and y, not h.  With y but no res_scale dL/dy is dx itself; dy
+ * and dres_scale are written only with res_scale.
+ *
+ * gdn_norm_gate: y = o weight / sqrt(mean(o^2) + eps) * gate / (1 + exp(-gate))
+ * per head row of `width` = Dv values in {16, 32, 64, 128}: the layer's output
+ * before its projection.  o, y [tokens, heads, width] dense, gate the same with
+ * gate_stride elements between tokens (0: dense; a slice of a wider projection
+ * otherwise), weight [width], rstd [tokens, heads] float32 (may be NULL).
+ * gdn_norm_gate_backward: do, dgate (both dense), dweight.
+ *
+ * The backward's workspace holds gdn_norm_workspace_bytes(shape, gate) bytes
+ * (gate: 0 for the block norm, 1 for the gated norm; 0 bytes: invalid shape).
+ * tokens * heads <= 2^29.  With tokens = 0 the backward writes zero weights'
+ * gradients.
+ */
+typedef struct {
+    int tokens, heads, width; /* heads = 1 for the block norm */
+    int dtype;                /* gdn_dtype */
+    float eps;                /* in (0, 1] */
+    long long gate_stride;    /* gated norm: elements between the gate's tokens, 0 = heads * width */
+} gdn_norm_shape;
+
+size_t gdn_norm_workspace_bytes(const gdn_norm_shape *shape, int gate);
+gdn_status gdn_norm_block(const gdn_norm_shape *shape, const void *x, const void *y,
+                          const float *res_scale, const float *weight, void *h, void *n,
+                          float *rstd, void *stream);
+gdn_status gdn_norm_block_backward(const gdn_norm_shape *shape, const void *dn, const void *dh,
+                                   const void *x, const void *y, const float *res_scale,
+                                   const float *weight, const float *rstd, void *dx, void *dy,
+                                   float *dweight, float *dres_scale, void *ws, size_t ws_bytes,
+                                   void *stream);
+gdn_status gdn_norm_gate(const gdn_norm_shape *shape, const void *o, const void *gate,
+                         const float *weight, void *y, float *rstd, void *stream);
+gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, const void *o,
+                                  const void *gate, const float *weight, const float *rstd,
+                                  void *dO, void *dgate, float *dweight, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/*
+ * Causal softmax attention with grouped heads over packed sequences.
+ *
+ * Query head h uses key head h / (Hq / Hkv).  The T token rows of q, k, v, o
+ * belong to B sequences: sequence b has rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+ * (device memory, B + 1 entries, non-decreasing, from 0 to at most T; entries
+ * outside are clamped, never followed out of the buffers).  Rows of no
+ * sequence are not used and not written: outputs there stay as they were.
+ *   q [T, Hq, D], k, v [T, Hkv, D] (dtype): dense within a token, with
+ *   q_stride, k_stride, v_stride elements between tokens (0 = dense; slices of
+ *   one projection's output otherwise); o, dO, dq [T, Hq, D], dk, dv
+ *   [T, Hkv, D] dense; lse [T, Hq] float32.
+ * scale 0 means D^-0.5.  D in {64, 128}; Hq a multiple of Hkv, at most 1024;
+ * T * Hq < 2^27.
+ *
+ * gdn_attn_forward: token i of a sequence attends to its tokens 0 .. i.
+ * lse = log sum exp(scale q.k) over them (may be NULL; the backward needs it).
+ * gdn_attn_backward: dq, dk, dv from dO; ws holds
+ * gdn_attn_workspace_bytes(shape, GDN_ATTN_BACKWARD) bytes.  A key head's
+ * gradient is the sum over its query heads.
+ *
+ * The paged cache: k_cache, v_cache [num_pages, page_size, Hkv, D] (dtype),
+ * page_size a power of two from 16 to 1024; position p of sequence b lies in
+ * slot p % page_size of page page_table[b][p / page_size] (device memory,
+ * [B, max_pages]; -1, or any value outside [0, num_pages), means that there is
+ * no such page).  kv_len[b] (device memory) counts the sequence's positions
+ * with its new tokens, so that the new token i of n stands at position
+ * kv_len[b] - n + i.
+ *
+ * gdn_attn_append writes every new token's k and v to its position, k rotated:
+ * for i < rot_dim / 2, with c, s = cos, sin[position][i],
+ *   x'[i] = x[i] c - x[i + rot_dim/2] s,  x'[i + rot_dim/2] = x[i + rot_dim/2] c + x[i] s,
+ * the rest of a head as it is; q rotated the same way into q_out [T, Hq, D]
+ * (q and q_out both NULL: not done; q_out may be q where q is dense).
+ * cos, sin [max_pos, rot_dim / 2] float32, rot_dim a multiple of 16 up to D (0:
+ * no rotation, cos, sin not read).  A token whose position is negative, not
+ * below max_pos or behind the table is left out, q_out included; one whose page does not exist writes
+ * no cache row.  Positions that two sequences of one call both write (pages
+ * they share) end with either's values.
+ *
+ * gdn_attn_paged: new token i attends to positions 0 .. kv_len[b] - n + i of
+ * its sequence, i.e. the cache after gdn_attn_append; q already rotated.
+ * Positions without a page are absent; a token that sees nothing gets zeros.
+ * One new token a sequence is decoding.  ws holds
+ * gdn_attn_workspace_bytes(shape, GDN_ATTN_PAGED) bytes.  k_stride and
+ * v_stride are not used.  Cache slots that no visible position names are not
+ * used, whatever they hold; a non-finite key or value of a token can reach
+ * outputs of its own sequence only.
+ */
+typedef struct {
+    int B, T, Hq, Hkv, D;
+    int dtype;   /* gdn_dtype */
+    float scale; /* 0 means D^-0.5 */
+    long long q_stride, k_stride, v_stride; /* elements between tokens, 0 = dense */
+    int num_pages, page_size, max_pages;    /* paged cache */
+    int rot_dim, max_pos;                   /* gdn_attn_append */
+} gdn_attn_shape;
+
+enum { GDN_ATTN_PAGED = 0, GDN_ATTN_BACKWARD = 1 };
+
+size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int call);
+gdn_status gdn_attn_forward(const gdn_attn_shape *shape, const void *q, const void *k,
+                            const void *v, const int *cu_seqlens, void *o, float *lse,
+                            void *stream);
+gdn_status gdn_attn_backward(const gdn_attn_shape *shape, const void *q, const void *k,
+                             const void *v, const int *cu_seqlens, const void *o,
+                             const float *lse, const void *dO, void *dq, void *dk, void *dv,
+                             void *ws, size_t ws_bytes, void *stream);
+gdn_status gdn_attn_append(const gdn_attn_shape *shape, const void *q, const void *k,
+                           const void *v, const float *cos, const float *sin,
+                           const int *cu_seqlens, const int *kv_len, const int *page_table,
+                           void *k_cache, void *v_cache, void *q_out, void *stream);
+gdn_status gdn_attn_paged(const gdn_attn_shape *shape, const void *q, const void *k_cache,
+                          const void *v_cache, const int *page_table, const int *cu_seqlens,
+                          const int *kv_len, void *o, void *ws, size_t ws_bytes, void *stream);
+
 /* gdn_status_string -- static, human-readable name of a status code. */
 const char *gdn_status_string(gdn_status status);
 
