@@ -23,7 +23,6 @@ are zeros in outputs that are allocated here.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -78,18 +77,18 @@ def _p(t):
 def _take(t, name, shape, dtype, device, *, stride=False):
     """Check a tensor: its shape, type and device, dense (or, with stride, dense
     within its first index).  Returns the elements between first indices."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}, a GPU, and is on {t.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
     if not stride or not t[0].is_contiguous():
         raise ValueError(f"{name} must be contiguous" + (" within a token" if stride else ""))
     # one token has no stride of its own
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return t.stride(0) if shape[0] > 1 else 0
 
 
 def _opt(t, name, shape, dtype, device):
@@ -97,16 +96,14 @@ def _opt(t, name, shape, dtype, device):
         _take(t, name, shape, dtype, device)
 
 
-def _on(device):
-    """The device's current stream, with the device current while a call is made."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _run(fn, name, device, *args):
-    with _on(device):
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    """Call on the device's current stream, with that device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
     if rc != 0:
         raise GdnError(rc, name)
 
@@ -123,7 +120,7 @@ def _workspace(query, shape, arg, ws, device, name):
         raise GdnError(2, name)
     if ws is None:
         return torch.empty(n, dtype=torch.uint8, device=device), n
-    if ws.device != device or not ws.is_contiguous():
+    if ws.get_device() != device.index or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous and on {device}")
     return ws, ws.numel() * ws.element_size()
 
@@ -132,7 +129,7 @@ def _workspace(query, shape, arg, ws, device, name):
 # norms
 # ---------------------------------------------------------------------------
 def _rows(x):
-    return x.shape[:-1].numel() if x.dim() > 1 else 1
+    return x.shape[:-1].numel()
 
 
 def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):

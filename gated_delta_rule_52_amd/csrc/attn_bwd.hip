@@ -27,6 +27,8 @@ struct BwdArgs {
     uint32_t q_bytes, k_bytes, v_bytes, o_bytes;  // bytes between tokens
     int B, T, Hq, Hkv, G;
     float scale;
+    int kparts, qparts;  // pieces that a key block's queries, a query block's keys are cut into
+    float *part_k, *part_q;  // [2][kparts][T * Hkv][D] (dk, dv), [qparts][T * Hq][D]
 };
 
 // delta and the log-sums in base 2, by query head.  A row of D values is held by
@@ -67,47 +69,63 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(BwdArgs a)
     }
 }
 
-// dk, dv of 128 keys: four waves of 32 keys, whose keys and values stay in
-// registers; tiles of QT tokens of one query head after the other go through
-// two LDS buffers.
+// Four accumulator rows of one column times f: to the gradient, or to a piece's
+// partial sums where the work is cut up.
+template <typename T>
+__device__ __forceinline__ void put4(T* out, float* part, size_t at, const f32x16& v, int i, float f)
+{
+    if (part)
+        store4<float>(part + at, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else
+        store4<T>(out + at, v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+}
+
+// dk, dv of 128 keys: four waves of 32 keys.  The keys stay in registers, the
+// values in LDS (with both in registers a wave would need more than the 256 that
+// two waves a SIMD have); tiles of 32 tokens of one query head after the other
+// go through two LDS buffers.
 template <typename T, int D>
-__global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(BwdArgs a)
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(BwdArgs a)
 {
     constexpr int KK = D / 16, DT = D / 32;
-    constexpr int QT = sizeof(T) == 2 ? 64 : 32, RW = QT / 4;
+    constexpr int QT = 32, RW = QT / 4;
     constexpr int TAB = QT * Rows<T, D>::BYTES;
+    __shared__ __align__(1024) char vtab[128 * Rows<T, D>::BYTES];
     __shared__ __align__(1024) char lds[2][2][TAB];
     __shared__ __align__(256) float ld[2][2][64];  // lse2, delta of a tile (64 lanes' words; QT are read)
 
     const int hk = blockIdx.x % a.Hkv;
+    const int rest = blockIdx.x / a.Hkv, part = rest % a.kparts;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, 1, 128, blockIdx.x / a.Hkv, s)) return;
+    if (!find_block(a.cu, a.B, a.T, 1, 128, rest / a.kparts, s)) return;
     const int key0 = s.blk * 128;  // the first keys have the most queries: they come first
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
     const int wkey = key0 + 32 * w;
     const int key = wkey + (l & 31);
     const int kc = key < s.n ? key : s.n - 1;
 
-    Frag<T> kf[KK], vf[KK];
+    Frag<T> kf[KK];
     {
         const T* kp = (const T*)((const char*)a.k + (size_t)(s.start + kc) * a.k_bytes) + (size_t)hk * D;
-        const T* vp = (const T*)((const char*)a.v + (size_t)(s.start + kc) * a.v_bytes) + (size_t)hk * D;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            kf[kk] = load_frag<T>(kp + 16 * kk + 8 * h);
-            vf[kk] = load_frag<T>(vp + 16 * kk + 8 * h);
-        }
+        for (int kk = 0; kk < KK; ++kk) kf[kk] = load_frag<T>(kp + 16 * kk + 8 * h);
+        const int at = wkey < s.n ? wkey : s.n - 1;
+        Rows<T, D>::template fetch<32>(vtab, 32 * w,
+                                       (const char*)a.v + (size_t)(s.start + at) * a.v_bytes + (size_t)hk * D * sizeof(T),
+                                       a.v_bytes, s.n - 1 - at);
     }
     f32x16 dk[DT], dv[DT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) dk[dt] = dv[dt] = zero16();
 
     const float sl2 = a.scale * kLog2e;
-    const int tq0 = key0 / QT, ntq = (s.n + QT - 1) / QT - tq0;  // query tiles at or after the block
+    // tiles: the query tiles at or after the block, of one head after the other; this piece's are i0 .. i1 - 1
+    const int tq0 = key0 / QT, ntq = (s.n + QT - 1) / QT - tq0;
     const int total = ntq * a.G;
-    auto fetch = [&](int it, int buf) {
-        const int g = it / ntq, q0 = (tq0 + it - g * ntq) * QT;
-        const int hq = hk * a.G + g;
+    const int i0 = (int)((long long)total * part / a.kparts), i1 = (int)((long long)total * (part + 1) / a.kparts);
+    int fg = i0 / ntq, fq = i0 - fg * ntq;  // head and query tile of the next fetch
+    auto fetch = [&](int buf) {
+        const int q0 = (tq0 + fq) * QT, hq = hk * a.G + fg;
         const int at = q0 + w * RW < s.n ? q0 + w * RW : s.n - 1;
         const int last = s.n - 1 - at;
         const size_t tok = (size_t)(s.start + at);
@@ -118,70 +136,72 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(BwdArgs a)
         const int t = q0 + l < s.n ? q0 + l : s.n - 1;
         if (w == 0) dma4(a.lse2 + (size_t)hq * a.T + s.start + t, ld[buf][0]);
         if (w == 1) dma4(a.delta + (size_t)hq * a.T + s.start + t, ld[buf][1]);
+        if (++fq == ntq) {
+            fq = 0;
+            ++fg;
+        }
     };
-    fetch(0, 0);
-    for (int it = 0; it < total; ++it) {
-        const int buf = it & 1;
+    int cq = fq;  // query tile of the one being multiplied
+    if (i0 < i1) fetch(0);
+    for (int it = i0; it < i1; ++it) {
+        const int buf = (it - i0) & 1;
         wait_vm<0>();
         __syncthreads();
-        if (it + 1 < total) fetch(it + 1, buf ^ 1);
-        const int q0 = (tq0 + it % ntq) * QT;
+        if (it + 1 < i1) fetch(buf ^ 1);
+        const int qs = (tq0 + cq) * QT;
+        if (++cq == ntq) cq = 0;
+        if (qs + 31 < wkey) continue;  // every query stands before the wave's keys
+        const void* qt = lds[buf][0];
+        const void* ot = lds[buf][1];
+        f32x16 sc = zero16(), dp = zero16();
 #pragma unroll
-        for (int sub = 0; sub < QT / 32; ++sub) {
-            const int qs = q0 + 32 * sub;
-            if (qs + 31 < wkey || qs >= s.n) continue;  // every query stands before the wave's keys
-            const void* qt = lds[buf][0];
-            const void* dt_ = lds[buf][1];
-            f32x16 sc = zero16(), dp = zero16();
+        for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(qt, 0, kk), kf[kk], sc);
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(qt, 32 * sub, kk), kf[kk], sc);
+        for (int kk = 0; kk < KK; ++kk)
+            dp = mma32(Rows<T, D>::along(ot, 0, kk), Rows<T, D>::along(vtab, 32 * w, kk), dp);
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) dp = mma32(Rows<T, D>::along(dt_, 32 * sub, kk), vf[kk], dp);
-            const bool edge = qs < wkey + 31 || qs + 32 > s.n;
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(&ld[buf][0][8 * i + 4 * h]);
+            const f32x4 de = *reinterpret_cast<const f32x4*>(&ld[buf][1][8 * i + 4 * h]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 ls = *reinterpret_cast<const f32x4*>(&ld[buf][0][32 * sub + 8 * i + 4 * h]);
-                const f32x4 de = *reinterpret_cast<const f32x4*>(&ld[buf][1][32 * sub + 8 * i + 4 * h]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 4 * i + e;
-                    sc[r] = exp2_hw(sc[r] * sl2 - ls[e]);
-                    dp[r] = sc[r] * (dp[r] - de[e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int r = 4 * i + e;
+                sc[r] = exp2_hw(sc[r] * sl2 - ls[e]);
+                dp[r] = sc[r] * (dp[r] - de[e]);
             }
-            if (edge) {
+        }
+        if (qs < wkey + 31 || qs + 32 > s.n) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int q = qs + 8 * (r >> 2) + 4 * h + (r & 3);
-                    const bool in = key <= q && q < s.n;
-                    sc[r] = in ? sc[r] : 0.f;
-                    dp[r] = in ? dp[r] : 0.f;
-                }
+            for (int r = 0; r < 16; ++r) {
+                const int q = qs + 8 * (r >> 2) + 4 * h + (r & 3);
+                const bool in = key <= q && q < s.n;
+                sc[r] = in ? sc[r] : 0.f;
+                dp[r] = in ? dp[r] : 0.f;
             }
+        }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                // both operands are rounded to the inputs' type, as in the forward
-                const Frag<T> p = acc_frag<T>(sc, b), ds = acc_frag<T>(dp, b);
+        for (int b = 0; b < 2; ++b) {
+            // both operands are rounded to the inputs' type, as in the forward
+            const Frag<T> p = acc_frag<T>(sc, b), ds = acc_frag<T>(dp, b);
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    dv[dt] = mma32(Rows<T, D>::down(dt_, 32 * sub + 16 * b, 32 * dt), p, dv[dt]);
-                    dk[dt] = mma32(Rows<T, D>::down(qt, 32 * sub + 16 * b, 32 * dt), ds, dk[dt]);
-                }
+            for (int dt = 0; dt < DT; ++dt) {
+                dv[dt] = mma32(Rows<T, D>::down(ot, 16 * b, 32 * dt), p, dv[dt]);
+                dk[dt] = mma32(Rows<T, D>::down(qt, 16 * b, 32 * dt), ds, dk[dt]);
             }
         }
     }
+    wait_vm<0>();  // a piece without tiles still has its values under way
     if (key < s.n) {
-        const size_t at = ((size_t)(s.start + key) * a.Hkv + hk) * D;
-        T* kp = (T*)a.dk + at;
-        T* vp = (T*)a.dv + at;
+        const size_t at = ((size_t)(s.start + key) * a.Hkv + hk) * D, all = (size_t)a.T * a.Hkv * D;
+        float* pk = a.kparts > 1 ? a.part_k + part * all : nullptr;
+        float* pv = a.kparts > 1 ? a.part_k + (a.kparts + part) * all : nullptr;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = 32 * dt + 8 * i + 4 * h;
-                store4<T>(kp + c, dk[dt][4 * i] * a.scale, dk[dt][4 * i + 1] * a.scale, dk[dt][4 * i + 2] * a.scale,
-                          dk[dt][4 * i + 3] * a.scale);
-                store4<T>(vp + c, dv[dt][4 * i], dv[dt][4 * i + 1], dv[dt][4 * i + 2], dv[dt][4 * i + 3]);
+                put4<T>((T*)a.dk, pk, at + c, dk[dt], i, a.scale);
+                put4<T>((T*)a.dv, pv, at + c, dv[dt], i, 1.f);
             }
     }
 }
@@ -197,8 +217,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
     __shared__ __align__(1024) char lds[2][2][TAB];
 
     const int hk = blockIdx.x % a.Hkv;
+    const int rest = blockIdx.x / a.Hkv, part = rest % a.qparts;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, a.G, 128, blockIdx.x / a.Hkv, s)) return;
+    if (!find_block(a.cu, a.B, a.T, a.G, 128, rest / a.qparts, s)) return;
     const int R = s.n * a.G, nblk = (R + 127) / 128;
     const int row0 = (nblk - 1 - s.blk) * 128;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
@@ -234,12 +255,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
         Rows<T, D>::template fetch<RW>(lds[buf][0], w * RW, kb + (size_t)kat * a.k_bytes, a.k_bytes, s.n - 1 - kat);
         Rows<T, D>::template fetch<RW>(lds[buf][1], w * RW, vb + (size_t)kat * a.v_bytes, a.v_bytes, s.n - 1 - kat);
     };
-    fetch(0, 0);
-    for (int t = 0; t < tiles; ++t) {
-        const int buf = t & 1;
+    const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
+    if (t0 < t1) fetch(t0, 0);
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
         wait_vm<0>();
         __syncthreads();
-        if (t + 1 < tiles) fetch(t + 1, buf ^ 1);
+        if (t + 1 < t1) fetch(t + 1, buf ^ 1);
 #pragma unroll
         for (int sub = 0; sub < KT / 32; ++sub) {
             const int key0 = t * KT + 32 * sub;
@@ -266,14 +288,38 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
         }
     }
     if (row < R) {
-        T* p = (T*)a.dq + (at * a.Hq + hq) * D;
+        const size_t out = (at * a.Hq + hq) * D;
+        float* pq = a.qparts > 1 ? a.part_q + part * ((size_t)a.T * a.Hq * D) : nullptr;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store4<T>(p + 32 * dt + 8 * i + 4 * h, dq[dt][4 * i] * a.scale, dq[dt][4 * i + 1] * a.scale,
-                          dq[dt][4 * i + 2] * a.scale, dq[dt][4 * i + 3] * a.scale);
+            for (int i = 0; i < 4; ++i) put4<T>((T*)a.dq, pq, out + 32 * dt + 8 * i + 4 * h, dq[dt], i, a.scale);
     }
+}
+
+// out = f * sum of the np pieces' partial sums, in their order, for the rows of
+// sequences; four values a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ cu, int B, const float* __restrict__ part,
+                                                       T* out, float f, int np, int per_token, size_t n)
+{
+    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const int tok = (int)(i / per_token);
+    if (tok < cu[0] || tok >= cu[B]) return;
+    f32x4 s = *reinterpret_cast<const f32x4*>(part + i);
+#pragma unroll 4
+    for (int p = 1; p < np; ++p) s += *reinterpret_cast<const f32x4*>(part + p * n + i);
+    store4<T>(out + i, s[0] * f, s[1] * f, s[2] * f, s[3] * f);
+}
+
+template <typename T>
+gdn_status launch_sum(const BwdArgs& a, const float* part, void* out, float f, int np, int heads, int D, hipStream_t st)
+{
+    const size_t n = (size_t)a.T * heads * D;
+    GDN_LAUNCH("attn_sum", attn_sum_kernel<T>, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), st, a.cu, a.B, part,
+               (T*)out, f, np, heads * D, n);
+    return GDN_OK;
 }
 
 template <typename T, int D>
@@ -282,18 +328,56 @@ gdn_status launch(const BwdArgs& a, hipStream_t st)
     constexpr int RPB = 256 / (D * (int)sizeof(T) / 16);
     const size_t rows = (size_t)a.T * a.Hq;
     GDN_LAUNCH("attn_delta", (attn_delta_kernel<T, D>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
-    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv;
+    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv * a.kparts;
     GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
-    const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv;
+    const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts;
     GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3((unsigned)qblocks), dim3(256), st, a);
-    return GDN_OK;
+    gdn_status r = GDN_OK;
+    if (a.kparts > 1) {
+        r = launch_sum<T>(a, a.part_k, a.dk, a.scale, a.kparts, a.Hkv, D, st);
+        if (r == GDN_OK)
+            r = launch_sum<T>(a, a.part_k + (size_t)a.kparts * a.T * a.Hkv * D, a.dv, 1.f, a.kparts, a.Hkv, D, st);
+    }
+    if (r == GDN_OK && a.qparts > 1) r = launch_sum<T>(a, a.part_q, a.dq, a.scale, a.qparts, a.Hq, D, st);
+    return r;
 }
 
-size_t half_ws(const gdn_attn_shape& s) { return ((size_t)s.T * s.Hq * sizeof(float) + 255) & ~(size_t)255; }
+// How the work of a block is cut up: until there are `want` workgroups, but
+// pieces of two tiles at least (on average: `tiles` are those of a middle block).
+int parts_for(long long blocks, long long want, long long tiles, int most)
+{
+    long long p = want / blocks;
+    p = p > tiles / 2 ? tiles / 2 : p;
+    return p < 1 ? 1 : p > most ? most : (int)p;
+}
+
+struct BwdPlan {
+    int kparts, qparts;
+    size_t o_delta, o_k, o_q, bytes;
+};
+
+BwdPlan bwd_plan(const gdn_attn_shape& s)
+{
+    BwdPlan p;
+    const long long G = s.Hq / s.Hkv, len = s.T / s.B;
+    const long long kb = ((long long)s.T + 127) / 128, qb = ((long long)s.T * G + 127) / 128;
+    const int kt = s.dtype == GDN_BF16 ? 64 : 32;
+    // a key block's work falls with its place in the sequence, so the first
+    // blocks decide the end unless there are several workgroups a compute unit
+    p.kparts = parts_for((kb > s.B ? kb : s.B) * s.Hkv, 1024, G * (len / 2 + 32) / 32, 16);
+    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / 2 + kt) / kt, 16);
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    const size_t f = sizeof(float), rows = (size_t)s.T * s.Hq;
+    p.o_delta = up(rows * f);
+    p.o_k = p.o_delta + up(rows * f);
+    p.o_q = p.o_k + (p.kparts > 1 ? up(2 * p.kparts * (size_t)s.T * s.Hkv * s.D * f) : 0);
+    p.bytes = p.o_q + (p.qparts > 1 ? up(p.qparts * rows * s.D * f) : 0);
+    return p;
+}
 
 }  // namespace
 
-size_t attn_backward_ws(const gdn_attn_shape& s) { return 2 * half_ws(s); }
+size_t attn_backward_ws(const gdn_attn_shape& s) { return bwd_plan(s).bytes; }
 
 gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const void* k, const void* v, const int* cu,
                                   const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
@@ -304,7 +388,12 @@ gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const 
     a.q = q; a.k = k; a.v = v; a.o = o; a.dO = dO; a.lse = lse; a.cu = cu;
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.lse2 = (float*)ws;
-    a.delta = (float*)((char*)ws + half_ws(s));
+    const BwdPlan p = bwd_plan(s);
+    a.delta = (float*)((char*)ws + p.o_delta);
+    a.part_k = (float*)((char*)ws + p.o_k);
+    a.part_q = (float*)((char*)ws + p.o_q);
+    a.kparts = p.kparts;
+    a.qparts = p.qparts;
     a.q_stride = s.q_stride;
     a.q_bytes = (uint32_t)(s.q_stride * e);
     a.k_bytes = (uint32_t)(s.k_stride * e);

@@ -23,7 +23,7 @@ struct FwdArgs {
     uint32_t k_bytes, v_bytes;    // bytes between tokens of k and v (slots of the cache)
     int B, T, Hq, Hkv, G;
     int num_pages, page_shift, max_pages;
-    int splits;
+    int splits, piece;            // the key axis in pieces of `piece` keys, at most `splits` of them
     float scale;
     float *part_o, *part_l;
 };
@@ -48,36 +48,28 @@ struct Queries {
         l = 0.f;
     }
 
-    // NK * 32 keys of the tables from row r0; key0 is the position of the first.
+    // 32 keys of the tables from row r0; key0 is the position of the first.
     // MASK: some key may lie behind some row's limit, or `gone` (a bit for each
     // run of CH keys) says that it is absent.
-    template <int NK, bool MASK, int CH>
+    template <bool MASK, int CH>
     __device__ __forceinline__ void step(const void* ktab, const void* vtab, int r0, int key0, unsigned gone, float sl2)
     {
         const int h = lane_id() >> 5;
-        f32x16 s[NK];
+        f32x16 s = zero16();
 #pragma unroll
-        for (int t = 0; t < NK; ++t) s[t] = zero16();
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int t = 0; t < NK; ++t) s[t] = mma32(Rows<T, D>::along(ktab, r0 + 32 * t, kk), q[kk], s[t]);
+        for (int kk = 0; kk < KK; ++kk) s = mma32(Rows<T, D>::along(ktab, r0, kk), q[kk], s);
         if (MASK) {
 #pragma unroll
-            for (int t = 0; t < NK; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-                    // CH >= 8: the four rows of a register group lie in one run
-                    const bool out = key0 + key >= limit || ((gone >> ((32 * t + 8 * (r >> 2)) / CH)) & 1);
-                    s[t][r] = out ? -INFINITY : s[t][r];
-                }
+            for (int r = 0; r < 16; ++r) {
+                const int key = 8 * (r >> 2) + 4 * h + (r & 3);
+                // CH >= 8: the four rows of a register group lie in one run
+                const bool out = key0 + key >= limit || ((gone >> (8 * (r >> 2) / CH)) & 1);
+                s[r] = out ? -INFINITY : s[r];
+            }
         }
-        float mx = s[0][0];
+        float mx = s[0];
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
         mx = half_max(mx);
         // The maximum is moved, and what was summed rescaled, only when it grew
         // by more than 2^8: until then the exponentials stay below 256, which
@@ -95,29 +87,35 @@ struct Queries {
         const float off = m == -INFINITY ? 0.f : m * sl2;
         float sum = 0.f;
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[t][r] = exp2_hw(s[t][r] * sl2 - off);
-                sum += s[t][r];
-            }
+        for (int r = 0; r < 16; ++r) {
+            s[r] = exp2_hw(s[r] * sl2 - off);
+            sum += s[r];
+        }
         l += sum;
         // The operand of the second product is rounded to the inputs' type: half
         // a step of bf16 a key, against the half step of the stored output; the
         // sum above takes the unrounded values.
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
+        for (int b = 0; b < 2; ++b) {
+            const Frag<T> p = acc_frag<T>(s, b);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const Frag<T> p = acc_frag<T>(s[t], b);
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    o[dt] = mma32(Rows<T, D>::down(vtab, r0 + 32 * t + 16 * b, 32 * dt), p, o[dt]);
-            }
+            for (int dt = 0; dt < DT; ++dt) o[dt] = mma32(Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt), p, o[dt]);
+        }
     }
 };
 
-// The keys of one (sequence, key head): where run `c` of CH keys lies.
+__device__ __forceinline__ int pieces_of(const FwdArgs& a, int len)
+{
+    return a.splits > 1 && len > a.piece ? (len + a.piece - 1) / a.piece : 1;
+}
+
+__device__ __forceinline__ int cached_len(const FwdArgs& a, int n)
+{
+    const long long cap = (long long)a.max_pages << a.page_shift;
+    return n < 0 ? 0 : n > cap ? (int)cap : n;
+}
+
+// The keys of one (sequence, key head): where a run of CH keys lies.
 template <typename T, int D, bool PAGED, int CH>
 struct Keys {
     const char *k, *v;
@@ -129,9 +127,8 @@ struct Keys {
     {
         if (PAGED) {
             int n = uniform(a.kv_len[s.b]);
-            const long long cap = (long long)a.max_pages << a.page_shift;
+            len = cached_len(a, n);
             n = n < 0 ? 0 : n > (1 << 30) ? 1 << 30 : n;
-            len = n > cap ? (int)cap : n;
             first = n - s.n;
             pages = a.table + (size_t)s.b * a.max_pages;
             k = (const char*)a.k + (size_t)hk * D * sizeof(T);
@@ -150,14 +147,16 @@ struct Keys {
         const int n = first + tok + 1;
         return n < 0 ? 0 : n < len ? n : len;
     }
-    // page of the run that starts at key `key` (of the last key where it starts behind the end), -1: none.
-    // A run never crosses a page: page sizes are powers of two, 16 at least, and runs are 8 or 16 keys from a multiple.
+    // Page of the run that starts at key `key` (of the last key where it starts behind the end), -1: none.  A run
+    // never crosses a page: page sizes are powers of two from 16 on, and runs start at multiples of their 8 or 16 keys.
     __device__ __forceinline__ int page(const FwdArgs& a, int key) const
     {
-        const int at = (key < len ? key : len - 1) >> a.page_shift;
-        const int p = pages[at];
+        if (!PAGED || len == 0) return 0;
+        const int p = pages[(key < len ? key : len - 1) >> a.page_shift];
         return p >= 0 && p < a.num_pages ? p : -1;
     }
+    // pieces of the key axis: one where no split is made
+    __device__ __forceinline__ int pieces(const FwdArgs& a) const { return pieces_of(a, len); }
     // the run from `key` into rows r0 .. r0 + CH - 1 of both tables
     __device__ __forceinline__ void fetch(const FwdArgs& a, int key, int page, void* ktab, void* vtab, int r0) const
     {
@@ -177,13 +176,17 @@ struct Keys {
 // ---------------------------------------------------------------------------
 // 128-row blocks: four waves of 32 rows; the workgroup's tiles of KT keys go
 // through two LDS buffers, each wave fetching a quarter of a tile while the
-// tile before it is multiplied.
+// tile before it is multiplied.  The waves take a tile 32 keys at a time, which
+// keeps the scores, the outputs and the queries of a row within the 256
+// registers that two waves a SIMD have: one wave's exponentials then run under
+// the other's matrix instructions.
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool PAGED>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a)
+__global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void attn_fwd_kernel(FwdArgs a)
 {
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32, CH = KT / 4, NK = KT / 32;
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32, CH = KT / 4;
     constexpr int TAB = KT * Rows<T, D>::BYTES;
+    constexpr int WIN = 16;  // tiles whose pages a wave holds: lane 4 i + c has run c of the i-th
     __shared__ __align__(1024) char lds[2][2][TAB];
 
     const int hk = blockIdx.x % a.Hkv;
@@ -193,10 +196,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a)
     const int R = s.n * a.G, nblk = (R + 127) / 128;
     const int row0 = (nblk - 1 - s.blk) * 128;  // the longest rows first
     const Keys<T, D, PAGED, CH> keys(a, s, hk);
+    const int pieces = keys.pieces(a);
+    if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
-    const int wrow = row0 + 32 * w;
-    const int row = wrow + (l & 31);
+    const int row = row0 + 32 * w + (l & 31);
     const int rr = row < R ? row : R - 1;
     const int tok = rr / a.G, hq = hk * a.G + (rr - tok * a.G);
     Queries<T, D> qs;
@@ -206,48 +210,50 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a)
     const int wmin = __builtin_amdgcn_readlane(qs.limit, 0), wmax = __builtin_amdgcn_readlane(qs.limit, 31);
     const int end = row0 + 127 < R ? row0 + 127 : R - 1;
     const int tiles = (keys.seen(end / a.G) + KT - 1) / KT;
-    const int t0 = (int)((long long)tiles * split / a.splits), t1 = (int)((long long)tiles * (split + 1) / a.splits);
+    const int t0 = pieces > 1 ? split * (a.piece / KT) : 0;
+    int t1 = pieces > 1 ? t0 + a.piece / KT : tiles;
+    t1 = t1 < tiles ? t1 : tiles;
     const float sl2 = a.scale * kLog2e;
 
-    int page[4] = {0, 0, 0, 0};
-    auto lookup = [&](int t) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) page[c] = PAGED ? keys.page(a, t * KT + c * CH) : 0;
-    };
-    auto absent = [&]() -> unsigned {
-        unsigned m = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) m |= page[c] < 0 ? 1u << c : 0;
-        return m;
-    };
-    auto fetch = [&](int t, int buf) {
-        const int p = w == 0 ? page[0] : w == 1 ? page[1] : w == 2 ? page[2] : page[3];
+    int ids = 0, ids_next = 0;  // pages of the window's tiles, and of the next window's
+    if (PAGED) {
+        ids = keys.page(a, (t0 + (l >> 2)) * KT + (l & 3) * CH);
+        ids_next = keys.page(a, (t0 + WIN + (l >> 2)) * KT + (l & 3) * CH);
+    }
+    auto fetch = [&](int t, int buf) -> unsigned {  // returns the runs that are absent
+        unsigned gone = 0;
+        int p = 0;
+        if (PAGED) {
+            const int i = (t - t0) % WIN;
+            if (i == 0 && t > t0) {
+                ids = ids_next;
+                ids_next = keys.page(a, (t + WIN + (l >> 2)) * KT + (l & 3) * CH);
+            }
+            gone = (unsigned)(__ballot(ids < 0) >> (4 * i)) & 15u;
+            p = __builtin_amdgcn_readlane(ids, 4 * i + w);
+        }
         keys.fetch(a, t * KT + w * CH, p, lds[buf][0], lds[buf][1], w * CH);
+        return gone;
     };
 
     unsigned gone = 0, gone_next = 0;
-    if (t0 < t1) {
-        lookup(t0);
-        gone_next = absent();
-        fetch(t0, 0);
-        if (t0 + 1 < t1) lookup(t0 + 1);
-    }
+    if (t0 < t1) gone_next = fetch(t0, 0);
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1;
         gone = gone_next;
         wait_vm<0>();
         __syncthreads();
-        if (t + 1 < t1) {
-            gone_next = absent();
-            fetch(t + 1, buf ^ 1);
-            if (t + 2 < t1) lookup(t + 2);
-        }
-        const int key0 = t * KT;
-        if (key0 < wmax) {
-            if (key0 + KT > wmin || gone)
-                qs.template step<NK, true, CH>(lds[buf][0], lds[buf][1], 0, key0, gone, sl2);
-            else
-                qs.template step<NK, false, CH>(lds[buf][0], lds[buf][1], 0, key0, 0, sl2);
+        if (t + 1 < t1) gone_next = fetch(t + 1, buf ^ 1);
+#pragma unroll
+        for (int sub = 0; sub < KT / 32; ++sub) {
+            const int key0 = t * KT + 32 * sub;
+            if (key0 < wmax) {
+                const unsigned g = gone >> (sub * 32 / CH);
+                if (key0 + 32 > wmin || gone)
+                    qs.template step<true, CH>(lds[buf][0], lds[buf][1], 32 * sub, key0, g, sl2);
+                else
+                    qs.template step<false, CH>(lds[buf][0], lds[buf][1], 32 * sub, key0, 0, sl2);
+            }
         }
     }
 
@@ -256,7 +262,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a)
     if (row < R) {
         const size_t at = (size_t)(s.start + tok) * a.Hq + hq;
         const float lse2 = sum == 0.f ? -INFINITY : qs.m * sl2 + __builtin_amdgcn_logf(sum);
-        if (a.splits > 1) {
+        if (pieces > 1) {
             const size_t p = (size_t)split * a.T * a.Hq + at;
             if (h == 0) a.part_l[p] = lse2;
             if (sum != 0.f) {
@@ -282,15 +288,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// 32-row blocks, for single tokens and short runs of them: the cost is the read
-// of the cache, so each wave streams tiles of 32 keys of its own (every NW-th)
-// through two LDS buffers of its own, with no barrier between waves, and the
-// waves' results are joined at the end.
+// 32-row blocks, for single tokens and short runs of them, and for prompts too
+// few to fill the card with 128-row blocks: the waves share out the keys.  Each
+// wave streams tiles of 32 keys of its own (every NW-th) through two LDS
+// buffers of its own, with no barrier between waves, and the waves' results
+// are joined at the end.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 struct Small {
     static constexpr int STAGE = 2 * 32 * Rows<T, D>::BYTES;  // keys and values
-    static constexpr int NW = STAGE > 16384 ? 2 : 4;
+    static constexpr int NW = STAGE > 8192 ? 2 : 4;           // 64 KB a workgroup (fp32 at D = 128: 128 KB)
     static constexpr int NS = 2;
     static constexpr int OROW = D + 4;  // floats; the pad spreads the rows over the banks
     static constexpr int RING = NW * NS * STAGE;
@@ -298,80 +305,85 @@ struct Small {
     static constexpr int LDS = RING > JOIN ? RING : JOIN;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool PAGED>
 __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(FwdArgs a)
 {
     typedef Small<T, D> C;
     constexpr int NW = C::NW, NS = C::NS;
     constexpr int LOADS = 2 * 32 / Rows<T, D>::PER;
+    constexpr int WIN = 32;  // tiles whose pages a wave holds: lane 2 i + c has run c of the wave's i-th tile
     __shared__ __align__(1024) char lds[C::LDS];
 
     const int hk = blockIdx.x % a.Hkv;
     const int rest = blockIdx.x / a.Hkv, split = rest % a.splits;
     Span s;
     if (!find_block(a.cu, a.B, a.T, a.G, 32, rest / a.splits, s)) return;
-    const int R = s.n * a.G;
-    const int row0 = s.blk * 32;
-    const Keys<T, D, true, 16> keys(a, s, hk);
+    const int R = s.n * a.G, nblk = (R + 31) / 32;
+    const int row0 = (nblk - 1 - s.blk) * 32;
+    const Keys<T, D, PAGED, 16> keys(a, s, hk);
+    const int pieces = keys.pieces(a);
+    if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
     const int row = row0 + (l & 31);
     const int rr = row < R ? row : R - 1;
     const int tok = rr / a.G, hq = hk * a.G + (rr - tok * a.G);
     Queries<T, D> qs;
-    qs.load((const T*)a.q + (size_t)(s.start + tok) * a.q_stride + (size_t)hq * D);
     qs.limit = keys.seen(tok);
     const int wmin = __builtin_amdgcn_readlane(qs.limit, 0), upto = __builtin_amdgcn_readlane(qs.limit, 31);
     const int tiles = (upto + 31) / 32;
-    const int t0 = (int)((long long)tiles * split / a.splits), t1 = (int)((long long)tiles * (split + 1) / a.splits);
+    const int t0 = pieces > 1 ? split * (a.piece / 32) : 0;
+    int t1 = pieces > 1 ? t0 + a.piece / 32 : tiles;
+    t1 = t1 < tiles ? t1 : tiles;
     const float sl2 = a.scale * kLog2e;
 
     char* ring = lds + w * NS * C::STAGE;
-    auto fetch = [&](int t, int p0, int p1, int st) {
+    // the wave's tiles are t0 + w + i NW, i = 0 .. n - 1
+    const int tw = t0 + w, n = t1 > tw ? (t1 - tw + NW - 1) / NW : 0;
+    auto window = [&](int i) { return PAGED ? keys.page(a, (tw + (i + (l >> 1)) * NW) * 32 + (l & 1) * 16) : 0; };
+    int ids = window(0), ids_next = 0;
+    if (n > WIN) ids_next = window(WIN);
+    qs.load((const T*)a.q + (size_t)(s.start + tok) * a.q_stride + (size_t)hq * D);
+    unsigned gone[NS] = {};  // absent runs of the tile in each buffer
+    auto fetch = [&](int i, int st) {
+        const int t = tw + i * NW, at = i % WIN;
+        int p0 = 0, p1 = 0;
+        if (PAGED) {
+            if (at == 0 && i > 0) {
+                ids = ids_next;
+                ids_next = window(i + WIN);
+            }
+            p0 = __builtin_amdgcn_readlane(ids, 2 * at);
+            p1 = __builtin_amdgcn_readlane(ids, 2 * at + 1);
+            gone[st] = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
+        }
         char* tab = ring + st * C::STAGE;
         keys.fetch(a, t * 32, p0, tab, tab + C::STAGE / 2, 0);
         keys.fetch(a, t * 32 + 16, p1, tab, tab + C::STAGE / 2, 16);
     };
-    int p0[NS], p1[NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int t = t0 + w + i * NW;
-        p0[i] = p1[i] = 0;
-        if (t < t1) {
-            p0[i] = keys.page(a, t * 32);
-            p1[i] = keys.page(a, t * 32 + 16);
-            fetch(t, p0[i], p1[i], i);
-        }
-    }
-    for (int t = t0 + w; t < t1; t += NS * NW) {
+    for (int i = 0; i < NS; ++i)
+        if (i < n) fetch(i, i);
+    for (int i0 = 0; i0 < n; i0 += NS) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int tt = t + i * NW;
-            if (tt < t1) {
-                const int tn = tt + NS * NW;
-                int n0 = 0, n1 = 0;
-                if (tn < t1) {
-                    n0 = keys.page(a, tn * 32);
-                    n1 = keys.page(a, tn * 32 + 16);
-                }
-                // this tile has landed; the one behind it may be under way (an
-                // absent run's tile issues fewer loads: then wait for all)
-                const bool whole = tt + NW < t1 && p0[(i + 1) % NS] >= 0 && p1[(i + 1) % NS] >= 0;
-                if (whole)
+        for (int st = 0; st < NS; ++st) {
+            const int i = i0 + st;
+            if (i < n) {
+                // this tile has landed; the one behind it may be under way (a
+                // tile with absent runs has fewer loads: then all are waited for)
+                if (i + 1 < n && gone[(st + 1) % NS] == 0)
                     wait_vm<LOADS>();
                 else
                     wait_vm<0>();
-                const char* tab = ring + i * C::STAGE;
-                const unsigned gone = (p0[i] < 0 ? 1u : 0u) | (p1[i] < 0 ? 2u : 0u);
-                if (tt * 32 + 32 > wmin || gone)
-                    qs.template step<1, true, 16>(tab, tab + C::STAGE / 2, 0, tt * 32, gone, sl2);
+                const int key0 = (tw + i * NW) * 32;
+                const char* tab = ring + st * C::STAGE;
+                if (key0 + 32 > wmin || gone[st])
+                    qs.template step<true, 16>(tab, tab + C::STAGE / 2, 0, key0, gone[st], sl2);
                 else
-                    qs.template step<1, false, 16>(tab, tab + C::STAGE / 2, 0, tt * 32, 0, sl2);
+                    qs.template step<false, 16>(tab, tab + C::STAGE / 2, 0, key0, 0, sl2);
                 // the table's reads are done before its next rows arrive
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                p0[i] = n0;
-                p1[i] = n1;
-                if (tn < t1) fetch(tn, n0, n1, i);
+                if (i + NS < n) fetch(i + NS, st);
             }
         }
     }
@@ -412,91 +424,132 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
         const float inv = sm == 0.f ? 0.f : 1.f / sm;
         const int tk = (row0 + r) / a.G;
         const size_t at = (size_t)(s.start + tk) * a.Hq + hk * a.G + (row0 + r - tk * a.G);
-        if (a.splits > 1) {
+        const float lse2 = sm == 0.f ? -INFINITY : mx * sl2 + __builtin_amdgcn_logf(sm);
+        if (pieces > 1) {
             const size_t p = (size_t)split * a.T * a.Hq + at;
-            if (c == 0) a.part_l[p] = sm == 0.f ? -INFINITY : mx * sl2 + __builtin_amdgcn_logf(sm);
+            if (c == 0) a.part_l[p] = lse2;
             store4<float>(a.part_o + p * D + c, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
         } else {
+            if (a.lse && c == 0) a.lse[at] = lse2 * kLn2;
             store4<T>((T*)a.o + at * D + c, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
         }
     }
 }
 
-// Join the splits of one row: weights 2^(l_s - max), in the order of the
-// splits within each of the workgroup's row copies, then the copies in order.
-template <typename T, int D>
+// Join the pieces of a row: weights 2^(l_s - max).  Q waves share a row's pieces
+// (every Q-th each), and their sums are added in order: the same in every run.
+template <typename T, int D, int Q>
 __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
 {
-    constexpr int LPR = D / 4, NG = 256 / LPR;
-    __shared__ f32x4 acc_s[NG][LPR];
-    __shared__ float sum_s[NG];
-    const size_t row = blockIdx.x;
-    const int tok = (int)(row / a.Hq);
-    int lo = a.cu[0], hi = a.cu[a.B];
-    if (tok < lo || tok >= hi) return;  // not a sequence's row
+    constexpr int V = D / 64;  // values a lane
+    __shared__ float acc_s[4][D];
+    __shared__ float sum_s[4];
+    const int w = uniform(wave_id()), l = lane_id(), q = w % Q;
     const size_t rows = (size_t)a.T * a.Hq;
-    const int g = threadIdx.x / LPR, c = threadIdx.x % LPR;
-    float mx = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, a.part_l[s * rows + row]);
-    float sum = 0.f;
-    f32x4 acc = zero4();
-    for (int s = g; s < a.splits; s += NG) {
-        const float p = a.part_l[s * rows + row];
-        if (p == -INFINITY) continue;  // nothing was seen, nothing written
-        const float f = exp2_hw(p - mx);
-        sum += f;
-        acc += f * *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * D + 4 * c);
+    const size_t row = (size_t)blockIdx.x * (4 / Q) + w / Q;
+    int np = 1;
+    if (row < rows) {
+        const int tok = (int)(row / a.Hq);
+        int b = 0;  // sequences that end at or before the token
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+            const int e = b0 + l < a.B ? a.cu[b0 + l + 1] : 0x7fffffff;
+            b += __popcll(__ballot(e <= tok));
+        }
+        if (b < a.B && tok >= a.cu[b]) np = pieces_of(a, cached_len(a, a.kv_len[b]));
     }
-    acc_s[g][c] = acc;
-    if (c == 0) sum_s[g] = sum;
-    __syncthreads();
-    if (g) return;
+    float acc[V] = {}, sum = 0.f;
+    if (np > 1) {
+        float mx = -INFINITY;
+        for (int s0 = 0; s0 < np; s0 += 64) {
+            float p = s0 + l < np ? a.part_l[(s0 + l) * rows + row] : -INFINITY;
 #pragma unroll
-    for (int x = 1; x < NG; ++x) {
-        acc += acc_s[x][c];
-        sum += sum_s[x];
+            for (int d = 32; d; d >>= 1) p = fmaxf(p, __shfl_xor(p, d));
+            mx = fmaxf(mx, p);
+        }
+#pragma unroll 4
+        for (int s = q; s < np; s += Q) {
+            const float p = a.part_l[s * rows + row];
+            // a piece that saw nothing wrote no output: its old contents are read and not used
+            const float f = p == -INFINITY ? 0.f : exp2_hw(p - mx);
+            sum += f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float x = a.part_o[(s * rows + row) * D + V * l + v];
+                acc[v] += p == -INFINITY ? 0.f : f * x;
+            }
+        }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    store4<T>((T*)a.o + row * D + 4 * c, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    if (Q > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc_s[w][V * l + v] = acc[v];
+        if (l == 0) sum_s[w] = sum;
+        __syncthreads();
+        if (q) return;
+#pragma unroll
+        for (int x = 1; x < Q; ++x) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += acc_s[w + x][V * l + v];
+            sum += sum_s[w + x];
+        }
+    }
+    if (np > 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        T* o = (T*)a.o + row * D + V * l;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = from_f32<T>(acc[v] * inv);
+    }
 }
 
 template <typename T, int D>
 gdn_status launch(const FwdArgs& a, const AttnPlan& p, bool paged, hipStream_t st)
 {
     const dim3 grid((unsigned)((size_t)p.blocks * a.splits * a.Hkv));
-    if (p.small)
-        GDN_LAUNCH("attn_small", (attn_small_kernel<T, D>), grid, dim3(Small<T, D>::NW * 64), st, a);
+    const dim3 threads(p.small ? Small<T, D>::NW * 64 : 256);
+    if (p.small && paged)
+        GDN_LAUNCH("attn_small_paged", (attn_small_kernel<T, D, true>), grid, threads, st, a);
+    else if (p.small)
+        GDN_LAUNCH("attn_small", (attn_small_kernel<T, D, false>), grid, threads, st, a);
     else if (paged)
-        GDN_LAUNCH("attn_paged", (attn_fwd_kernel<T, D, true>), grid, dim3(256), st, a);
+        GDN_LAUNCH("attn_paged", (attn_fwd_kernel<T, D, true>), grid, threads, st, a);
     else
-        GDN_LAUNCH("attn_fwd", (attn_fwd_kernel<T, D, false>), grid, dim3(256), st, a);
-    if (a.splits > 1)
-        GDN_LAUNCH("attn_join", (attn_join_kernel<T, D>), dim3((unsigned)((size_t)a.T * a.Hq)), dim3(256), st, a);
+        GDN_LAUNCH("attn_fwd", (attn_fwd_kernel<T, D, false>), grid, threads, st, a);
+    if (a.splits > 1) {
+        const size_t rows = (size_t)a.T * a.Hq;
+        if (rows <= 1024)
+            GDN_LAUNCH("attn_join", (attn_join_kernel<T, D, 4>), dim3((unsigned)rows), dim3(256), st, a);
+        else
+            GDN_LAUNCH("attn_join", (attn_join_kernel<T, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), st, a);
+    }
     return GDN_OK;
 }
 
 }  // namespace
 
-// 32-row blocks where the sequences have, on average, at most 64 rows.  The key axis is
-// split where the blocks alone do not fill the card's 256 compute units.
+// 32-row blocks where the sequences have, on average, at most 64 rows, and for
+// prompts whose 128-row blocks would leave compute units idle.  The key axis of
+// a cache is cut into pieces of one length where the blocks alone do not fill
+// the card several times: pieces, not shares of each sequence, so that long and
+// short sequences end at the same time.
 AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
 {
     AttnPlan p{};
     const long long G = s.Hq / s.Hkv, rows = (long long)s.T * G;
-    p.small = paged && rows <= 64LL * s.B;
+    const long long big = ((rows + 127) / 128) * s.Hkv;
+    p.small = paged ? rows <= 64LL * s.B : big < 256;
     p.rows = p.small ? 32 : 128;
     p.blocks = (int)(rows / p.rows + s.B);
     p.splits = 1;
+    const long long cap = (long long)s.max_pages * s.page_size;
+    p.piece = 1 << 30;
     if (paged) {
-        // blocks that can hold work: every sequence but the first of a block has less than a whole one
-        const long long busy = (rows + p.rows - 1) / p.rows > s.B ? (rows + p.rows - 1) / p.rows : s.B;
-        const long long items = busy * s.Hkv;
-        const long long want = p.small ? 512 : 512;
-        const long long keys = (long long)s.max_pages * s.page_size;
-        const long long most = keys / (p.small ? 512 : 1024);  // at least so many keys a piece
-        long long n = want / items;
-        n = n > most ? most : n;
-        p.splits = n < 1 ? 1 : n > 128 ? 128 : (int)n;
+        const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B;
+        const long long want = 1024;  // workgroups
+        long long piece = (cap * busy * s.Hkv / want + 127) / 128 * 128;
+        piece = piece < 1024 ? 1024 : piece;
+        if (piece < cap) {
+            p.piece = (int)piece;
+            p.splits = (int)((cap + piece - 1) / piece);
+        }
     }
     if (p.splits > 1) p.ws_bytes = (size_t)p.splits * s.T * s.Hq * (s.D + 1) * sizeof(float);
     return p;
@@ -517,7 +570,7 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
     a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
     a.num_pages = s.num_pages; a.max_pages = s.max_pages;
     a.page_shift = paged ? __builtin_ctz((unsigned)s.page_size) : 0;
-    a.splits = p.splits;
+    a.splits = p.splits; a.piece = p.piece;
     a.scale = s.scale;
     a.part_o = (float*)ws;
     a.part_l = (float*)ws + (size_t)p.splits * s.T * s.Hq * s.D;

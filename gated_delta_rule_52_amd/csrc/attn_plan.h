@@ -11,10 +11,10 @@ namespace gdn {
 
 // How a forward call is laid out: blocks of `rows` query rows (a row is one
 // token of one of the query heads that share a key head), `blocks` of them at
-// most for any lengths, and `splits` pieces of the key axis.
+// most for any lengths, and at most `splits` pieces of `piece` keys each.
 struct AttnPlan {
     bool small;  // 32-row blocks whose waves share out the keys; else 128-row blocks
-    int rows, blocks, splits;
+    int rows, blocks, splits, piece;
     size_t ws_bytes;  // partial outputs [splits][T * Hq][D] and log-sums [splits][T * Hq], fp32
 };
 

@@ -261,8 +261,10 @@ __global__ __launch_bounds__(256) void norm_finish_kernel(const float* __restric
     const int c = blockIdx.x * 16 + (threadIdx.x & 15), strip = threadIdx.x >> 4;
     const float* p = part + (size_t)blockIdx.y * nb * width;
     float s = 0.f;
-    if (c < width)
+    if (c < width) {
+#pragma unroll 8
         for (int r = strip; r < nb; r += 16) s += p[(size_t)r * width + c];
+    }
     tot[strip][threadIdx.x & 15] = s;
     __syncthreads();
     if (strip == 0 && c < width) {
@@ -372,7 +374,7 @@ struct Split {
 };
 Split pick_split(int words, int rows)
 {
-    static const Split all[] = {{16, 1}, {16, 2}, {16, 3}, {16, 4}, {64, 1}, {64, 2}, {64, 3}, {64, 4},
+    static const Split all[] = {{16, 1}, {16, 2}, {16, 3}, {16, 4}, {32, 1}, {32, 2}, {32, 3}, {32, 4}, {64, 1}, {64, 2}, {64, 3}, {64, 4},
                                 {256, 1}, {256, 2}, {256, 3}, {256, 4}, {256, 8}};
     const bool few = rows <= 2048;
     Split best{0, 0};
@@ -390,6 +392,7 @@ template <typename F> gdn_status with_split(Split s, F&& f)
 #define GDN_SPLIT(l, n) \
     if (s.L == l && s.N == n) return f(std::integral_constant<int, l>{}, std::integral_constant<int, n>{})
     GDN_SPLIT(16, 1); GDN_SPLIT(16, 2); GDN_SPLIT(16, 3); GDN_SPLIT(16, 4);
+    GDN_SPLIT(32, 1); GDN_SPLIT(32, 2); GDN_SPLIT(32, 3); GDN_SPLIT(32, 4);
     GDN_SPLIT(64, 1); GDN_SPLIT(64, 2); GDN_SPLIT(64, 3); GDN_SPLIT(64, 4);
     GDN_SPLIT(256, 1); GDN_SPLIT(256, 2); GDN_SPLIT(256, 3); GDN_SPLIT(256, 4); GDN_SPLIT(256, 8);
 #undef GDN_SPLIT

@@ -123,7 +123,7 @@ def test_attention_pointers():
     assert L.gdn_attn_append(sh, P, P, P, None, P, P, P, P, P, P, P, None) == 1
     assert L.gdn_attn_append(sh, P, P, P, P, P, P, P, P, MIS, P, P, None) == 3
     assert L.gdn_attn_paged(sh, P, P, P, None, P, P, P, P, BIG, None) == 1
-    # two sequences of 65536 positions: the key axis is split, which takes a workspace
+    # two sequences of up to 65536 positions: the key axis is split, which takes a workspace
     long = attn(T=2, max_pages=4096)
     assert L.gdn_attn_workspace_bytes(long, gdn.GDN_ATTN_PAGED) > 256
     assert L.gdn_attn_paged(long, P, P, P, P, P, P, P, P, 256, None) == 4
