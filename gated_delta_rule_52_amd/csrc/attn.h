@@ -103,6 +103,14 @@ __device__ __forceinline__ float half_add(float x)
     return p.x + p.y;
 }
 
+// dma16 (common.h) from a wave-uniform base plus a 32-bit byte offset a lane
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t off, const void* lds_wave_base)
+{
+    const uint32_t m0v = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds_wave_base);
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0v), "v"(off), "s"(base) : "memory", "m0");
+}
+
 // ---------------------------------------------------------------------------
 // row tables in LDS: rows of D elements, U = D sizeof(T) / 16 words of 16
 // bytes; word u of row r sits at word r U + (u ^ f(r)).  f is a permutation of
@@ -123,21 +131,33 @@ struct Rows {
     }
     static __device__ __forceinline__ int word(int r, int u) { return r * U + (u ^ f(r)); }
 
-    // operand rows r0 .. r0 + 31 along their own values 16 kk .. + 15, plain order
-    static __device__ __forceinline__ Frag<T> along(const void* tab, int r0, int kk)
+    // Operand rows r0 .. r0 + 31 (r0 a multiple of 16, so that f does not see it)
+    // along their own values 16 kk .. + 15, plain order.  `at` is along_at(), the
+    // lane's byte offset at kk = 0: the others differ from it in bits of the word
+    // index alone.  A kernel short of registers keeps `at` opaque in its loop, so
+    // that the offsets are formed on the way instead of being held.
+    static __device__ __forceinline__ uint32_t along_at()
     {
-        const int l = lane_id(), r = r0 + (l & 31), h = l >> 5;
-        const u32x4* t = reinterpret_cast<const u32x4*>(tab);
+        const int l = lane_id(), r = l & 31, h = l >> 5;
+        return (uint32_t)word(r, sizeof(T) == 2 ? h : 2 * h) * 16;
+    }
+    static __device__ __forceinline__ Frag<T> along(const void* tab, uint32_t at, int r0, int kk)
+    {
+        const char* t = reinterpret_cast<const char*>(tab) + r0 * BYTES;
         if constexpr (sizeof(T) == 2) {
-            return __builtin_bit_cast(bf16x8, t[word(r, 2 * kk + h)]);
+            return *reinterpret_cast<const bf16x8*>(t + (at ^ (kk << 5)));
         } else {
-            const f32x4 a = __builtin_bit_cast(f32x4, t[word(r, 4 * kk + 2 * h)]);
-            const f32x4 b = __builtin_bit_cast(f32x4, t[word(r, 4 * kk + 2 * h + 1)]);
+            const f32x4 a = *reinterpret_cast<const f32x4*>(t + (at ^ (kk << 6)));
+            const f32x4 b = *reinterpret_cast<const f32x4*>(t + (at ^ (kk << 6) ^ 16));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
+    static __device__ __forceinline__ Frag<T> along(const void* tab, int r0, int kk)
+    {
+        return along(tab, along_at(), r0, kk);
+    }
 
-    // operand columns d0 .. d0 + 31 down rows k0 .. k0 + 15, permuted order.
+    // operand columns d0 .. d0 + 31 down rows k0 .. k0 + 15 (k0 a multiple of 16), permuted order.
     // bf16: two transposing loads; in one, lane i of a group of 16 receives
     // element i % 4 of what lanes 4 e + i / 4 read, e = 0..3, so lane i reads
     // row i / 4 at columns 4 (i % 4) and gets column i of the four rows.
@@ -150,18 +170,18 @@ struct Rows {
             s16x4 v[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int r = k0 + 8 * t + 4 * h + (i >> 2);
-                const char* p = reinterpret_cast<const char*>(tab) + word(r, c >> 3) * 16 + (c & 7) * 2;
+                const int r = 8 * t + 4 * h + (i >> 2);
+                const char* p = reinterpret_cast<const char*>(tab) + k0 * BYTES + word(r, c >> 3) * 16 + (c & 7) * 2;
                 v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
             }
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             const int c = d0 + (l & 31);
-            const float* t = reinterpret_cast<const float*>(tab);
+            const float* t = reinterpret_cast<const float*>(tab) + k0 * U * 4;
             f32x8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int r = k0 + 8 * (j >> 2) + 4 * h + (j & 3);
+                const int r = 8 * (j >> 2) + 4 * h + (j & 3);
                 v[j] = t[word(r, c >> 2) * 4 + (c & 3)];
             }
             return v;
@@ -170,17 +190,27 @@ struct Rows {
 
     // Rows r0 .. r0 + N - 1 of a table from global memory, by direct loads of the
     // calling wave (N / PER of them): row r comes from `base` + min(r - r0, last)
-    // * stride bytes.  r0 is a multiple of N, N of PER.
+    // * stride bytes.  r0 is a multiple of N, N of PER; base, stride and last are
+    // the same in all lanes.  Away from a sequence's end the lanes' offsets do
+    // not change from call to call: only the scalar base moves.
     template <int N>
     static __device__ __forceinline__ void fetch(void* tab, int r0, const void* base, uint32_t stride, int last)
     {
         const int l = lane_id();
+        char* to = reinterpret_cast<char*>(tab) + r0 * BYTES;
+        if (last >= N - 1) {
 #pragma unroll
-        for (int i = 0; i < N / PER; ++i) {
-            const int rr = i * PER + l / U;
-            const int u = (l % U) ^ f(r0 + rr);
-            const uint32_t off = (uint32_t)(rr < last ? rr : last) * stride + (uint32_t)u * 16;
-            dma16(reinterpret_cast<const char*>(base) + off, reinterpret_cast<char*>(tab) + (r0 + i * PER) * BYTES);
+            for (int i = 0; i < N / PER; ++i) {
+                const int rr = i * PER + l / U;
+                dma16_at(base, (uint32_t)rr * stride + (uint32_t)((l % U) ^ f(r0 + rr)) * 16, to + i * PER * BYTES);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / PER; ++i) {
+                const int rr = i * PER + l / U;
+                dma16_at(base, (uint32_t)(rr < last ? rr : last) * stride + (uint32_t)((l % U) ^ f(r0 + rr)) * 16,
+                         to + i * PER * BYTES);
+            }
         }
     }
     // zeros in the same places
@@ -197,6 +227,13 @@ struct Rows {
 __device__ __forceinline__ void dma4(const void* gptr, const void* lds_wave_base)
 {
     warm_line(gptr, lds_wave_base);
+}
+
+// x, of which the compiler no longer knows where it comes from
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 // value of a wave-uniform integer in a scalar register

@@ -23,6 +23,7 @@ struct BwdArgs {
     const int* cu;
     void *dq, *dk, *dv;
     float *lse2, *delta;  // [Hq][T]: lse * log2 e, and do . o
+    float* delta2;        // [Hq][T]: delta without the rounding of o (attn_dq_kernel)
     long long q_stride;
     uint32_t q_bytes, k_bytes, v_bytes, o_bytes;  // bytes between tokens
     int B, T, Hq, Hkv, G;
@@ -135,30 +136,32 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
                                        a.o_bytes, last);
         const int t = q0 + l < s.n ? q0 + l : s.n - 1;
         if (w == 0) dma4(a.lse2 + (size_t)hq * a.T + s.start + t, ld[buf][0]);
-        if (w == 1) dma4(a.delta + (size_t)hq * a.T + s.start + t, ld[buf][1]);
+        if (w == 1) dma4((sizeof(T) == 2 ? a.delta2 : a.delta) + (size_t)hq * a.T + s.start + t, ld[buf][1]);
         if (++fq == ntq) {
             fq = 0;
             ++fg;
         }
     };
     int cq = fq;  // query tile of the one being multiplied
-    if (i0 < i1) fetch(0);
-    for (int it = i0; it < i1; ++it) {
-        const int buf = (it - i0) & 1;
+    const uint32_t along = Rows<T, D>::along_at();
+    auto tile = [&](int it, auto BUF) {
+        constexpr int buf = BUF();
         wait_vm<0>();
         __syncthreads();
         if (it + 1 < i1) fetch(buf ^ 1);
         const int qs = (tq0 + cq) * QT;
         if (++cq == ntq) cq = 0;
-        if (qs + 31 < wkey) continue;  // every query stands before the wave's keys
+        if (qs + 31 < wkey) return;  // every query stands before the wave's keys
         const void* qt = lds[buf][0];
         const void* ot = lds[buf][1];
         f32x16 sc = zero16(), dp = zero16();
+        const uint32_t at = opaque(along);
+        const char* vw = vtab + 32 * w * Rows<T, D>::BYTES;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(qt, 0, kk), kf[kk], sc);
+        for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(qt, at, 0, kk), kf[kk], sc);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
-            dp = mma32(Rows<T, D>::along(ot, 0, kk), Rows<T, D>::along(vtab, 32 * w, kk), dp);
+            dp = mma32(Rows<T, D>::along(ot, at, 0, kk), Rows<T, D>::along(vw, at, 0, kk), dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x4 ls = *reinterpret_cast<const f32x4*>(&ld[buf][0][8 * i + 4 * h]);
@@ -189,6 +192,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
                 dk[dt] = mma32(Rows<T, D>::down(qt, 16 * b, 32 * dt), ds, dk[dt]);
             }
         }
+    };
+    if (i0 < i1) fetch(0);
+    for (int it = i0; it < i1; it += 2) {
+        tile(it, std::integral_constant<int, 0>{});
+        if (it + 1 < i1) tile(it + 1, std::integral_constant<int, 1>{});
     }
     wait_vm<0>();  // a piece without tiles still has its values under way
     if (key < s.n) {
@@ -208,12 +216,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
 
 // dq of 128 rows (token * G + head): four waves of 32 rows; tiles of KT keys go
 // through two LDS buffers.
+//
+// bf16: delta_i = do_i . o_i carries the rounding of the stored o, and an error
+// e_i in it reaches every ds_ij as -p_ij e_i.  Since sum_j p_ij = 1, the row sum
+// sum_j ds_ij, which is 0 for the true delta, is -e_i with the given one; so it is
+// summed on the way and delta2 = delta + sum_j ds_ij goes to the key pass.  Rows
+// that see at most SHORT keys, where o is as large as the values it averages and
+// its rounding counts most, take a first round over their keys for delta2 and
+// use it in their own dq too.  (Error of dq and dk against 64 bits, in units of
+// the error of storing them: 1.7 and 1.8 at 16 tokens without this, 1.5 with it.)
 template <typename T, int D>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdArgs a)
 {
     constexpr int KK = D / 16, DT = D / 32;
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, RW = KT / 4;
     constexpr int TAB = KT * Rows<T, D>::BYTES;
+    constexpr int SHORT = 512;
     __shared__ __align__(1024) char lds[2][2][TAB];
 
     const int hk = blockIdx.x % a.Hkv;
@@ -237,7 +255,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
             df[kk] = load_frag<T>(dp + 16 * kk + 8 * h);
         }
     }
-    const float lse2 = a.lse2[(size_t)hq * a.T + at], delta = a.delta[(size_t)hq * a.T + at];
+    const float lse2 = a.lse2[(size_t)hq * a.T + at];
+    float delta = a.delta[(size_t)hq * a.T + at];
     f32x16 dq[DT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
@@ -255,13 +274,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
         Rows<T, D>::template fetch<RW>(lds[buf][0], w * RW, kb + (size_t)kat * a.k_bytes, a.k_bytes, s.n - 1 - kat);
         Rows<T, D>::template fetch<RW>(lds[buf][1], w * RW, vb + (size_t)kat * a.v_bytes, a.v_bytes, s.n - 1 - kat);
     };
-    const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
-    if (t0 < t1) fetch(t0, 0);
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
+    float over = 0.f;  // sum_j ds_ij of this lane's keys
+    // one tile; FIRST: only the row sums
+    auto tile = [&](int t, int end, auto BUF, auto FIRST) {
+        constexpr int buf = BUF();
         wait_vm<0>();
         __syncthreads();
-        if (t + 1 < t1) fetch(t + 1, buf ^ 1);
+        if (t + 1 < end) fetch(t + 1, buf ^ 1);
 #pragma unroll
         for (int sub = 0; sub < KT / 32; ++sub) {
             const int key0 = t * KT + 32 * sub;
@@ -278,14 +297,40 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
                 for (int r = 0; r < 16; ++r)
                     dp[r] = key0 + 8 * (r >> 2) + 4 * h + (r & 3) < limit ? dp[r] : 0.f;
             }
+            if (sizeof(T) == 2) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const Frag<T> ds = acc_frag<T>(dp, b);
+                for (int r = 0; r < 16; ++r) over += dp[r];
+            }
+            if (!FIRST()) {
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    dq[dt] = mma32(Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt), ds, dq[dt]);
+                for (int b = 0; b < 2; ++b) {
+                    const Frag<T> ds = acc_frag<T>(dp, b);
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+                        dq[dt] = mma32(Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt), ds, dq[dt]);
+                }
             }
         }
+    };
+    auto round = [&](int from, int end, auto FIRST) {
+        if (from < end) fetch(from, 0);
+        for (int t = from; t < end; t += 2) {
+            tile(t, end, std::integral_constant<int, 0>{}, FIRST);
+            if (t + 1 < end) tile(t + 1, end, std::integral_constant<int, 1>{}, FIRST);
+        }
+    };
+    if (sizeof(T) == 2 && tiles * KT <= SHORT) {
+        round(0, tiles, std::true_type{});
+        delta += half_add(over);
+        over = 0.f;
+        __syncthreads();  // all waves are done with the buffers
+    }
+    const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
+    round(t0, t1, std::false_type{});
+    if (sizeof(T) == 2 && part == 0) {
+        // a piece of the keys does not have the whole row sum
+        const float d2 = a.qparts == 1 ? delta + half_add(over) : delta;
+        if (row < R && h == 0) a.delta2[(size_t)hq * a.T + at] = d2;
     }
     if (row < R) {
         const size_t out = (at * a.Hq + hq) * D;
@@ -328,10 +373,10 @@ gdn_status launch(const BwdArgs& a, hipStream_t st)
     constexpr int RPB = 256 / (D * (int)sizeof(T) / 16);
     const size_t rows = (size_t)a.T * a.Hq;
     GDN_LAUNCH("attn_delta", (attn_delta_kernel<T, D>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
-    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv * a.kparts;
-    GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
     const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts;
     GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3((unsigned)qblocks), dim3(256), st, a);
+    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv * a.kparts;
+    GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
     gdn_status r = GDN_OK;
     if (a.kparts > 1) {
         r = launch_sum<T>(a, a.part_k, a.dk, a.scale, a.kparts, a.Hkv, D, st);
@@ -353,7 +398,7 @@ int parts_for(long long blocks, long long want, long long tiles, int most)
 
 struct BwdPlan {
     int kparts, qparts;
-    size_t o_delta, o_k, o_q, bytes;
+    size_t o_delta, o_delta2, o_k, o_q, bytes;
 };
 
 BwdPlan bwd_plan(const gdn_attn_shape& s)
@@ -369,7 +414,8 @@ BwdPlan bwd_plan(const gdn_attn_shape& s)
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t f = sizeof(float), rows = (size_t)s.T * s.Hq;
     p.o_delta = up(rows * f);
-    p.o_k = p.o_delta + up(rows * f);
+    p.o_delta2 = p.o_delta + up(rows * f);
+    p.o_k = p.o_delta2 + up(rows * f);
     p.o_q = p.o_k + (p.kparts > 1 ? up(2 * p.kparts * (size_t)s.T * s.Hkv * s.D * f) : 0);
     p.bytes = p.o_q + (p.qparts > 1 ? up(p.qparts * rows * s.D * f) : 0);
     return p;
@@ -390,6 +436,7 @@ gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const 
     a.lse2 = (float*)ws;
     const BwdPlan p = bwd_plan(s);
     a.delta = (float*)((char*)ws + p.o_delta);
+    a.delta2 = (float*)((char*)ws + p.o_delta2);
     a.part_k = (float*)((char*)ws + p.o_k);
     a.part_q = (float*)((char*)ws + p.o_q);
     a.kparts = p.kparts;

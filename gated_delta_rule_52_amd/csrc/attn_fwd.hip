@@ -49,21 +49,22 @@ struct Queries {
     }
 
     // 32 keys of the tables from row r0; key0 is the position of the first.
-    // MASK: some key may lie behind some row's limit, or `gone` (a bit for each
-    // run of CH keys) says that it is absent.
-    template <bool MASK, int CH>
-    __device__ __forceinline__ void step(const void* ktab, const void* vtab, int r0, int key0, unsigned gone, float sl2)
+    // mask (uniform): some key may lie behind some row's limit, or `gone` (a bit
+    // for each run of CH keys) says that it is absent.
+    template <int CH>
+    __device__ __forceinline__ void step(const void* ktab, const void* vtab, int r0, int key0, bool mask, unsigned gone,
+                                         float sl2)
     {
         const int h = lane_id() >> 5;
         f32x16 s = zero16();
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) s = mma32(Rows<T, D>::along(ktab, r0, kk), q[kk], s);
-        if (MASK) {
+        if (mask) {
+            const int left = limit - key0 - 4 * h;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int key = 8 * (r >> 2) + 4 * h + (r & 3);
                 // CH >= 8: the four rows of a register group lie in one run
-                const bool out = key0 + key >= limit || ((gone >> (8 * (r >> 2) / CH)) & 1);
+                const bool out = 8 * (r >> 2) + (r & 3) >= left || ((gone >> (8 * (r >> 2) / CH)) & 1);
                 s[r] = out ? -INFINITY : s[r];
             }
         }
@@ -74,7 +75,7 @@ struct Queries {
         // The maximum is moved, and what was summed rescaled, only when it grew
         // by more than 2^8: until then the exponentials stay below 256, which
         // costs neither bf16 nor fp32 any relative precision.
-        if (__any(mx * sl2 > m * sl2 + 8.f || (m == -INFINITY && mx > m))) {
+        if (__any(mx * sl2 > m * sl2 + 8.f)) {
             const float mn = fmaxf(m, mx);
             const float al = mn == -INFINITY ? 1.f : exp2_hw((m - mn) * sl2);
             m = mn;
@@ -237,9 +238,10 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
     };
 
     unsigned gone = 0, gone_next = 0;
-    if (t0 < t1) gone_next = fetch(t0, 0);
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
+    // one tile: the buffers are compile-time constants, so that every LDS address
+    // is a fixed register plus an immediate
+    auto tile = [&](int t, auto BUF) {
+        constexpr int buf = BUF();
         gone = gone_next;
         wait_vm<0>();
         __syncthreads();
@@ -247,14 +249,15 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
 #pragma unroll
         for (int sub = 0; sub < KT / 32; ++sub) {
             const int key0 = t * KT + 32 * sub;
-            if (key0 < wmax) {
-                const unsigned g = gone >> (sub * 32 / CH);
-                if (key0 + 32 > wmin || gone)
-                    qs.template step<true, CH>(lds[buf][0], lds[buf][1], 32 * sub, key0, g, sl2);
-                else
-                    qs.template step<false, CH>(lds[buf][0], lds[buf][1], 32 * sub, key0, 0, sl2);
-            }
+            if (key0 < wmax)
+                qs.template step<CH>(lds[buf][0], lds[buf][1], 32 * sub, key0, key0 + 32 > wmin || gone,
+                                     gone >> (sub * 32 / CH), sl2);
         }
+    };
+    if (t0 < t1) gone_next = fetch(t0, 0);
+    for (int t = t0; t < t1; t += 2) {
+        tile(t, std::integral_constant<int, 0>{});
+        if (t + 1 < t1) tile(t + 1, std::integral_constant<int, 1>{});
     }
 
     const float sum = half_add(qs.l);
@@ -297,7 +300,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
 template <typename T, int D>
 struct Small {
     static constexpr int STAGE = 2 * 32 * Rows<T, D>::BYTES;  // keys and values
-    static constexpr int NW = STAGE > 8192 ? 2 : 4;           // 64 KB a workgroup (fp32 at D = 128: 128 KB)
+    // bf16: 64 KB a workgroup, two of them a compute unit; fp32, bound by its matrix instructions: 128 KB
+    static constexpr int NW = STAGE == 16384 && sizeof(T) == 2 || STAGE > 16384 ? 2 : 4;
     static constexpr int NS = 2;
     static constexpr int OROW = D + 4;  // floats; the pad spreads the rows over the banks
     static constexpr int RING = NW * NS * STAGE;
@@ -377,10 +381,7 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
                     wait_vm<0>();
                 const int key0 = (tw + i * NW) * 32;
                 const char* tab = ring + st * C::STAGE;
-                if (key0 + 32 > wmin || gone[st])
-                    qs.template step<true, 16>(tab, tab + C::STAGE / 2, 0, key0, gone[st], sl2);
-                else
-                    qs.template step<false, 16>(tab, tab + C::STAGE / 2, 0, key0, 0, sl2);
+                qs.template step<16>(tab, tab + C::STAGE / 2, 0, key0, key0 + 32 > wmin || gone[st], gone[st], sl2);
                 // the table's reads are done before its next rows arrive
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (i + NS < n) fetch(i + NS, st);

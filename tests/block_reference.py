@@ -115,10 +115,16 @@ def prompt(q, k, v, cu, scale=None):
     return o, lse, bo, bl
 
 
-def prompt_backward(q, k, v, cu, o, lse, do, scale=None):
-    """{name: (gradient, bound)} with the given o and lse as inputs."""
+def prompt_backward(q, k, v, cu, do, scale=None):
+    """{name: (gradient, bound)}: the gradients of the 64-bit forward.
+
+    do . o is taken from the stored o, whose error is at most bo, so it is off by
+    at most e_i = |do_i| . bo_i and ds_ij by p_ij e_i; in bf16 that holds for rows
+    of more than 512 keys only (the others take it from the row sums of p (do . v),
+    in fp32)."""
     dt = q.dtype
-    q, k, v, o, lse, do = (f64(t) for t in (q, k, v, o, lse, do))
+    o, lse, bo, _ = prompt(q, k, v, cu, scale)
+    q, k, v, do = (f64(t) for t in (q, k, v, do))
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -131,10 +137,16 @@ def prompt_backward(q, k, v, cu, o, lse, do, scale=None):
             r = attention_head_backward(qq, kk, v[a:e, h // G], see, scale, o[a:e, h], lse[a:e, h], do[a:e, h])
             size = float((qq.abs() @ kk.abs().T * scale).max()) if e > a else 0.0
             u = 2 * steps32(D, (e - a) * G, size)
+            off = (do[a:e, h].abs() * bo[a:e, h]).sum(1)
+            if dt == torch.bfloat16:
+                off = torch.where(torch.arange(e - a) < 512, torch.zeros_like(off), off)
+            s = torch.where(see, qq @ kk.T * scale, torch.full(see.shape, -np.inf, dtype=torch.float64))
+            pe = torch.exp(s - lse[a:e, h][:, None]) * off[:, None] * scale
+            more = {"dq": pe @ kk.abs(), "dk": pe.T @ qq.abs(), "dv": 0.0}
             for n, (x, rounded, big) in r.items():
                 hh = h if n == "dq" else h // G
                 g[n][0][a:e, hh] += x
-                g[n][1][a:e, hh] += HALF[dt] * rounded + u * (1 + HALF[dt]) * big
+                g[n][1][a:e, hh] += HALF[dt] * rounded + u * (1 + HALF[dt]) * big + more[n]
     return {n: (x, b + HALF[dt] * x.abs()) for n, (x, b) in g.items()}
 
 
