@@ -74,6 +74,11 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle by device index; the public call makes a Stream object for it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _take(t, name, shape, dtype, device, *, stride=False):
     """Check a tensor: its shape, type and device, dense (or, with stride, dense
     within its first index).  Returns the elements between first indices."""
@@ -98,13 +103,13 @@ def _opt(t, name, shape, dtype, device):
 
 def _run(fn, name, device, *args):
     """Call on the device's current stream, with that device current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc != 0:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
         raise GdnError(rc, name)
 
 
@@ -137,10 +142,11 @@ def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):
     Returns (h, n, rstd); out = (h, n, rstd) takes them (h, rstd may be None: not
     wanted).  Without y, h is x."""
     dt, dev = _dtype(x, "x"), _gpu(x, "x")
-    width, lead = x.shape[-1], x.shape[:-1]
-    _take(x, "x", x.shape, x.dtype, dev)
+    shape, dtype = x.shape, x.dtype
+    width, lead = shape[-1], shape[:-1]
+    _take(x, "x", shape, dtype, dev)
     _take(weight, "weight", (width,), torch.float32, dev)
-    _opt(y, "y", x.shape, x.dtype, dev)
+    _opt(y, "y", shape, dtype, dev)
     _opt(res_scale, "res_scale", (width,), torch.float32, dev)
     if res_scale is not None and y is None:
         raise ValueError("res_scale scales y: pass y too")
@@ -149,10 +155,10 @@ def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):
         n, rstd = torch.empty_like(x), torch.empty(lead, dtype=torch.float32, device=dev)
     else:
         h, n, rstd = out
-        _opt(h, "h", x.shape, x.dtype, dev)
-        _take(n, "n", x.shape, x.dtype, dev)
+        _opt(h, "h", shape, dtype, dev)
+        _take(n, "n", shape, dtype, dev)
         _opt(rstd, "rstd", lead, torch.float32, dev)
-    sh = GdnNormShape(_rows(x), 1, width, dt, eps, 0)
+    sh = GdnNormShape(lead.numel(), 1, width, dt, eps, 0)
     _run(lib().gdn_norm_block, "gdn_norm_block", dev, ctypes.byref(sh), _p(x), _p(y), _p(res_scale), _p(weight), _p(h),
          _p(n), _p(rstd))
     return (x if h is None and y is None else h), n, rstd

@@ -245,21 +245,73 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 // of theirs reaches outside the buffers.
 // ---------------------------------------------------------------------------
 struct Span {
-    int b, start, n, blk;
+    int b, start, n;
+    int level, blocks;  // the block's place and the number of the sequence's blocks
 };
 
 // Block `id` of all sequences' blocks of BR rows, a sequence of n tokens having
 // n * G rows; every wave finds it by itself.  False: there is no such block.
+// BY_LEVEL, up to 64 sequences: the blocks come in the order of their level, the
+// highest first, across sequences: a causal prompt's block has work in
+// proportion to its level, and the largest pieces first is what lets a grid end
+// evenly (eight packed prompts of up to 4096 tokens, forward and backward: 737 us
+// with the sequences one after the other, 668 us by level).  Otherwise the
+// sequences come one after the other, each from its highest level down, which
+// keeps the blocks that share keys together (new tokens over a cache: 295 us by
+// level, 241 us so).
+template <bool BY_LEVEL>
 __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, int T, int G, int BR, int id, Span& s)
 {
     const int l = lane_id();
-    int before = 0;
-    for (int b0 = 0; b0 < B; b0 += 64) {
+    auto bounds = [&](int b0, int& st, int& en) {
         const int b = b0 + l < B ? b0 + l : B - 1;
-        int st = cu[b], en = cu[b + 1];
+        st = cu[b], en = cu[b + 1];
         st = st < 0 ? 0 : st > T ? T : st;
         en = en < st ? st : en > T ? T : en;
-        const int nb = b0 + l < B ? (int)(((long long)(en - st) * G + BR - 1) / BR) : 0;
+        return b0 + l < B ? (int)(((long long)(en - st) * G + BR - 1) / BR) : 0;
+    };
+    auto wave_sum = [&](int x) {
+#pragma unroll
+        for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+        return uniform(x);
+    };
+    auto take = [&](int b0, int lane, int level, int st, int en, int nb) {
+        s.b = b0 + lane;
+        s.start = __builtin_amdgcn_readlane(st, lane);
+        s.n = __builtin_amdgcn_readlane(en, lane) - s.start;
+        s.blocks = __builtin_amdgcn_readlane(nb, lane);
+        s.level = level;
+    };
+    int st, en;
+    if (BY_LEVEL && B <= 64) {
+        const int nb = bounds(0, st, en);
+        if (id >= wave_sum(nb)) return false;
+        // the level j with above(j + 1) <= id < above(j), above(j) the number of blocks at level j and higher
+        int lo = 0, hi = nb, past = 0;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            const int o = __shfl_xor(hi, d);
+            hi = hi > o ? hi : o;
+        }
+        hi = uniform(hi);
+        while (hi - lo > 1) {  // above(lo) > id >= above(hi)
+            const int mid = (lo + hi) >> 1;
+            const int n = wave_sum(nb > mid ? nb - mid : 0);
+            if (n > id) {
+                lo = mid;
+            } else {
+                hi = mid;
+                past = n;
+            }
+        }
+        uint64_t have = __ballot(nb > lo);
+        for (int i = id - past; i > 0; --i) have &= have - 1;
+        take(0, __builtin_ctzll(have), lo, st, en, nb);
+        return true;
+    }
+    int before = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        const int nb = bounds(b0, st, en);
         int inc = nb;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -269,10 +321,7 @@ __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, in
         const uint64_t hit = __ballot(before + inc > id);
         if (hit) {
             const int first = __builtin_ctzll(hit);
-            s.b = b0 + first;
-            s.start = __builtin_amdgcn_readlane(st, first);
-            s.n = __builtin_amdgcn_readlane(en, first) - s.start;
-            s.blk = id - (before + __builtin_amdgcn_readlane(inc - nb, first));
+            take(b0, first, before + __builtin_amdgcn_readlane(inc, first) - 1 - id, st, en, nb);
             return true;
         }
         before += __builtin_amdgcn_readlane(inc, 63);

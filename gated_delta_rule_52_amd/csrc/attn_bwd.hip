@@ -22,8 +22,7 @@ struct BwdArgs {
     const float* lse;
     const int* cu;
     void *dq, *dk, *dv;
-    float *lse2, *delta;  // [Hq][T]: lse * log2 e, and do . o
-    float* delta2;        // [Hq][T]: delta without the rounding of o (attn_dq_kernel)
+    float *lse2, *delta;  // [Hq][T]: lse * log2 e and delta, left by the query pass for the key pass
     long long q_stride;
     uint32_t q_bytes, k_bytes, v_bytes, o_bytes;  // bytes between tokens
     int B, T, Hq, Hkv, G;
@@ -31,44 +30,6 @@ struct BwdArgs {
     int kparts, qparts;  // pieces that a key block's queries, a query block's keys are cut into
     float *part_k, *part_q;  // [2][kparts][T * Hkv][D] (dk, dv), [qparts][T * Hq][D]
 };
-
-// delta and the log-sums in base 2, by query head.  A row of D values is held by
-// D / VE lanes.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_delta_kernel(BwdArgs a)
-{
-    constexpr int VE = 16 / (int)sizeof(T), L = D / VE;
-    const size_t rows = (size_t)a.T * a.Hq;
-    const size_t row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int c = (threadIdx.x % L) * VE;
-    const size_t at = (row < rows ? row : rows - 1) * D + c;
-    float sum = 0.f;
-    const T* o = (const T*)a.o + at;
-    const T* d = (const T*)a.dO + at;
-    if constexpr (sizeof(T) == 2) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(o), y = *reinterpret_cast<const u32x4*>(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sum += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16);
-            sum += __uint_as_float(x[i] & 0xffff0000u) * __uint_as_float(y[i] & 0xffff0000u);
-        }
-    } else {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(o), y = *reinterpret_cast<const f32x4*>(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum += x[i] * y[i];
-    }
-    if (L == 8) {
-        sum = lane8_sum(sum);
-    } else {
-        sum = lane16_sum(sum);
-        if (L == 32) sum += __shfl_xor(sum, 16);
-    }
-    if (c == 0 && row < rows) {
-        const size_t t = row / a.Hq, h = row % a.Hq;
-        a.delta[h * a.T + t] = sum;
-        a.lse2[h * a.T + t] = a.lse[row] * kLog2e;
-    }
-}
 
 // Four accumulator rows of one column times f: to the gradient, or to a piece's
 // partial sums where the work is cut up.
@@ -98,8 +59,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
     const int hk = blockIdx.x % a.Hkv;
     const int rest = blockIdx.x / a.Hkv, part = rest % a.kparts;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, 1, 128, rest / a.kparts, s)) return;
-    const int key0 = s.blk * 128;  // the first keys have the most queries: they come first
+    if (!find_block<true>(a.cu, a.B, a.T, 1, 128, rest / a.kparts, s)) return;
+    const int key0 = (s.blocks - 1 - s.level) * 128;  // the first keys have the most queries: they come first
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
     const int wkey = key0 + 32 * w;
     const int key = wkey + (l & 31);
@@ -136,7 +97,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
                                        a.o_bytes, last);
         const int t = q0 + l < s.n ? q0 + l : s.n - 1;
         if (w == 0) dma4(a.lse2 + (size_t)hq * a.T + s.start + t, ld[buf][0]);
-        if (w == 1) dma4((sizeof(T) == 2 ? a.delta2 : a.delta) + (size_t)hq * a.T + s.start + t, ld[buf][1]);
+        if (w == 1) dma4(a.delta + (size_t)hq * a.T + s.start + t, ld[buf][1]);
         if (++fq == ntq) {
             fq = 0;
             ++fg;
@@ -220,10 +181,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
 // bf16: delta_i = do_i . o_i carries the rounding of the stored o, and an error
 // e_i in it reaches every ds_ij as -p_ij e_i.  Since sum_j p_ij = 1, the row sum
 // sum_j ds_ij, which is 0 for the true delta, is -e_i with the given one; so it is
-// summed on the way and delta2 = delta + sum_j ds_ij goes to the key pass.  Rows
-// that see at most SHORT keys, where o is as large as the values it averages and
-// its rounding counts most, take a first round over their keys for delta2 and
-// use it in their own dq too.  (Error of dq and dk against 64 bits, in units of
+// summed on the way and delta + sum_j ds_ij goes to the key pass.  Rows that see
+// at most SHORT keys, where o is as large as the values it averages and its
+// rounding counts most, take a first round over their keys for it and use it in
+// their own dq too.  (Error of dq and dk against 64 bits, in units of
 // the error of storing them: 1.7 and 1.8 at 16 tokens without this, 1.5 with it.)
 template <typename T, int D>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdArgs a)
@@ -237,26 +198,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
     const int hk = blockIdx.x % a.Hkv;
     const int rest = blockIdx.x / a.Hkv, part = rest % a.qparts;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, a.G, 128, rest / a.qparts, s)) return;
-    const int R = s.n * a.G, nblk = (R + 127) / 128;
-    const int row0 = (nblk - 1 - s.blk) * 128;
+    if (!find_block<true>(a.cu, a.B, a.T, a.G, 128, rest / a.qparts, s)) return;
+    const int R = s.n * a.G, row0 = s.level * 128;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
     const int row = row0 + 32 * w + (l & 31);
     const int rr = row < R ? row : R - 1;
     const int tok = rr / a.G, hq = hk * a.G + (rr - tok * a.G);
     const size_t at = (size_t)(s.start + tok);
     Frag<T> qf[KK], df[KK];
+    float delta = 0.f;
     {
         const T* qp = (const T*)a.q + at * a.q_stride + (size_t)hq * D;
         const T* dp = (const T*)a.dO + (at * a.Hq + hq) * D;
+        const T* op = (const T*)a.o + (at * a.Hq + hq) * D;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             qf[kk] = load_frag<T>(qp + 16 * kk + 8 * h);
             df[kk] = load_frag<T>(dp + 16 * kk + 8 * h);
+            const Frag<T> of = load_frag<T>(op + 16 * kk + 8 * h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) delta += (float)of[j] * (float)df[kk][j];
         }
     }
-    const float lse2 = a.lse2[(size_t)hq * a.T + at];
-    float delta = a.delta[(size_t)hq * a.T + at];
+    delta = half_add(delta);
+    const float lse2 = a.lse[at * a.Hq + hq] * kLog2e;
     f32x16 dq[DT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
@@ -327,10 +292,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
     }
     const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
     round(t0, t1, std::false_type{});
-    if (sizeof(T) == 2 && part == 0) {
+    if (part == 0) {
         // a piece of the keys does not have the whole row sum
-        const float d2 = a.qparts == 1 ? delta + half_add(over) : delta;
-        if (row < R && h == 0) a.delta2[(size_t)hq * a.T + at] = d2;
+        if (sizeof(T) == 2 && a.qparts == 1) delta += half_add(over);
+        if (row < R && h == 0) {
+            a.lse2[(size_t)hq * a.T + at] = lse2;
+            a.delta[(size_t)hq * a.T + at] = delta;
+        }
     }
     if (row < R) {
         const size_t out = (at * a.Hq + hq) * D;
@@ -343,14 +311,28 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
 }
 
 // out = f * sum of the np pieces' partial sums, in their order, for the rows of
-// sequences; four values a thread.
+// sequences; four values a thread.  Up to three outputs of one call.
+struct SumArgs {
+    const float* part[3];
+    void* out[3];
+    float f[3];
+    int np[3], per_token[3];
+    size_t n[3];
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ cu, int B, const float* __restrict__ part,
-                                                       T* out, float f, int np, int per_token, size_t n)
+__global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ cu, int B, SumArgs a)
 {
+    const int y = blockIdx.y;
+    const float* part = y == 0 ? a.part[0] : y == 1 ? a.part[1] : a.part[2];
+    T* out = (T*)(y == 0 ? a.out[0] : y == 1 ? a.out[1] : a.out[2]);
+    const float f = y == 0 ? a.f[0] : y == 1 ? a.f[1] : a.f[2];
+    const int np = y == 0 ? a.np[0] : y == 1 ? a.np[1] : a.np[2];
+    const int per = y == 0 ? a.per_token[0] : y == 1 ? a.per_token[1] : a.per_token[2];
+    const size_t n = y == 0 ? a.n[0] : y == 1 ? a.n[1] : a.n[2];
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
-    const int tok = (int)(i / per_token);
+    const int tok = (int)(i / per);
     if (tok < cu[0] || tok >= cu[B]) return;
     f32x4 s = *reinterpret_cast<const f32x4*>(part + i);
 #pragma unroll 4
@@ -358,47 +340,44 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ c
     store4<T>(out + i, s[0] * f, s[1] * f, s[2] * f, s[3] * f);
 }
 
-template <typename T>
-gdn_status launch_sum(const BwdArgs& a, const float* part, void* out, float f, int np, int heads, int D, hipStream_t st)
-{
-    const size_t n = (size_t)a.T * heads * D;
-    GDN_LAUNCH("attn_sum", attn_sum_kernel<T>, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), st, a.cu, a.B, part,
-               (T*)out, f, np, heads * D, n);
-    return GDN_OK;
-}
-
 template <typename T, int D>
 gdn_status launch(const BwdArgs& a, hipStream_t st)
 {
-    constexpr int RPB = 256 / (D * (int)sizeof(T) / 16);
-    const size_t rows = (size_t)a.T * a.Hq;
-    GDN_LAUNCH("attn_delta", (attn_delta_kernel<T, D>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
     const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts;
     GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3((unsigned)qblocks), dim3(256), st, a);
     const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv * a.kparts;
     GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
-    gdn_status r = GDN_OK;
+    SumArgs m{};
+    int n = 0;
+    size_t most = 0;
+    auto add = [&](const float* part, void* out, float f, int np, int heads) {
+        m.part[n] = part; m.out[n] = out; m.f[n] = f; m.np[n] = np; m.per_token[n] = heads * D;
+        m.n[n] = (size_t)a.T * heads * D;
+        most = most > m.n[n] ? most : m.n[n];
+        ++n;
+    };
     if (a.kparts > 1) {
-        r = launch_sum<T>(a, a.part_k, a.dk, a.scale, a.kparts, a.Hkv, D, st);
-        if (r == GDN_OK)
-            r = launch_sum<T>(a, a.part_k + (size_t)a.kparts * a.T * a.Hkv * D, a.dv, 1.f, a.kparts, a.Hkv, D, st);
+        add(a.part_k, a.dk, a.scale, a.kparts, a.Hkv);
+        add(a.part_k + (size_t)a.kparts * a.T * a.Hkv * D, a.dv, 1.f, a.kparts, a.Hkv);
     }
-    if (r == GDN_OK && a.qparts > 1) r = launch_sum<T>(a, a.part_q, a.dq, a.scale, a.qparts, a.Hq, D, st);
-    return r;
+    if (a.qparts > 1) add(a.part_q, a.dq, a.scale, a.qparts, a.Hq);
+    if (n)
+        GDN_LAUNCH("attn_sum", attn_sum_kernel<T>, dim3((unsigned)((most / 4 + 255) / 256), n), dim3(256), st, a.cu, a.B, m);
+    return GDN_OK;
 }
 
 // How the work of a block is cut up: until there are `want` workgroups, but
-// pieces of two tiles at least (on average: `tiles` are those of a middle block).
-int parts_for(long long blocks, long long want, long long tiles, int most)
+// pieces of `least` tiles at least (on average: `tiles` are those of a middle block).
+int parts_for(long long blocks, long long want, long long tiles, long long least, int most)
 {
     long long p = want / blocks;
-    p = p > tiles / 2 ? tiles / 2 : p;
+    p = p > tiles / least ? tiles / least : p;
     return p < 1 ? 1 : p > most ? most : (int)p;
 }
 
 struct BwdPlan {
     int kparts, qparts;
-    size_t o_delta, o_delta2, o_k, o_q, bytes;
+    size_t o_delta, o_k, o_q, bytes;
 };
 
 BwdPlan bwd_plan(const gdn_attn_shape& s)
@@ -409,13 +388,14 @@ BwdPlan bwd_plan(const gdn_attn_shape& s)
     const int kt = s.dtype == GDN_BF16 ? 64 : 32;
     // a key block's work falls with its place in the sequence, so the first
     // blocks decide the end unless there are several workgroups a compute unit
-    p.kparts = parts_for((kb > s.B ? kb : s.B) * s.Hkv, 1024, G * (len / 2 + 32) / 32, 16);
-    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / 2 + kt) / kt, 16);
+    // (fp32, whose tiles take eight times as long, goes down to one tile a piece)
+    const int least = s.dtype == GDN_BF16 ? 2 : 1;
+    p.kparts = parts_for((kb > s.B ? kb : s.B) * s.Hkv, 1024, G * (len / 2 + 32) / 32, least, 16);
+    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / 2 + kt) / kt, least, 16);
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t f = sizeof(float), rows = (size_t)s.T * s.Hq;
     p.o_delta = up(rows * f);
-    p.o_delta2 = p.o_delta + up(rows * f);
-    p.o_k = p.o_delta2 + up(rows * f);
+    p.o_k = p.o_delta + up(rows * f);
     p.o_q = p.o_k + (p.kparts > 1 ? up(2 * p.kparts * (size_t)s.T * s.Hkv * s.D * f) : 0);
     p.bytes = p.o_q + (p.qparts > 1 ? up(p.qparts * rows * s.D * f) : 0);
     return p;
@@ -436,7 +416,6 @@ gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const 
     a.lse2 = (float*)ws;
     const BwdPlan p = bwd_plan(s);
     a.delta = (float*)((char*)ws + p.o_delta);
-    a.delta2 = (float*)((char*)ws + p.o_delta2);
     a.part_k = (float*)((char*)ws + p.o_k);
     a.part_q = (float*)((char*)ws + p.o_q);
     a.kparts = p.kparts;

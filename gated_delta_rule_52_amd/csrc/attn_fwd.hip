@@ -193,9 +193,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
     const int hk = blockIdx.x % a.Hkv;
     const int rest = blockIdx.x / a.Hkv, split = rest % a.splits;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, a.G, 128, rest / a.splits, s)) return;
-    const int R = s.n * a.G, nblk = (R + 127) / 128;
-    const int row0 = (nblk - 1 - s.blk) * 128;  // the longest rows first
+    if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 128, rest / a.splits, s)) return;
+    const int R = s.n * a.G, row0 = s.level * 128;
     const Keys<T, D, PAGED, CH> keys(a, s, hk);
     const int pieces = keys.pieces(a);
     if (split >= pieces) return;
@@ -321,9 +320,8 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
     const int hk = blockIdx.x % a.Hkv;
     const int rest = blockIdx.x / a.Hkv, split = rest % a.splits;
     Span s;
-    if (!find_block(a.cu, a.B, a.T, a.G, 32, rest / a.splits, s)) return;
-    const int R = s.n * a.G, nblk = (R + 31) / 32;
-    const int row0 = (nblk - 1 - s.blk) * 32;
+    if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 32, rest / a.splits, s)) return;
+    const int R = s.n * a.G, row0 = s.level * 32;
     const Keys<T, D, PAGED, 16> keys(a, s, hk);
     const int pieces = keys.pieces(a);
     if (split >= pieces) return;
@@ -467,7 +465,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
             for (int d = 32; d; d >>= 1) p = fmaxf(p, __shfl_xor(p, d));
             mx = fmaxf(mx, p);
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int s = q; s < np; s += Q) {
             const float p = a.part_l[s * rows + row];
             // a piece that saw nothing wrote no output: its old contents are read and not used
