@@ -229,6 +229,25 @@ __device__ __forceinline__ void dma4(const void* gptr, const void* lds_wave_base
     warm_line(gptr, lds_wave_base);
 }
 
+// Order of issue within a block of code: the next N LDS reads, the next N matrix
+// instructions.  Left alone the compiler reads an operand into the registers that
+// the last one has just left, and every matrix instruction waits out an LDS
+// latency; the kernels keep four operands ahead.
+template <int N> __device__ __forceinline__ void order_reads() { __builtin_amdgcn_sched_group_barrier(0x100, N, 0); }
+template <int N> __device__ __forceinline__ void order_mma() { __builtin_amdgcn_sched_group_barrier(0x008, N, 0); }
+// N products of one read (R instructions) each, P operands ahead
+template <int N, int R, int P> __device__ __forceinline__ void order_products()
+{
+    constexpr int A = P < N ? P : N;
+    order_reads<A * R>();
+#pragma unroll
+    for (int i = 0; i < N - A; ++i) {
+        order_mma<1>();
+        order_reads<R>();
+    }
+    order_mma<A>();
+}
+
 // x, of which the compiler no longer knows where it comes from
 __device__ __forceinline__ uint32_t opaque(uint32_t x)
 {

@@ -123,6 +123,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
             dp = mma32(Rows<T, D>::along(ot, at, 0, kk), Rows<T, D>::along(vw, at, 0, kk), dp);
+        if (sizeof(T) == 2) {
+            order_products<KK, 1, 4>();
+            order_products<KK, 2, 2>();
+            __builtin_amdgcn_sched_barrier(0);  // the statistics' reads stay behind
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x4 ls = *reinterpret_cast<const f32x4*>(&ld[buf][0][8 * i + 4 * h]);
@@ -153,6 +158,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
                 dk[dt] = mma32(Rows<T, D>::down(qt, 16 * b, 32 * dt), ds, dk[dt]);
             }
         }
+        if (sizeof(T) == 2) order_products<4 * DT, 2, 3>();
     };
     if (i0 < i1) fetch(0);
     for (int it = i0; it < i1; it += 2) {
@@ -255,6 +261,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
             for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(lds[buf][0], 32 * sub, kk), qf[kk], sc);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) dp = mma32(Rows<T, D>::along(lds[buf][1], 32 * sub, kk), df[kk], dp);
+            // bf16: the keys' columns are read now, to arrive under the exponentials
+            constexpr bool AHEAD = sizeof(T) == 2 && !FIRST();
+            Frag<T> kd[2 * DT];
+            if (AHEAD) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+                        kd[b * DT + dt] = Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt);
+            }
+            if (sizeof(T) == 2) {
+                order_products<2 * KK, 1, 4>();
+                if (AHEAD) order_reads<4 * DT>();
+            }
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = exp2_hw(sc[r] * sl2 - lse2) * (dp[r] - delta);
             if (key0 + 32 > wmin) {
@@ -272,7 +292,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
                     const Frag<T> ds = acc_frag<T>(dp, b);
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt)
-                        dq[dt] = mma32(Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt), ds, dq[dt]);
+                        dq[dt] = mma32(AHEAD ? kd[b * DT + dt] : Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt),
+                                       ds, dq[dt]);
                 }
             }
         }
@@ -391,7 +412,7 @@ BwdPlan bwd_plan(const gdn_attn_shape& s)
     // (fp32, whose tiles take eight times as long, goes down to one tile a piece)
     const int least = s.dtype == GDN_BF16 ? 2 : 1;
     p.kparts = parts_for((kb > s.B ? kb : s.B) * s.Hkv, 1024, G * (len / 2 + 32) / 32, least, 16);
-    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / 2 + kt) / kt, least, 16);
+    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / least + kt) / kt, least, 16);
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t f = sizeof(float), rows = (size_t)s.T * s.Hq;
     p.o_delta = up(rows * f);

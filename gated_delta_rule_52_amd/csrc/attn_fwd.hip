@@ -23,7 +23,10 @@ struct FwdArgs {
     uint32_t k_bytes, v_bytes;    // bytes between tokens of k and v (slots of the cache)
     int B, T, Hq, Hkv, G;
     int num_pages, page_shift, max_pages;
-    int splits, piece;            // the key axis in pieces of `piece` keys, at most `splits` of them
+    // the key axis is cut into pieces, at most `splits` of them: of `piece` keys, or,
+    // where a wave can read all lengths at once, of such a length that there are
+    // about `want` workgroups
+    int splits, piece, want, block_rows;
     float scale;
     float *part_o, *part_l;
 };
@@ -59,6 +62,17 @@ struct Queries {
         f32x16 s = zero16();
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) s = mma32(Rows<T, D>::along(ktab, r0, kk), q[kk], s);
+        // bf16: the values are read now, to arrive under the exponentials
+        constexpr bool AHEAD = sizeof(T) == 2;
+        Frag<T> v[2 * DT];
+        if (AHEAD) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) v[b * DT + dt] = Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt);
+            order_products<KK, 1, 4>();
+            order_reads<4 * DT>();
+        }
         if (mask) {
             const int left = limit - key0 - 4 * h;
 #pragma unroll
@@ -100,21 +114,51 @@ struct Queries {
         for (int b = 0; b < 2; ++b) {
             const Frag<T> p = acc_frag<T>(s, b);
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) o[dt] = mma32(Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt), p, o[dt]);
+            for (int dt = 0; dt < DT; ++dt)
+                o[dt] = mma32(AHEAD ? v[b * DT + dt] : Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt), p, o[dt]);
         }
     }
 };
-
-__device__ __forceinline__ int pieces_of(const FwdArgs& a, int len)
-{
-    return a.splits > 1 && len > a.piece ? (len + a.piece - 1) / a.piece : 1;
-}
 
 __device__ __forceinline__ int cached_len(const FwdArgs& a, int n)
 {
     const long long cap = (long long)a.max_pages << a.page_shift;
     return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
+
+// Keys a piece, the same in every wave of the call: from the lengths themselves
+// where they fit a wave (64 sequences), for the table's width says little about
+// them; a multiple of 128, at least 1024 keys.
+__device__ __forceinline__ int piece_keys(const FwdArgs& a)
+{
+    if (a.splits <= 1) return 1 << 30;
+    if (a.B > 64) return a.piece;
+    const int l = lane_id();
+    float work = 0.f;
+    int most = 0;
+    if (l < a.B) {
+        int st = a.cu[l], en = a.cu[l + 1];
+        st = st < 0 ? 0 : st > a.T ? a.T : st;
+        en = en < st ? st : en > a.T ? a.T : en;
+        most = en > st ? cached_len(a, a.kv_len[l]) : 0;
+        work = (float)(((long long)(en - st) * a.G + a.block_rows - 1) / a.block_rows) * (float)most;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        work += __shfl_xor(work, d);
+        const int o = __shfl_xor(most, d);
+        most = most > o ? most : o;
+    }
+    const float even = work * (float)a.Hkv / (float)a.want;
+    const int need = (most + a.splits - 1) / a.splits;  // no more pieces than there is room for
+    int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even;
+    keys = keys > need ? keys : need;
+    keys = keys > 1024 ? keys : 1024;
+    return uniform((keys + 127) / 128 * 128);
+}
+
+// pieces of a sequence of len keys
+__device__ __forceinline__ int pieces_of(int len, int piece) { return len > piece ? (len + piece - 1) / piece : 1; }
 
 // The keys of one (sequence, key head): where a run of CH keys lies.
 template <typename T, int D, bool PAGED, int CH>
@@ -156,8 +200,6 @@ struct Keys {
         const int p = pages[(key < len ? key : len - 1) >> a.page_shift];
         return p >= 0 && p < a.num_pages ? p : -1;
     }
-    // pieces of the key axis: one where no split is made
-    __device__ __forceinline__ int pieces(const FwdArgs& a) const { return pieces_of(a, len); }
     // the run from `key` into rows r0 .. r0 + CH - 1 of both tables
     __device__ __forceinline__ void fetch(const FwdArgs& a, int key, int page, void* ktab, void* vtab, int r0) const
     {
@@ -196,7 +238,7 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
     if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 128, rest / a.splits, s)) return;
     const int R = s.n * a.G, row0 = s.level * 128;
     const Keys<T, D, PAGED, CH> keys(a, s, hk);
-    const int pieces = keys.pieces(a);
+    const int piece = piece_keys(a), pieces = pieces_of(keys.len, piece);
     if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
@@ -210,8 +252,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
     const int wmin = __builtin_amdgcn_readlane(qs.limit, 0), wmax = __builtin_amdgcn_readlane(qs.limit, 31);
     const int end = row0 + 127 < R ? row0 + 127 : R - 1;
     const int tiles = (keys.seen(end / a.G) + KT - 1) / KT;
-    const int t0 = pieces > 1 ? split * (a.piece / KT) : 0;
-    int t1 = pieces > 1 ? t0 + a.piece / KT : tiles;
+    const int t0 = pieces > 1 ? split * (piece / KT) : 0;
+    int t1 = pieces > 1 ? t0 + piece / KT : tiles;
     t1 = t1 < tiles ? t1 : tiles;
     const float sl2 = a.scale * kLog2e;
 
@@ -323,7 +365,7 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
     if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 32, rest / a.splits, s)) return;
     const int R = s.n * a.G, row0 = s.level * 32;
     const Keys<T, D, PAGED, 16> keys(a, s, hk);
-    const int pieces = keys.pieces(a);
+    const int piece = piece_keys(a), pieces = pieces_of(keys.len, piece);
     if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
@@ -334,8 +376,8 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
     qs.limit = keys.seen(tok);
     const int wmin = __builtin_amdgcn_readlane(qs.limit, 0), upto = __builtin_amdgcn_readlane(qs.limit, 31);
     const int tiles = (upto + 31) / 32;
-    const int t0 = pieces > 1 ? split * (a.piece / 32) : 0;
-    int t1 = pieces > 1 ? t0 + a.piece / 32 : tiles;
+    const int t0 = pieces > 1 ? split * (piece / 32) : 0;
+    int t1 = pieces > 1 ? t0 + piece / 32 : tiles;
     t1 = t1 < tiles ? t1 : tiles;
     const float sl2 = a.scale * kLog2e;
 
@@ -446,6 +488,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
     const int w = uniform(wave_id()), l = lane_id(), q = w % Q;
     const size_t rows = (size_t)a.T * a.Hq;
     const size_t row = (size_t)blockIdx.x * (4 / Q) + w / Q;
+    const int piece = piece_keys(a);
     int np = 1;
     if (row < rows) {
         const int tok = (int)(row / a.Hq);
@@ -454,7 +497,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
             const int e = b0 + l < a.B ? a.cu[b0 + l + 1] : 0x7fffffff;
             b += __popcll(__ballot(e <= tok));
         }
-        if (b < a.B && tok >= a.cu[b]) np = pieces_of(a, cached_len(a, a.kv_len[b]));
+        if (b < a.B && tok >= a.cu[b]) np = pieces_of(cached_len(a, a.kv_len[b]), piece);
     }
     float acc[V] = {}, sum = 0.f;
     if (np > 1) {
@@ -527,8 +570,8 @@ gdn_status launch(const FwdArgs& a, const AttnPlan& p, bool paged, hipStream_t s
 // 32-row blocks where the sequences have, on average, at most 64 rows, and for
 // prompts whose 128-row blocks would leave compute units idle.  The key axis of
 // a cache is cut into pieces of one length where the blocks alone do not fill
-// the card several times: pieces, not shares of each sequence, so that long and
-// short sequences end at the same time.
+// the card: pieces, not shares of each sequence, so that long and short
+// sequences end at the same time.
 AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
 {
     AttnPlan p{};
@@ -540,15 +583,20 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
     p.piece = 1 << 30;
+    p.want = p.small ? 1024 : 384;
     if (paged) {
-        const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B;
-        const long long want = 1024;  // workgroups
-        long long piece = (cap * busy * s.Hkv / want + 127) / 128 * 128;
+        const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B, items = busy * s.Hkv;
+        long long piece = (cap * items / p.want + 127) / 128 * 128;
         piece = piece < 1024 ? 1024 : piece;
-        if (piece < cap) {
-            p.piece = (int)piece;
-            p.splits = (int)((cap + piece - 1) / piece);
+        long long n = (cap + piece - 1) / piece;
+        if (s.B <= 64) {  // the kernel sets the length: room for twice as many where the lengths differ
+            const long long most = (cap + 1023) / 1024;
+            n = 2 * p.want / items;
+            n = n > most ? most : n;
         }
+        p.splits = n < 1 ? 1 : n > 128 ? 128 : (int)n;
+        const long long least = ((cap + p.splits - 1) / p.splits + 127) / 128 * 128;
+        p.piece = (int)(piece > least ? piece : least);
     }
     if (p.splits > 1) p.ws_bytes = (size_t)p.splits * s.T * s.Hq * (s.D + 1) * sizeof(float);
     return p;
@@ -569,7 +617,7 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
     a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
     a.num_pages = s.num_pages; a.max_pages = s.max_pages;
     a.page_shift = paged ? __builtin_ctz((unsigned)s.page_size) : 0;
-    a.splits = p.splits; a.piece = p.piece;
+    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.block_rows = p.rows;
     a.scale = s.scale;
     a.part_o = (float*)ws;
     a.part_l = (float*)ws + (size_t)p.splits * s.T * s.Hq * s.D;
