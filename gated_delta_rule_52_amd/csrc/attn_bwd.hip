@@ -412,7 +412,7 @@ BwdPlan bwd_plan(const gdn_attn_shape& s)
     // (fp32, whose tiles take eight times as long, goes down to one tile a piece)
     const int least = s.dtype == GDN_BF16 ? 2 : 1;
     p.kparts = parts_for((kb > s.B ? kb : s.B) * s.Hkv, 1024, G * (len / 2 + 32) / 32, least, 16);
-    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / least + kt) / kt, least, 16);
+    p.qparts = parts_for((qb > s.B ? qb : s.B) * s.Hkv, 512, (len / 2 + kt) / kt, least, 16);
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t f = sizeof(float), rows = (size_t)s.T * s.Hq;
     p.o_delta = up(rows * f);

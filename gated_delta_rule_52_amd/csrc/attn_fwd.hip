@@ -25,8 +25,8 @@ struct FwdArgs {
     int num_pages, page_shift, max_pages;
     // the key axis is cut into pieces, at most `splits` of them: of `piece` keys, or,
     // where a wave can read all lengths at once, of such a length that there are
-    // about `want` workgroups
-    int splits, piece, want, block_rows;
+    // about `want` workgroups (for blocks of `block_rows` rows)
+    int splits, piece, want, least, block_rows;
     float scale;
     float *part_o, *part_l;
 };
@@ -126,39 +126,86 @@ __device__ __forceinline__ int cached_len(const FwdArgs& a, int n)
     return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
 
-// Keys a piece, the same in every wave of the call: from the lengths themselves
-// where they fit a wave (64 sequences), for the table's width says little about
-// them; a multiple of 128, at least 1024 keys.
-__device__ __forceinline__ int piece_keys(const FwdArgs& a)
-{
-    if (a.splits <= 1) return 1 << 30;
-    if (a.B > 64) return a.piece;
-    const int l = lane_id();
-    float work = 0.f;
-    int most = 0;
-    if (l < a.B) {
-        int st = a.cu[l], en = a.cu[l + 1];
-        st = st < 0 ? 0 : st > a.T ? a.T : st;
-        en = en < st ? st : en > a.T ? a.T : en;
-        most = en > st ? cached_len(a, a.kv_len[l]) : 0;
-        work = (float)(((long long)(en - st) * a.G + a.block_rows - 1) / a.block_rows) * (float)most;
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        work += __shfl_xor(work, d);
-        const int o = __shfl_xor(most, d);
-        most = most > o ? most : o;
-    }
-    const float even = work * (float)a.Hkv / (float)a.want;
-    const int need = (most + a.splits - 1) / a.splits;  // no more pieces than there is room for
-    int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even;
-    keys = keys > need ? keys : need;
-    keys = keys > 1024 ? keys : 1024;
-    return uniform((keys + 127) / 128 * 128);
-}
-
 // pieces of a sequence of len keys
 __device__ __forceinline__ int pieces_of(int len, int piece) { return len > piece ? (len + piece - 1) / piece : 1; }
+
+// A wave's view of up to 64 sequences, lane b that of sequence b: its rows, its
+// blocks and its keys (0 without new tokens); and the length of a piece, the
+// same in every wave of the call: the keys of all blocks over the workgroups
+// wanted, for the table's width says little about the lengths (8 sequences of
+// 8192 keys in a table for 131072, 64 new tokens each, 16 heads over 2: 64 us,
+// against 429 us with pieces from the table's width; one token each for 16 of
+// them: 30 us, against 83 us).  A multiple of 128, at least `least` keys, and
+// no more pieces than there is room for.
+struct View {
+    int st, en, nb, len, piece;
+    __device__ __forceinline__ View(const FwdArgs& a)
+    {
+        const int l = lane_id(), b = l < a.B ? l : a.B - 1;
+        st = a.cu[b], en = a.cu[b + 1], len = a.kv_len[b];
+        st = st < 0 ? 0 : st > a.T ? a.T : st;
+        en = en < st ? st : en > a.T ? a.T : en;
+        if (l >= a.B) en = st;
+        nb = (int)(((long long)(en - st) * a.G + a.block_rows - 1) / a.block_rows);
+        len = en > st ? cached_len(a, len) : 0;
+        float work = (float)nb * (float)len;
+        int most = len;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            work += __shfl_xor(work, d);
+            const int o = __shfl_xor(most, d);
+            most = most > o ? most : o;
+        }
+        const float even = work * (float)a.Hkv / (float)a.want;
+        const int need = (most + a.splits - 1) / a.splits;
+        int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even + 1;
+        keys = keys > need ? keys : need;
+        keys = keys > a.least ? keys : a.least;
+        piece = uniform((keys + 127) / 128 * 128);
+    }
+};
+
+// What a workgroup does: block `s`, and of its sequence's `pieces` pieces of
+// `piece` keys the `split`-th.  False: nothing.
+struct Job {
+    Span s;
+    int split, pieces, piece;
+    template <bool PAGED, int BR>
+    __device__ __forceinline__ bool find(const FwdArgs& a, int id)
+    {
+        split = 0, pieces = 1, piece = 1 << 30;
+        if (!PAGED || a.splits <= 1) return find_block<!PAGED>(a.cu, a.B, a.T, a.G, BR, id, s);
+        if (a.B > 64) {
+            split = id % a.splits;
+            if (!find_block<false>(a.cu, a.B, a.T, a.G, BR, id / a.splits, s)) return false;
+            piece = a.piece;
+            pieces = pieces_of(cached_len(a, uniform(a.kv_len[s.b])), piece);
+            return split < pieces;
+        }
+        // every (block, piece) there is, one after the other: nobody starts for nothing but at the end
+        const View v(a);
+        const int l = lane_id(), np = pieces_of(v.len, v.piece), n = v.nb * np;
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(inc, d);
+            if (l >= d) inc += up;
+        }
+        const uint64_t hit = __ballot(inc > id);
+        if (!hit) return false;
+        const int b = __builtin_ctzll(hit);
+        const int at = id - __builtin_amdgcn_readlane(inc - n, b);
+        piece = v.piece;
+        pieces = __builtin_amdgcn_readlane(np, b);
+        s.b = b;
+        s.start = __builtin_amdgcn_readlane(v.st, b);
+        s.n = __builtin_amdgcn_readlane(v.en, b) - s.start;
+        s.blocks = __builtin_amdgcn_readlane(v.nb, b);
+        split = at / s.blocks;  // blocks that read the same keys together
+        s.level = s.blocks - 1 - at % s.blocks;
+        return true;
+    }
+};
 
 // The keys of one (sequence, key head): where a run of CH keys lies.
 template <typename T, int D, bool PAGED, int CH>
@@ -233,13 +280,12 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
     __shared__ __align__(1024) char lds[2][2][TAB];
 
     const int hk = blockIdx.x % a.Hkv;
-    const int rest = blockIdx.x / a.Hkv, split = rest % a.splits;
-    Span s;
-    if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 128, rest / a.splits, s)) return;
+    Job job;
+    if (!job.find<PAGED, 128>(a, blockIdx.x / a.Hkv)) return;
+    const Span& s = job.s;
+    const int split = job.split, pieces = job.pieces, piece = job.piece;
     const int R = s.n * a.G, row0 = s.level * 128;
     const Keys<T, D, PAGED, CH> keys(a, s, hk);
-    const int piece = piece_keys(a), pieces = pieces_of(keys.len, piece);
-    if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
     const int row = row0 + 32 * w + (l & 31);
@@ -360,13 +406,12 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
     __shared__ __align__(1024) char lds[C::LDS];
 
     const int hk = blockIdx.x % a.Hkv;
-    const int rest = blockIdx.x / a.Hkv, split = rest % a.splits;
-    Span s;
-    if (!find_block<!PAGED>(a.cu, a.B, a.T, a.G, 32, rest / a.splits, s)) return;
+    Job job;
+    if (!job.find<PAGED, 32>(a, blockIdx.x / a.Hkv)) return;
+    const Span& s = job.s;
+    const int split = job.split, pieces = job.pieces, piece = job.piece;
     const int R = s.n * a.G, row0 = s.level * 32;
     const Keys<T, D, PAGED, 16> keys(a, s, hk);
-    const int piece = piece_keys(a), pieces = pieces_of(keys.len, piece);
-    if (split >= pieces) return;
     const int w = uniform(wave_id()), l = lane_id(), h = l >> 5;
 
     const int row = row0 + (l & 31);
@@ -488,16 +533,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
     const int w = uniform(wave_id()), l = lane_id(), q = w % Q;
     const size_t rows = (size_t)a.T * a.Hq;
     const size_t row = (size_t)blockIdx.x * (4 / Q) + w / Q;
-    const int piece = piece_keys(a);
     int np = 1;
     if (row < rows) {
         const int tok = (int)(row / a.Hq);
-        int b = 0;  // sequences that end at or before the token
-        for (int b0 = 0; b0 < a.B; b0 += 64) {
-            const int e = b0 + l < a.B ? a.cu[b0 + l + 1] : 0x7fffffff;
-            b += __popcll(__ballot(e <= tok));
+        if (a.B <= 64) {
+            const View v(a);
+            const uint64_t hit = __ballot(tok >= v.st && tok < v.en);
+            if (hit) np = __builtin_amdgcn_readlane(pieces_of(v.len, v.piece), __builtin_ctzll(hit));
+        } else {
+            int b = 0;  // sequences that end at or before the token
+            for (int b0 = 0; b0 < a.B; b0 += 64) {
+                const int e = b0 + l < a.B ? a.cu[b0 + l + 1] : 0x7fffffff;
+                b += __popcll(__ballot(e <= tok));
+            }
+            if (b < a.B && tok >= a.cu[b]) np = pieces_of(cached_len(a, a.kv_len[b]), a.piece);
         }
-        if (b < a.B && tok >= a.cu[b]) np = pieces_of(cached_len(a, a.kv_len[b]), piece);
     }
     float acc[V] = {}, sum = 0.f;
     if (np > 1) {
@@ -545,7 +595,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
 template <typename T, int D>
 gdn_status launch(const FwdArgs& a, const AttnPlan& p, bool paged, hipStream_t st)
 {
-    const dim3 grid((unsigned)((size_t)p.blocks * a.splits * a.Hkv));
+    const dim3 grid((unsigned)(p.jobs * a.Hkv));
     const dim3 threads(p.small ? Small<T, D>::NW * 64 : 256);
     if (p.small && paged)
         GDN_LAUNCH("attn_small_paged", (attn_small_kernel<T, D, true>), grid, threads, st, a);
@@ -583,14 +633,15 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
     p.piece = 1 << 30;
-    p.want = p.small ? 1024 : 384;
+    p.want = p.small ? 512 : 768;
+    p.least = p.small ? 256 : 1024;
     if (paged) {
         const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B, items = busy * s.Hkv;
         long long piece = (cap * items / p.want + 127) / 128 * 128;
         piece = piece < 1024 ? 1024 : piece;
         long long n = (cap + piece - 1) / piece;
         if (s.B <= 64) {  // the kernel sets the length: room for twice as many where the lengths differ
-            const long long most = (cap + 1023) / 1024;
+            const long long most = (cap + p.least - 1) / p.least;
             n = 2 * p.want / items;
             n = n > most ? most : n;
         }
@@ -598,6 +649,11 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
         const long long least = ((cap + p.splits - 1) / p.splits + 127) / 128 * 128;
         p.piece = (int)(piece > least ? piece : least);
     }
+    p.jobs = (long long)p.blocks * p.splits;
+    // Pieces from the lengths: sum of ceil(len / piece) over the blocks, at most
+    // one a block more than the sum of len / piece, which piece holds to want / Hkv.
+    if (p.splits > 1 && s.B <= 64 && p.jobs > p.want / s.Hkv + p.blocks + 2)
+        p.jobs = p.want / s.Hkv + p.blocks + 2;
     if (p.splits > 1) p.ws_bytes = (size_t)p.splits * s.T * s.Hq * (s.D + 1) * sizeof(float);
     return p;
 }
@@ -617,7 +673,7 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
     a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
     a.num_pages = s.num_pages; a.max_pages = s.max_pages;
     a.page_shift = paged ? __builtin_ctz((unsigned)s.page_size) : 0;
-    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.block_rows = p.rows;
+    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.least = p.least; a.block_rows = p.rows;
     a.scale = s.scale;
     a.part_o = (float*)ws;
     a.part_l = (float*)ws + (size_t)p.splits * s.T * s.Hq * s.D;

@@ -86,7 +86,7 @@ gdn_status check_attn(const gdn_attn_shape* sh, AttnCall call, gdn_attn_shape& s
         if (s.T >= (1 << 26)) return GDN_ERR_UNSUPPORTED;
     } else {
         const AttnPlan p = attn_plan(s, call == CALL_PAGED);
-        if ((long long)p.blocks * p.splits * s.Hkv >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
+        if (p.jobs * s.Hkv >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
     }
     return GDN_OK;
 }
