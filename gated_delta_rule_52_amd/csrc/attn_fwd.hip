@@ -26,7 +26,7 @@ struct FwdArgs {
     // the key axis is cut into pieces, at most `splits` of them: of `piece` keys, or,
     // where a wave can read all lengths at once, of such a length that there are
     // about `want` workgroups (for blocks of `block_rows` rows)
-    int splits, piece, want, least, block_rows;
+    int splits, piece, want, block_rows;
     float scale;
     float *part_o, *part_l;
 };
@@ -120,6 +120,8 @@ struct Queries {
     }
 };
 
+constexpr int kLeastPiece = 256;
+
 __device__ __forceinline__ int cached_len(const FwdArgs& a, int n)
 {
     const long long cap = (long long)a.max_pages << a.page_shift;
@@ -135,8 +137,10 @@ __device__ __forceinline__ int pieces_of(int len, int piece) { return len > piec
 // wanted, for the table's width says little about the lengths (8 sequences of
 // 8192 keys in a table for 131072, 64 new tokens each, 16 heads over 2: 64 us,
 // against 429 us with pieces from the table's width; one token each for 16 of
-// them: 30 us, against 83 us).  A multiple of 128, at least `least` keys, and
-// no more pieces than there is room for.
+// them: 30 us, against 83 us).  A multiple of 128 and no more pieces than
+// there is room for; below 1024 keys, where writing and joining the partial
+// outputs begins to count, only as far as one workgroup for each compute unit asks
+// for it.
 struct View {
     int st, en, nb, len, piece;
     __device__ __forceinline__ View(const FwdArgs& a)
@@ -156,11 +160,12 @@ struct View {
             const int o = __shfl_xor(most, d);
             most = most > o ? most : o;
         }
-        const float even = work * (float)a.Hkv / (float)a.want;
+        work *= (float)a.Hkv;
+        const float even = fmaxf(work / (float)a.want, fminf(work * (1.f / 256.f), 1024.f));
         const int need = (most + a.splits - 1) / a.splits;
         int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even + 1;
         keys = keys > need ? keys : need;
-        keys = keys > a.least ? keys : a.least;
+        keys = keys > kLeastPiece ? keys : kLeastPiece;
         piece = uniform((keys + 127) / 128 * 128);
     }
 };
@@ -627,21 +632,20 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     AttnPlan p{};
     const long long G = s.Hq / s.Hkv, rows = (long long)s.T * G;
     const long long big = ((rows + 127) / 128) * s.Hkv;
-    p.small = paged ? rows <= 64LL * s.B : big < 256;
+    p.small = paged ? rows <= 32LL * s.B : big < 256;
     p.rows = p.small ? 32 : 128;
     p.blocks = (int)(rows / p.rows + s.B);
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
     p.piece = 1 << 30;
     p.want = p.small ? 512 : 768;
-    p.least = p.small ? 256 : 1024;
     if (paged) {
         const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B, items = busy * s.Hkv;
         long long piece = (cap * items / p.want + 127) / 128 * 128;
         piece = piece < 1024 ? 1024 : piece;
         long long n = (cap + piece - 1) / piece;
         if (s.B <= 64) {  // the kernel sets the length: room for twice as many where the lengths differ
-            const long long most = (cap + p.least - 1) / p.least;
+            const long long most = (cap + kLeastPiece - 1) / kLeastPiece;
             n = 2 * p.want / items;
             n = n > most ? most : n;
         }
@@ -673,7 +677,7 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
     a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
     a.num_pages = s.num_pages; a.max_pages = s.max_pages;
     a.page_shift = paged ? __builtin_ctz((unsigned)s.page_size) : 0;
-    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.least = p.least; a.block_rows = p.rows;
+    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.block_rows = p.rows;
     a.scale = s.scale;
     a.part_o = (float*)ws;
     a.part_l = (float*)ws + (size_t)p.splits * s.T * s.Hq * s.D;

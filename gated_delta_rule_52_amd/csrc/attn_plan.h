@@ -15,7 +15,7 @@ namespace gdn {
 // keys or as many as make `want` workgroups.
 struct AttnPlan {
     bool small;  // 32-row blocks whose waves share out the keys; else 128-row blocks
-    int rows, blocks, splits, piece, want, least;
+    int rows, blocks, splits, piece, want;
     long long jobs;  // workgroups a key head
     size_t ws_bytes;  // partial outputs [splits][T * Hq][D] and log-sums [splits][T * Hq], fp32
 };
