@@ -92,8 +92,12 @@ def _take(t, name, shape, dtype, device, *, stride=False):
         return 0
     if not stride or not t[0].is_contiguous():
         raise ValueError(f"{name} must be contiguous" + (" within a token" if stride else ""))
-    # one token has no stride of its own
-    return t.stride(0) if shape[0] > 1 else 0
+    if shape[0] < 2:
+        return 0  # one token has no stride of its own
+    step = t.stride(0)
+    if step < t[0].numel():  # an expanded tensor: its tokens are one, and 0 would say dense
+        raise ValueError(f"{name}: its tokens overlap (stride {step})")
+    return step
 
 
 def _opt(t, name, shape, dtype, device):

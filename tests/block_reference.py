@@ -1,5 +1,5 @@
-"""Plain 64-bit forms of the operators around the layer, on the CPU, a sequence
-and a head at a time, and how far a result may be from them.
+"""Plain 64-bit forms of the operators around the layer, on the CPU (or, for the
+long cases, wherever `where` says), a sequence and a head at a time, and how far a result may be from them.
 
 Bounds count roundings.  Storing a value in type t moves it by at most half a
 step, HALF[t] = eps(t) / 2 relative; an operand of a matrix product that is
@@ -8,6 +8,8 @@ the sum of the products' sizes.  fp32 arithmetic adds 2^-24 for every operation
 on the way; `steps32` counts them for a score of d products, its exponential
 (whose argument's absolute error is the score's) and a sum of n terms.
 """
+import contextlib
+
 import numpy as np
 import torch
 
@@ -15,8 +17,23 @@ HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 U32 = 2.0 ** -24
 
 
+_where = "cpu"
+
+
+@contextlib.contextmanager
+def where(device):
+    """Compute the plain forms on `device` inside."""
+    global _where
+    _where = device
+    try:
+        with torch.device(device):
+            yield
+    finally:
+        _where = "cpu"
+
+
 def f64(t):
-    return t.detach().cpu().double()
+    return t.detach().to(_where).double()
 
 
 def norm_block(x, weight, y=None, a=None, eps=1e-6):

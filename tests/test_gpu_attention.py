@@ -75,6 +75,29 @@ def test_prompt(dtype, D, heads, lens):
     assert max(errs.values()) <= 1, errs
 
 
+@pytest.mark.parametrize("dtype,D,heads,lens", [
+    ("bf16", 128, (16, 4), [2100, 700, 1500]), ("bf16", 64, (24, 3), [1111, 2500]), ("f32", 128, (8, 8), [1300, 900])])
+def test_prompt_long(dtype, D, heads, lens):
+    """Enough blocks that the keys of a query block are not cut up (and those of a
+    key block less), and rows of more than 512 keys."""
+    import gated_delta_rule_52_amd as gdn
+    dt, (Hq, Hkv) = DT[dtype], heads
+    cu = cumulate(lens)
+    log(f"long prompts {dtype} D={D} heads={heads} {lens}")
+    q, k, v = qkv(cu[-1], Hq, Hkv, D, dt, True)
+    o, lse = gdn.gdn_attn_forward(q, k, v, ints(cu))
+    dO = rand(cu[-1], Hq, D, dtype=dt, seed=8)
+    got = gdn.gdn_attn_backward(q, k, v, ints(cu), o, lse, dO)
+    torch.cuda.synchronize()
+    with ref.where("cuda"):
+        wo, wl, bo, bl = ref.prompt(q, k, v, cu)
+        errs = {"o": worst(o, wo, bo), "lse": worst(lse, wl, bl)}
+        for (name, (want, bound)), x in zip(ref.prompt_backward(q, k, v, cu, dO).items(), got):
+            errs[name] = worst(x, want, bound)
+    log("  " + " ".join(f"{k}={v:.2f}" for k, v in errs.items()))
+    assert max(errs.values()) <= 1, errs
+
+
 @pytest.mark.parametrize("scale", [0.01, 3.0])
 def test_prompt_scale_and_large_scores(scale):
     """Scores of a hundred and more: the running maximum moves, and nearly all
@@ -169,6 +192,69 @@ def test_paged(dtype, D, heads, page, new, whole):
     want, bound = ref.paged(q[:n], kc, vc, table, cu, whole)
     e = worst(o[:n], want, bound)
     log(f"  o={e:.2f}")
+    assert e <= 1
+
+
+@pytest.mark.parametrize("B", [64, 65, 150])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences(dtype, B):
+    """More sequences than a wave has lanes (and just as many): prompt, append and
+    paged, the key axis in one piece and in several."""
+    import gated_delta_rule_52_amd as gdn
+    dt = DT[dtype]
+    log(f"many sequences {dtype} B={B}")
+    lens = [(7 * b) % 40 for b in range(B)]
+    cu = cumulate(lens)
+    q, k, v = qkv(cu[-1], 4, 2, 64, dt, True)
+    o, lse = gdn.gdn_attn_forward(q, k, v, ints(cu))
+    dO = rand(cu[-1], 4, 64, dtype=dt, seed=4)
+    got = gdn.gdn_attn_backward(q, k, v, ints(cu), o, lse, dO)
+    torch.cuda.synchronize()
+    wo, wl, bo, bl = ref.prompt(q, k, v, cu)
+    errs = {"o": worst(o, wo, bo), "lse": worst(lse, wl, bl)}
+    for (name, (want, bound)), x in zip(ref.prompt_backward(q, k, v, cu, dO).items(), got):
+        errs[name] = worst(x, want, bound)
+    new = [b % 3 for b in range(B)]
+    whole = [n + (37 * b) % 90 for b, n in enumerate(new)]
+    whole[B // 2] += 3000  # one that is cut into pieces
+    cu = cumulate(new)
+    q, k, v = qkv(cu[-1], 2, 1, 64, dt, True)
+    kc, vc, table = make_cache(whole, 16, 1, 64, dt, poison=0.0)
+    wk, wv, wq = ref.append(q, k, v, None, None, cu, whole, table, kc, vc, torch.zeros_like(q))
+    qo = gdn.gdn_attn_append(q, k, v, None, None, ints(cu), ints(whole), table, kc, vc)
+    x = gdn.gdn_attn_paged(qo, kc, vc, table, ints(cu), ints(whole))
+    torch.cuda.synchronize()
+    assert torch.equal(ref.f64(kc), wk) and torch.equal(ref.f64(vc), wv) and torch.equal(ref.f64(qo), wq)
+    want, bound = ref.paged(qo, kc, vc, table, cu, whole)
+    errs["paged"] = worst(x, want, bound)
+    log("  " + " ".join(f"{k}={v:.2f}" for k, v in errs.items()))
+    assert max(errs.values()) <= 1, errs
+
+
+def test_cache_past_32_bits():
+    """Pages whose first byte lies past 2^32 and whose first element past 2^31."""
+    import gated_delta_rule_52_amd as gdn
+    dt, Hkv, D, page, num = torch.bfloat16, 8, 128, 16, 140000
+    kc = torch.empty(num, page, Hkv, D, dtype=dt, device="cuda")
+    vc = torch.empty_like(kc)
+    assert kc[num - 4:].storage_offset() * 2 > 2 ** 32 and kc.numel() > 2 ** 31
+    whole, new = [70, 33], [2, 1]
+    at = [num - 1, 5, num - 3, num - 2, 132000, num - 7, 131500, 7]
+    for i in at:
+        kc[i] = rand(page, Hkv, D, dtype=dt, seed=i)
+        vc[i] = rand(page, Hkv, D, dtype=dt, seed=i + 1)
+    table = ints([at[:5], at[5:] + [-1, -1]])
+    q, k, v = qkv(3, 16, Hkv, D, dt, True)
+    gdn.gdn_attn_append(None, k, v, None, None, ints([0, 2, 3]), ints(whole), table, kc, vc)
+    torch.cuda.synchronize()
+    for t, (b, p) in enumerate(((0, 68), (0, 69), (1, 32))):
+        pg = int(table[b, p // page])
+        assert torch.equal(kc[pg, p % page], k[t]) and torch.equal(vc[pg, p % page], v[t])
+    o = gdn.gdn_attn_paged(q, kc, vc, table, ints([0, 2, 3]), ints(whole))
+    small = ints([[0, 1, 2, 3, 4], [5, 6, 7, -1, -1]])
+    want, bound = ref.paged(q, kc[at], vc[at], small, [0, 2, 3], whole)
+    e = worst(o, want, bound)
+    log(f"past 32 bits: {e:.2f}")
     assert e <= 1
 
 
@@ -406,6 +492,10 @@ def test_refusals():
         gdn.gdn_attn_forward(q[:, :3], k, v, cu)  # 3 query heads over 2
     with pytest.raises(gdn.GdnError):
         gdn.gdn_attn_forward(*qkv(6, 4, 2, 80, dt, False), cu)
+    with pytest.raises(ValueError):
+        gdn.gdn_attn_forward(q[:1].expand(6, 4, 64), k, v, cu)  # one token seen six times
+    with pytest.raises(ValueError):
+        gdn.gdn_norm_gate(q, q[:1].expand(6, 4, 64), torch.ones(64, device="cuda"))
     kc = torch.zeros(4, 16, 2, 64, dtype=dt, device="cuda")
     table, kv = ints([[0, 1]]), ints([6])
     with pytest.raises(ValueError):
