@@ -80,8 +80,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _take(t, name, shape, dtype, device, *, stride=False):
-    """Check a tensor: its shape, type and device, dense (or, with stride, dense
-    within its first index).  Returns the elements between first indices."""
+    """Check a tensor: its shape, type and device, dense (or, with stride, a
+    [T, H, D] that is dense within its tokens).  Returns the elements between
+    tokens, 0 for dense."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != device.index:
@@ -90,12 +91,14 @@ def _take(t, name, shape, dtype, device, *, stride=False):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
-    if not stride or not t[0].is_contiguous():
-        raise ValueError(f"{name} must be contiguous" + (" within a token" if stride else ""))
+    if not stride:
+        raise ValueError(f"{name} must be contiguous")
+    step, row, one = t.stride()  # [T, H, D]
+    if (one != 1 and shape[2] > 1) or (row != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous within a token")
     if shape[0] < 2:
         return 0  # one token has no stride of its own
-    step = t.stride(0)
-    if step < t[0].numel():  # an expanded tensor: its tokens are one, and 0 would say dense
+    if step < shape[1] * shape[2]:  # an expanded tensor: its tokens are one, and 0 would say dense
         raise ValueError(f"{name}: its tokens overlap (stride {step})")
     return step
 
