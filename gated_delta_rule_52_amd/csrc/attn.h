@@ -258,6 +258,50 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x)
 // value of a wave-uniform integer in a scalar register
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// Sum and maximum over the wave, and the sum over the lanes up to and with the
+// lane itself, by DPP moves (a workgroup begins with up to a dozen of these:
+// through the LDS crossbar each kernel took 0.6 us longer).
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_or_zero(int x)
+{
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_sum(int x)
+{
+    x += dpp_or_zero<0xB1, 0xF>(x);   // quad_perm [1,0,3,2]
+    x += dpp_or_zero<0x4E, 0xF>(x);   // quad_perm [2,3,0,1]
+    x += dpp_or_zero<0x141, 0xF>(x);  // row_half_mirror
+    x += dpp_or_zero<0x140, 0xF>(x);  // row_mirror
+    return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) + __builtin_amdgcn_readlane(x, 32) +
+           __builtin_amdgcn_readlane(x, 48);
+}
+__device__ __forceinline__ int wave_max(int x)  // of values >= 0
+{
+    auto up = [](int a, int b) { return a > b ? a : b; };
+    x = up(x, dpp_or_zero<0xB1, 0xF>(x));
+    x = up(x, dpp_or_zero<0x4E, 0xF>(x));
+    x = up(x, dpp_or_zero<0x141, 0xF>(x));
+    x = up(x, dpp_or_zero<0x140, 0xF>(x));
+    return up(up(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+              up(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
+__device__ __forceinline__ float wave_sum(float x)
+{
+    x = lane16_sum(x);
+    const int u = __builtin_bit_cast(int, x);
+    auto at = [u](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, l)); };
+    return (at(0) + at(16)) + (at(32) + at(48));
+}
+__device__ __forceinline__ int wave_scan(int x)
+{
+    x += dpp_or_zero<0x111, 0xF>(x);  // row_shr:1, 2, 4, 8: within the rows of 16
+    x += dpp_or_zero<0x112, 0xF>(x);
+    x += dpp_or_zero<0x114, 0xF>(x);
+    x += dpp_or_zero<0x118, 0xF>(x);
+    x += dpp_or_zero<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+    x += dpp_or_zero<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+    return x;
+}
+
 // ---------------------------------------------------------------------------
 // Packed sequences: sequence b has the rows cu[b] .. cu[b + 1] - 1.  The bounds
 // are device data: they are clamped to 0 <= start <= end <= T, so that no value
@@ -289,11 +333,6 @@ __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, in
         en = en < st ? st : en > T ? T : en;
         return b0 + l < B ? (int)(((long long)(en - st) * G + BR - 1) / BR) : 0;
     };
-    auto wave_sum = [&](int x) {
-#pragma unroll
-        for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-        return uniform(x);
-    };
     auto take = [&](int b0, int lane, int level, int st, int en, int nb) {
         s.b = b0 + lane;
         s.start = __builtin_amdgcn_readlane(st, lane);
@@ -306,13 +345,7 @@ __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, in
         const int nb = bounds(0, st, en);
         if (id >= wave_sum(nb)) return false;
         // the level j with above(j + 1) <= id < above(j), above(j) the number of blocks at level j and higher
-        int lo = 0, hi = nb, past = 0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            const int o = __shfl_xor(hi, d);
-            hi = hi > o ? hi : o;
-        }
-        hi = uniform(hi);
+        int lo = 0, hi = wave_max(nb), past = 0;
         while (hi - lo > 1) {  // above(lo) > id >= above(hi)
             const int mid = (lo + hi) >> 1;
             const int n = wave_sum(nb > mid ? nb - mid : 0);
@@ -331,12 +364,7 @@ __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, in
     int before = 0;
     for (int b0 = 0; b0 < B; b0 += 64) {
         const int nb = bounds(b0, st, en);
-        int inc = nb;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(inc, d);
-            if (l >= d) inc += up;
-        }
+        const int inc = wave_scan(nb);
         const uint64_t hit = __ballot(before + inc > id);
         if (hit) {
             const int first = __builtin_ctzll(hit);

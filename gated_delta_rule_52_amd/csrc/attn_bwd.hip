@@ -391,7 +391,7 @@ gdn_status launch(const BwdArgs& a, hipStream_t st)
 // pieces of `least` tiles at least (on average: `tiles` are those of a middle block).
 int parts_for(long long blocks, long long want, long long tiles, long long least, int most)
 {
-    long long p = want / blocks;
+    long long p = (want + blocks - 1) / blocks;
     p = p > tiles / least ? tiles / least : p;
     return p < 1 ? 1 : p > most ? most : (int)p;
 }

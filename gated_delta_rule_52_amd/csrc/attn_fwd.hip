@@ -152,15 +152,8 @@ struct View {
         if (l >= a.B) en = st;
         nb = (int)(((long long)(en - st) * a.G + a.block_rows - 1) / a.block_rows);
         len = en > st ? cached_len(a, len) : 0;
-        float work = (float)nb * (float)len;
-        int most = len;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            work += __shfl_xor(work, d);
-            const int o = __shfl_xor(most, d);
-            most = most > o ? most : o;
-        }
-        work *= (float)a.Hkv;
+        const float work = wave_sum((float)nb * (float)len) * (float)a.Hkv;
+        const int most = wave_max(len);
         const float even = fmaxf(work / (float)a.want, fminf(work * (1.f / 256.f), 1024.f));
         const int need = (most + a.splits - 1) / a.splits;
         int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even + 1;
@@ -189,13 +182,7 @@ struct Job {
         }
         // every (block, piece) there is, one after the other: nobody starts for nothing but at the end
         const View v(a);
-        const int l = lane_id(), np = pieces_of(v.len, v.piece), n = v.nb * np;
-        int inc = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(inc, d);
-            if (l >= d) inc += up;
-        }
+        const int np = pieces_of(v.len, v.piece), n = v.nb * np, inc = wave_scan(n);
         const uint64_t hit = __ballot(inc > id);
         if (!hit) return false;
         const int b = __builtin_ctzll(hit);
