@@ -103,9 +103,16 @@ def _take(t, name, shape, dtype, device, *, stride=False):
     return step
 
 
-def _opt(t, name, shape, dtype, device):
-    if t is not None:
-        _take(t, name, shape, dtype, device)
+def _alike(device, shape, dtype, names, *tensors):
+    """_take for dense tensors of one shape and type (None ones are left out), in
+    one call: a decoding step's calls are short enough for the host to count."""
+    index = device.index
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or t.shape != shape
+                              or not t.is_contiguous()):
+            for t, name in zip(tensors, names):
+                if t is not None:
+                    _take(t, name, shape, dtype, device)
 
 
 def _run(fn, name, device, *args):
@@ -140,32 +147,26 @@ def _workspace(query, shape, arg, ws, device, name):
 # ---------------------------------------------------------------------------
 # norms
 # ---------------------------------------------------------------------------
-def _rows(x):
-    return x.shape[:-1].numel()
-
-
 def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):
     """h = x + res_scale * y; n = rmsnorm(h) * weight over the last dimension.
     Returns (h, n, rstd); out = (h, n, rstd) takes them (h, rstd may be None: not
     wanted).  Without y, h is x."""
     dt, dev = _dtype(x, "x"), _gpu(x, "x")
-    shape, dtype = x.shape, x.dtype
-    width, lead = shape[-1], shape[:-1]
-    _take(x, "x", shape, dtype, dev)
-    _take(weight, "weight", (width,), torch.float32, dev)
-    _opt(y, "y", shape, dtype, dev)
-    _opt(res_scale, "res_scale", (width,), torch.float32, dev)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    lead, channels = shape[:-1], shape[-1:]
     if res_scale is not None and y is None:
         raise ValueError("res_scale scales y: pass y too")
     if out is None:
         h = torch.empty_like(x) if y is not None else None
-        n, rstd = torch.empty_like(x), torch.empty(lead, dtype=torch.float32, device=dev)
+        n, rstd = torch.empty_like(x), torch.empty(lead, dtype=f32, device=dev)
     else:
         h, n, rstd = out
-        _opt(h, "h", shape, dtype, dev)
-        _take(n, "n", shape, dtype, dev)
-        _opt(rstd, "rstd", lead, torch.float32, dev)
-    sh = GdnNormShape(lead.numel(), 1, width, dt, eps, 0)
+        if n is None:
+            raise ValueError("out: n is required")
+    _alike(dev, shape, dtype, ("x", "y", "h", "n"), x, y, h, n)
+    _alike(dev, channels, f32, ("weight", "res_scale"), weight, res_scale)
+    _alike(dev, lead, f32, ("rstd",), rstd)
+    sh = GdnNormShape(lead.numel(), 1, shape[-1], dt, eps, 0)
     _run(lib().gdn_norm_block, "gdn_norm_block", dev, ctypes.byref(sh), _p(x), _p(y), _p(res_scale), _p(weight), _p(h),
          _p(n), _p(rstd))
     return (x if h is None and y is None else h), n, rstd
@@ -176,31 +177,22 @@ def gdn_norm_block_backward(dn, x, weight, rstd, y=None, res_scale=None, *, dh=N
     (None = zero).  dy and dres_scale are None without y and res_scale; with y
     but no res_scale dy is dx.  out = (dx, dy, dweight, dres_scale)."""
     dt, dev = _dtype(x, "x"), _gpu(x, "x")
-    width = x.shape[-1]
-    for t, name in ((x, "x"), (dn, "dn")):
-        _take(t, name, x.shape, x.dtype, dev)
-    _opt(y, "y", x.shape, x.dtype, dev)
-    _opt(dh, "dh", x.shape, x.dtype, dev)
-    _take(weight, "weight", (width,), torch.float32, dev)
-    _take(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    _opt(res_scale, "res_scale", (width,), torch.float32, dev)
-    if res_scale is not None and y is None:
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    lead, channels, scaled = shape[:-1], shape[-1:], res_scale is not None
+    if scaled and y is None:
         raise ValueError("res_scale scales y: pass y too")
     if out is None:
-        scaled = res_scale is not None
         out = (torch.empty_like(x), torch.empty_like(x) if scaled else None, torch.empty_like(weight),
                torch.empty_like(weight) if scaled else None)
     dx, dy, dw, da = out
-    _take(dx, "dx", x.shape, x.dtype, dev)
-    _take(dw, "dweight", (width,), torch.float32, dev)
-    if res_scale is not None:
-        if dy is None or da is None:
-            raise ValueError("out: dy and dres_scale are required with res_scale")
-        _take(dy, "dy", x.shape, x.dtype, dev)
-        _take(da, "dres_scale", (width,), torch.float32, dev)
-    else:
+    if not scaled:
         dy = da = None
-    sh = GdnNormShape(_rows(x), 1, width, dt, 1e-6, 0)  # the saved rstd holds the forward's eps
+    if dx is None or dw is None or (scaled and (dy is None or da is None)):
+        raise ValueError("out: dx and dweight are required, dy and dres_scale with res_scale")
+    _alike(dev, shape, dtype, ("x", "dn", "y", "dh", "dx", "dy"), x, dn, y, dh, dx, dy)
+    _alike(dev, channels, f32, ("weight", "res_scale", "dweight", "dres_scale"), weight, res_scale, dw, da)
+    _alike(dev, lead, f32, ("rstd",), rstd)
+    sh = GdnNormShape(lead.numel(), 1, shape[-1], dt, 1e-6, 0)  # the saved rstd holds the forward's eps
     L = lib()
     ws, n = _workspace(L.gdn_norm_workspace_bytes, sh, 0, ws, dev, "gdn_norm_workspace_bytes")
     _run(L.gdn_norm_block_backward, "gdn_norm_block_backward", dev, ctypes.byref(sh), _p(dn), _p(dh), _p(x), _p(y),
@@ -209,48 +201,48 @@ def gdn_norm_block_backward(dn, x, weight, rstd, y=None, res_scale=None, *, dh=N
 
 
 def _gate_shape(o, gate, weight, dev, eps):
-    if o.dim() < 3:
-        raise ValueError(f"o must be [..., H, D], got {tuple(o.shape)}")
-    H, D = o.shape[-2:]
-    tokens = o.shape[:-2].numel()
-    _take(o, "o", o.shape, o.dtype, dev)
-    if tuple(gate.shape) != tuple(o.shape):
-        raise ValueError(f"gate must have shape {tuple(o.shape)}, got {tuple(gate.shape)}")
-    if not gate.is_contiguous() and gate.dim() > 3:
+    shape, dtype = o.shape, o.dtype
+    if len(shape) < 3:
+        raise ValueError(f"o must be [..., H, D], got {tuple(shape)}")
+    tokens, (H, D) = shape[:-2].numel(), shape[-2:]
+    if gate.shape != shape:
+        raise ValueError(f"gate must have shape {tuple(shape)}, got {tuple(gate.shape)}")
+    if not gate.is_contiguous() and len(shape) > 3:
         try:
             gate = gate.view(tokens, H, D)
         except RuntimeError:
             raise ValueError("gate must have one token stride") from None
-    stride = _take(gate, "gate", gate.shape, o.dtype, dev, stride=True)
-    _take(weight, "weight", (D,), torch.float32, dev)
+    stride = _take(gate, "gate", gate.shape, dtype, dev, stride=True)
+    _alike(dev, shape[-1:], torch.float32, ("weight",), weight)
     return GdnNormShape(tokens, H, D, _dtype(o, "o"), eps, stride)
 
 
 def gdn_norm_gate(o, gate, weight, *, eps=1e-6, out=None):
     """y = rmsnorm(o) * weight * silu(gate) for o, gate [..., H, D], the norm over
     D.  Returns (y, rstd); out = (y, rstd), rstd None: not wanted."""
-    dev = _gpu(o, "o")
+    dev, shape = _gpu(o, "o"), o.shape
     sh = _gate_shape(o, gate, weight, dev, eps)
     if out is None:
-        y, rstd = torch.empty_like(o), torch.empty(o.shape[:-1], dtype=torch.float32, device=dev)
-    else:
-        y, rstd = out
-        _take(y, "y", o.shape, o.dtype, dev)
-        _opt(rstd, "rstd", o.shape[:-1], torch.float32, dev)
+        out = torch.empty_like(o), torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    y, rstd = out
+    if y is None:
+        raise ValueError("out: y is required")
+    _alike(dev, shape, o.dtype, ("o", "y"), o, y)
+    _alike(dev, shape[:-1], torch.float32, ("rstd",), rstd)
     _run(lib().gdn_norm_gate, "gdn_norm_gate", dev, ctypes.byref(sh), _p(o), _p(gate), _p(weight), _p(y), _p(rstd))
     return y, rstd
 
 
 def gdn_norm_gate_backward(dy, o, gate, weight, rstd, *, out=None, ws=None):
     """Gradients of gdn_norm_gate: (do, dgate, dweight); out takes them."""
-    dev = _gpu(o, "o")
+    dev, shape = _gpu(o, "o"), o.shape
     sh = _gate_shape(o, gate, weight, dev, 1e-6)  # the saved rstd holds the forward's eps
-    _take(dy, "dy", o.shape, o.dtype, dev)
-    _take(rstd, "rstd", o.shape[:-1], torch.float32, dev)
     do, dgate, dw = out if out is not None else (torch.empty_like(o), torch.empty_like(o), torch.empty_like(weight))
-    _take(do, "do", o.shape, o.dtype, dev)
-    _take(dgate, "dgate", o.shape, o.dtype, dev)
-    _take(dw, "dweight", weight.shape, torch.float32, dev)
+    if rstd is None or do is None or dgate is None or dw is None:
+        raise ValueError("rstd, and do, dgate and dweight of out, are required")
+    _alike(dev, shape, o.dtype, ("dy", "o", "do", "dgate"), dy, o, do, dgate)
+    _alike(dev, shape[:-1], torch.float32, ("rstd",), rstd)
+    _alike(dev, shape[-1:], torch.float32, ("dweight",), dw)
     L = lib()
     ws, n = _workspace(L.gdn_norm_workspace_bytes, sh, 1, ws, dev, "gdn_norm_workspace_bytes")
     _run(L.gdn_norm_gate_backward, "gdn_norm_gate_backward", dev, ctypes.byref(sh), _p(dy), _p(o), _p(gate), _p(weight),
@@ -293,8 +285,8 @@ def gdn_attn_forward(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None):
         o = torch.zeros(q.shape, dtype=q.dtype, device=dev)
     if lse is None:
         lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=dev)
-    _take(o, "o", q.shape, q.dtype, dev)
-    _take(lse, "lse", q.shape[:2], torch.float32, dev)
+    _alike(dev, q.shape, q.dtype, ("o",), o)
+    _alike(dev, q.shape[:2], torch.float32, ("lse",), lse)
     _run(lib().gdn_attn_forward, "gdn_attn_forward", dev, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(cu_seqlens), _p(o),
          _p(lse))
     return o, lse
@@ -322,15 +314,15 @@ def gdn_attn_backward(q, k, v, cu_seqlens, o, lse, dO, *, scale=None, out=None, 
 
 
 def _cache(sh, k_cache, v_cache, page_table, kv_len, dtype, dev):
-    if k_cache.dim() != 4 or k_cache.shape[2:] != (sh.Hkv, sh.D):
-        raise ValueError(f"k_cache must be [num_pages, page_size, {sh.Hkv}, {sh.D}], got {tuple(k_cache.shape)}")
-    _take(k_cache, "k_cache", k_cache.shape, dtype, dev)
-    _take(v_cache, "v_cache", k_cache.shape, dtype, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != sh.B:
-        raise ValueError(f"page_table must be [{sh.B}, max_pages], got {tuple(page_table.shape)}")
-    _take(page_table, "page_table", page_table.shape, torch.int32, dev)
+    shape, table = k_cache.shape, page_table.shape
+    if len(shape) != 4 or shape[2:] != (sh.Hkv, sh.D):
+        raise ValueError(f"k_cache must be [num_pages, page_size, {sh.Hkv}, {sh.D}], got {tuple(shape)}")
+    if len(table) != 2 or table[0] != sh.B:
+        raise ValueError(f"page_table must be [{sh.B}, max_pages], got {tuple(table)}")
+    _alike(dev, shape, dtype, ("k_cache", "v_cache"), k_cache, v_cache)
+    _take(page_table, "page_table", table, torch.int32, dev)
     _take(kv_len, "kv_len", (sh.B,), torch.int32, dev)
-    sh.num_pages, sh.page_size, sh.max_pages = k_cache.shape[0], k_cache.shape[1], page_table.shape[1]
+    sh.num_pages, sh.page_size, sh.max_pages = shape[0], shape[1], table[1]
 
 
 def gdn_attn_append(q, k, v, cos, sin, cu_seqlens, kv_len, page_table, k_cache, v_cache, *, q_out=None):
@@ -355,11 +347,11 @@ def gdn_attn_append(q, k, v, cos, sin, cu_seqlens, kv_len, page_table, k_cache, 
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        if cos.dim() != 2:
-            raise ValueError(f"cos must be [max_pos, rot_dim / 2], got {tuple(cos.shape)}")
-        _take(cos, "cos", cos.shape, torch.float32, dev)
-        _take(sin, "sin", cos.shape, torch.float32, dev)
-        sh.max_pos, sh.rot_dim = cos.shape[0], 2 * cos.shape[1]
+        angles = cos.shape
+        if len(angles) != 2:
+            raise ValueError(f"cos must be [max_pos, rot_dim / 2], got {tuple(angles)}")
+        _alike(dev, angles, torch.float32, ("cos", "sin"), cos, sin)
+        sh.max_pos, sh.rot_dim = angles[0], 2 * angles[1]
     _run(lib().gdn_attn_append, "gdn_attn_append", dev, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(cos), _p(sin),
          _p(cu_seqlens), _p(kv_len), _p(page_table), _p(k_cache), _p(v_cache), _p(q_out))
     return q_out
