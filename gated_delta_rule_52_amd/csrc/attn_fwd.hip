@@ -379,9 +379,11 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
 template <typename T, int D>
 struct Small {
     static constexpr int STAGE = 2 * 32 * Rows<T, D>::BYTES;  // keys and values
-    // bf16: 64 KB a workgroup, two of them a compute unit; fp32, bound by its matrix instructions: 128 KB
-    static constexpr int NW = STAGE == 16384 && sizeof(T) == 2 || STAGE > 16384 ? 2 : 4;
+    // bf16: 64 KB a workgroup, two of them a compute unit; fp32, bound by its
+    // matrix instructions, as many waves as fit 128 KB
+    static constexpr int NW = (sizeof(T) == 2 ? 65536 : 131072) / (2 * STAGE);
     static constexpr int NS = 2;
+    static_assert(NW == 2 || NW == 4, "waves");
     static constexpr int OROW = D + 4;  // floats; the pad spreads the rows over the banks
     static constexpr int RING = NW * NS * STAGE;
     static constexpr int JOIN = NW * 32 * OROW * 4 + NW * 32 * 8;
@@ -517,14 +519,15 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
 // Join the pieces of a row: weights 2^(l_s - max).  Q waves share a row's pieces
 // (every Q-th each), and their sums are added in order: the same in every run.
 template <typename T, int D, int Q>
-__global__ __launch_bounds__(256) void attn_join_kernel(FwdArgs a)
+__global__ __launch_bounds__((Q > 4 ? Q : 4) * 64) void attn_join_kernel(FwdArgs a)
 {
     constexpr int V = D / 64;  // values a lane
-    __shared__ float acc_s[4][D];
-    __shared__ float sum_s[4];
+    constexpr int NW = Q > 4 ? Q : 4;
+    __shared__ float acc_s[NW][D];
+    __shared__ float sum_s[NW];
     const int w = uniform(wave_id()), l = lane_id(), q = w % Q;
     const size_t rows = (size_t)a.T * a.Hq;
-    const size_t row = (size_t)blockIdx.x * (4 / Q) + w / Q;
+    const size_t row = (size_t)blockIdx.x * (NW / Q) + w / Q;
     int np = 1;
     if (row < rows) {
         const int tok = (int)(row / a.Hq);
@@ -599,7 +602,9 @@ gdn_status launch(const FwdArgs& a, const AttnPlan& p, bool paged, hipStream_t s
         GDN_LAUNCH("attn_fwd", (attn_fwd_kernel<T, D, false>), grid, threads, st, a);
     if (a.splits > 1) {
         const size_t rows = (size_t)a.T * a.Hq;
-        if (rows <= 1024)
+        if (rows <= 128)
+            GDN_LAUNCH("attn_join", (attn_join_kernel<T, D, 16>), dim3((unsigned)rows), dim3(1024), st, a);
+        else if (rows <= 2048)
             GDN_LAUNCH("attn_join", (attn_join_kernel<T, D, 4>), dim3((unsigned)rows), dim3(256), st, a);
         else
             GDN_LAUNCH("attn_join", (attn_join_kernel<T, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), st, a);

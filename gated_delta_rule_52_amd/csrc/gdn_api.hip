@@ -117,7 +117,7 @@ const char* gdn_status_string(gdn_status s)
     switch (s) {
     case GDN_OK: return "GDN_OK";
     case GDN_ERR_INVALID_ARG: return "GDN_ERR_INVALID_ARG: invalid shape, dtype or NULL pointer";
-    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: (chunk, Dk, Dv) not compiled in";
+    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: sizes or options that are not compiled in";
     case GDN_ERR_ALIGNMENT: return "GDN_ERR_ALIGNMENT: a pointer is not 16-byte aligned";
     case GDN_ERR_WORKSPACE: return "GDN_ERR_WORKSPACE: workspace missing or too small";
     case GDN_ERR_HIP: return "GDN_ERR_HIP: a kernel launch failed";

@@ -340,6 +340,10 @@ gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, c
  * scale 0 means D^-0.5.  D in {64, 128}; Hq a multiple of Hkv, at most 1024;
  * T * Hq < 2^27.
  *
+ * Sequences do not touch each other: a non-finite value in one token's rows can
+ * reach results of its own sequence only (there also those of earlier tokens,
+ * which share a tile of keys with it).
+ *
  * gdn_attn_forward: token i of a sequence attends to its tokens 0 .. i.
  * lse = log sum exp(scale q.k) over them (may be NULL; the backward needs it).
  * gdn_attn_backward: dq, dk, dv from dO; ws holds
@@ -370,9 +374,8 @@ gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, c
  * Positions without a page are absent; a token that sees nothing gets zeros.
  * One new token a sequence is decoding.  ws holds
  * gdn_attn_workspace_bytes(shape, GDN_ATTN_PAGED) bytes.  k_stride and
- * v_stride are not used.  Cache slots that no visible position names are not
- * used, whatever they hold; a non-finite key or value of a token can reach
- * outputs of its own sequence only.
+ * v_stride are not used.  Cache slots that no position below kv_len[b] names are
+ * not used, whatever they hold.  Calls that overlap must not share a workspace.
  */
 typedef struct {
     int B, T, Hq, Hkv, D;

@@ -71,6 +71,26 @@ def test_norm_block(dtype, shape, mode):
     assert max(errs.values()) <= 1, errs
 
 
+@pytest.mark.parametrize("shape", [(3, 16384), (600, 10000)])
+def test_norm_block_wide(shape):
+    """The widest rows, more of them than there are workgroups."""
+    import gated_delta_rule_52_amd as gdn
+    W = shape[-1]
+    x, y, dn, dh = (rand(*shape, dtype=torch.bfloat16, seed=i) for i in range(4))
+    w, a = rand(W, std=0.2, mean=1.0, seed=5), rand(W, std=0.3, mean=0.5, seed=6)
+    (h, n, r), grads, b = block_bounds(torch.bfloat16, x, y, a, w, dn, dh)
+    gh, gn, gr = gdn.gdn_norm_block(x, w, y, a)
+    got = gdn.gdn_norm_block_backward(dn, x, w, gr, y, a, dh=dh)
+    torch.cuda.synchronize()
+    errs = {"h": worst(gh, h, b["h"]), "n": worst(gn, n, b["n"]), "rstd": worst(gr, r, b["rstd"])}
+    for name, t, want in zip(("dx", "dy", "dweight", "dres_scale"), got, grads):
+        errs[name] = worst(t, want, b[name])
+    log(f"wide {shape}: " + " ".join(f"{k}={v:.2f}" for k, v in errs.items()))
+    assert max(errs.values()) <= 1, errs
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_norm_block(torch.zeros(1, 16392, dtype=torch.bfloat16, device="cuda"), torch.ones(16392, device="cuda"))
+
+
 def test_norm_block_edges():
     """Rows of zeros, no rows, outputs in place of the inputs, only n."""
     import gated_delta_rule_52_amd as gdn
