@@ -23,10 +23,9 @@ struct FwdArgs {
     uint32_t k_bytes, v_bytes;    // bytes between tokens of k and v (slots of the cache)
     int B, T, Hq, Hkv, G;
     int num_pages, page_shift, max_pages;
-    // the key axis is cut into pieces, at most `splits` of them: of `piece` keys, or,
-    // where a wave can read all lengths at once, of such a length that there are
-    // about `want` workgroups (for blocks of `block_rows` rows)
-    int splits, piece, want, block_rows;
+    // the key axis is cut into pieces, at most `splits` of them, of such a length that
+    // there are about `want` workgroups (for blocks of `block_rows` rows)
+    int splits, want, block_rows;
     float scale;
     float *part_o, *part_l;
 };
@@ -131,40 +130,52 @@ __device__ __forceinline__ int cached_len(const FwdArgs& a, int n)
 // pieces of a sequence of len keys
 __device__ __forceinline__ int pieces_of(int len, int piece) { return len > piece ? (len + piece - 1) / piece : 1; }
 
-// A wave's view of up to 64 sequences, lane b that of sequence b: its rows, its
-// blocks and its keys (0 without new tokens); and the length of a piece, the
-// same in every wave of the call: the keys of all blocks over the workgroups
-// wanted, for the table's width says little about the lengths (8 sequences of
-// 8192 keys in a table for 131072, 64 new tokens each, 16 heads over 2: 64 us,
-// against 429 us with pieces from the table's width; one token each for 16 of
-// them: 30 us, against 83 us).  A multiple of 128 and no more pieces than
-// there is room for; below 1024 keys, where writing and joining the partial
-// outputs begins to count, only as far as one workgroup for each compute unit asks
-// for it.
-struct View {
-    int st, en, nb, len, piece;
-    __device__ __forceinline__ View(const FwdArgs& a)
+// 64 sequences from b0 on, lane l that of sequence b0 + l: its rows, its blocks
+// and its keys (0 without new tokens).
+struct Lengths {
+    int st, en, nb, len;
+    __device__ __forceinline__ Lengths(const FwdArgs& a, int b0)
     {
-        const int l = lane_id(), b = l < a.B ? l : a.B - 1;
+        const int l = lane_id(), b = b0 + l < a.B ? b0 + l : a.B - 1;
         st = a.cu[b], en = a.cu[b + 1], len = a.kv_len[b];
         st = st < 0 ? 0 : st > a.T ? a.T : st;
         en = en < st ? st : en > a.T ? a.T : en;
-        if (l >= a.B) en = st;
+        if (b0 + l >= a.B) en = st;
         nb = (int)(((long long)(en - st) * a.G + a.block_rows - 1) / a.block_rows);
         len = en > st ? cached_len(a, len) : 0;
-        const float work = wave_sum((float)nb * (float)len) * (float)a.Hkv;
-        const int most = wave_max(len);
-        const float even = fmaxf(work / (float)a.want, fminf(work * (1.f / 256.f), 1024.f));
-        const int need = (most + a.splits - 1) / a.splits;
-        int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even + 1;
-        keys = keys > need ? keys : need;
-        keys = keys > kLeastPiece ? keys : kLeastPiece;
-        piece = uniform((keys + 127) / 128 * 128);
     }
 };
 
-// What a workgroup does: block `s`, and of its sequence's `pieces` pieces of
-// `piece` keys the `split`-th.  False: nothing.
+// Keys a piece, the same in every wave of the call: the keys of all blocks over
+// the workgroups wanted, for the table's width says little about the lengths (8
+// sequences of 8192 keys in a table for 131072, 64 new tokens each, 16 heads over
+// 2: 64 us, against 429 us with pieces from the table's width; one token each
+// for 16 of them: 30 us, against 83 us).  A multiple of 128 and no more pieces
+// than there is room for; below 1024 keys, where writing and joining the partial
+// outputs begins to count, only as far as one workgroup for each compute unit
+// asks for it.
+__device__ __forceinline__ int piece_keys(const FwdArgs& a, const Lengths& first)
+{
+    float work = wave_sum((float)first.nb * (float)first.len);
+    int most = wave_max(first.len);
+    for (int b0 = 64; b0 < a.B; b0 += 64) {
+        const Lengths v(a, b0);
+        work += wave_sum((float)v.nb * (float)v.len);
+        const int m = wave_max(v.len);
+        most = most > m ? most : m;
+    }
+    work *= (float)a.Hkv;
+    const float even = fmaxf(work / (float)a.want, fminf(work * (1.f / 256.f), 1024.f));
+    const int need = (most + a.splits - 1) / a.splits;
+    int keys = even > (float)(1 << 29) ? 1 << 29 : (int)even + 1;
+    keys = keys > need ? keys : need;
+    keys = keys > kLeastPiece ? keys : kLeastPiece;
+    return uniform((keys + 127) / 128 * 128);
+}
+
+// What a workgroup does: block `s`, and of its sequence's `pieces` pieces, of
+// `piece` keys each (the sequence's own share, so that its last piece is no
+// remnant), the `split`-th.  False: nothing.
 struct Job {
     Span s;
     int split, pieces, piece;
@@ -173,29 +184,30 @@ struct Job {
     {
         split = 0, pieces = 1, piece = 1 << 30;
         if (!PAGED || a.splits <= 1) return find_block<!PAGED>(a.cu, a.B, a.T, a.G, BR, id, s);
-        if (a.B > 64) {
-            split = id % a.splits;
-            if (!find_block<false>(a.cu, a.B, a.T, a.G, BR, id / a.splits, s)) return false;
-            piece = a.piece;
-            pieces = pieces_of(cached_len(a, uniform(a.kv_len[s.b])), piece);
-            return split < pieces;
-        }
         // every (block, piece) there is, one after the other: nobody starts for nothing but at the end
-        const View v(a);
-        const int np = pieces_of(v.len, v.piece), n = v.nb * np, inc = wave_scan(n);
-        const uint64_t hit = __ballot(inc > id);
-        if (!hit) return false;
-        const int b = __builtin_ctzll(hit);
-        const int at = id - __builtin_amdgcn_readlane(inc - n, b);
-        piece = v.piece;
-        pieces = __builtin_amdgcn_readlane(np, b);
-        s.b = b;
-        s.start = __builtin_amdgcn_readlane(v.st, b);
-        s.n = __builtin_amdgcn_readlane(v.en, b) - s.start;
-        s.blocks = __builtin_amdgcn_readlane(v.nb, b);
-        split = at / s.blocks;  // blocks that read the same keys together
-        s.level = s.blocks - 1 - at % s.blocks;
-        return true;
+        Lengths v(a, 0);
+        const int most = piece_keys(a, v);
+        for (int b0 = 0, before = 0;;) {
+            const int np = pieces_of(v.len, most), n = v.nb * np, inc = wave_scan(n);
+            const uint64_t hit = __ballot(before + inc > id);
+            if (hit) {
+                const int b = __builtin_ctzll(hit);
+                const int at = id - before - __builtin_amdgcn_readlane(inc - n, b);
+                pieces = __builtin_amdgcn_readlane(np, b);
+                s.b = b0 + b;
+                s.start = __builtin_amdgcn_readlane(v.st, b);
+                s.n = __builtin_amdgcn_readlane(v.en, b) - s.start;
+                s.blocks = __builtin_amdgcn_readlane(v.nb, b);
+                split = at / s.blocks;  // blocks that read the same keys together
+                s.level = s.blocks - 1 - at % s.blocks;
+                piece = ((__builtin_amdgcn_readlane(v.len, b) + pieces - 1) / pieces + 127) / 128 * 128;
+                return true;
+            }
+            before += __builtin_amdgcn_readlane(inc, 63);
+            b0 += 64;
+            if (b0 >= a.B) return false;
+            v = Lengths(a, b0);
+        }
     }
 };
 
@@ -531,17 +543,17 @@ __global__ __launch_bounds__((Q > 4 ? Q : 4) * 64) void attn_join_kernel(FwdArgs
     int np = 1;
     if (row < rows) {
         const int tok = (int)(row / a.Hq);
-        if (a.B <= 64) {
-            const View v(a);
+        Lengths v(a, 0);
+        const int most = piece_keys(a, v);
+        for (int b0 = 0;;) {
             const uint64_t hit = __ballot(tok >= v.st && tok < v.en);
-            if (hit) np = __builtin_amdgcn_readlane(pieces_of(v.len, v.piece), __builtin_ctzll(hit));
-        } else {
-            int b = 0;  // sequences that end at or before the token
-            for (int b0 = 0; b0 < a.B; b0 += 64) {
-                const int e = b0 + l < a.B ? a.cu[b0 + l + 1] : 0x7fffffff;
-                b += __popcll(__ballot(e <= tok));
+            if (hit) {
+                np = __builtin_amdgcn_readlane(pieces_of(v.len, most), __builtin_ctzll(hit));
+                break;
             }
-            if (b < a.B && tok >= a.cu[b]) np = pieces_of(cached_len(a, a.kv_len[b]), a.piece);
+            b0 += 64;
+            if (b0 >= a.B) break;
+            v = Lengths(a, b0);
         }
     }
     float acc[V] = {}, sum = 0.f;
@@ -629,27 +641,20 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     p.blocks = (int)(rows / p.rows + s.B);
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
-    p.piece = 1 << 30;
     p.want = p.small ? 512 : 768;
     if (paged) {
         const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B, items = busy * s.Hkv;
-        long long piece = (cap * items / p.want + 127) / 128 * 128;
-        piece = piece < 1024 ? 1024 : piece;
-        long long n = (cap + piece - 1) / piece;
-        if (s.B <= 64) {  // the kernel sets the length: room for twice as many where the lengths differ
-            const long long most = (cap + kLeastPiece - 1) / kLeastPiece;
-            n = 2 * p.want / items;
-            n = n > most ? most : n;
-        }
+        // room for twice the pieces that equal lengths would make
+        const long long most = (cap + kLeastPiece - 1) / kLeastPiece;
+        long long n = 2 * p.want / items;
+        n = n > most ? most : n;
         p.splits = n < 1 ? 1 : n > 128 ? 128 : (int)n;
-        const long long least = ((cap + p.splits - 1) / p.splits + 127) / 128 * 128;
-        p.piece = (int)(piece > least ? piece : least);
     }
     p.jobs = (long long)p.blocks * p.splits;
-    // Pieces from the lengths: sum of ceil(len / piece) over the blocks, at most
-    // one a block more than the sum of len / piece, which piece holds to want / Hkv.
-    if (p.splits > 1 && s.B <= 64 && p.jobs > p.want / s.Hkv + p.blocks + 2)
-        p.jobs = p.want / s.Hkv + p.blocks + 2;
+    // The sum of ceil(len / piece) over the blocks is at most one a block more than
+    // the sum of len / piece, which a piece's length holds to want / Hkv (or to 256
+    // / Hkv, where it is below 1024).
+    if (p.splits > 1 && p.jobs > p.want / s.Hkv + p.blocks + 2) p.jobs = p.want / s.Hkv + p.blocks + 2;
     if (p.splits > 1) p.ws_bytes = (size_t)p.splits * s.T * s.Hq * (s.D + 1) * sizeof(float);
     return p;
 }
@@ -669,7 +674,7 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
     a.B = s.B; a.T = s.T; a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.Hq / s.Hkv;
     a.num_pages = s.num_pages; a.max_pages = s.max_pages;
     a.page_shift = paged ? __builtin_ctz((unsigned)s.page_size) : 0;
-    a.splits = p.splits; a.piece = p.piece; a.want = p.want; a.block_rows = p.rows;
+    a.splits = p.splits; a.want = p.want; a.block_rows = p.rows;
     a.scale = s.scale;
     a.part_o = (float*)ws;
     a.part_l = (float*)ws + (size_t)p.splits * s.T * s.Hq * s.D;

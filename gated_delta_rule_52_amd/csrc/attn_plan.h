@@ -11,11 +11,11 @@ namespace gdn {
 
 // How a forward call is laid out: blocks of `rows` query rows (a row is one
 // token of one of the query heads that share a key head), `blocks` of them at
-// most for any lengths, and at most `splits` pieces of the key axis, of `piece`
-// keys or as many as make `want` workgroups.
+// most for any lengths, and at most `splits` pieces of the key axis, about as
+// many as make `want` workgroups.
 struct AttnPlan {
     bool small;  // 32-row blocks whose waves share out the keys; else 128-row blocks
-    int rows, blocks, splits, piece, want;
+    int rows, blocks, splits, want;
     long long jobs;  // workgroups a key head
     size_t ws_bytes;  // partial outputs [splits][T * Hq][D] and log-sums [splits][T * Hq], fp32
 };
