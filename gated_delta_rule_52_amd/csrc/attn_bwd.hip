@@ -22,7 +22,9 @@ struct BwdArgs {
     const float* lse;
     const int* cu;
     void *dq, *dk, *dv;
-    float *lse2, *delta;  // [Hq][T]: lse * log2 e and delta, left by the query pass for the key pass
+    // [Hq][T]: lse * log2 e and delta for the key pass, left by the query pass (bf16)
+    // or by attn_delta_kernel (fp32)
+    float *lse2, *delta;
     long long q_stride;
     uint32_t q_bytes, k_bytes, v_bytes, o_bytes;  // bytes between tokens
     int B, T, Hq, Hkv, G;
@@ -42,22 +44,29 @@ __device__ __forceinline__ void put4(T* out, float* part, size_t at, const f32x1
         store4<T>(out + at, v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
 }
 
-// dk, dv of 128 keys: four waves of 32 keys.  The keys stay in registers, the
+// The key pass: dk, dv of 128 keys: four waves of 32 keys.  The keys stay in registers, the
 // values in LDS (with both in registers a wave would need more than the 256 that
 // two waves a SIMD have); tiles of 32 tokens of one query head after the other
 // go through two LDS buffers.
 template <typename T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(BwdArgs a)
+struct KeyLds {
+    static constexpr int QT = 32, TAB = QT * Rows<T, D>::BYTES;
+    char lds[2][2][TAB];  // q, do
+    float ld[2][2][64];   // lse2, delta of a tile (64 lanes' words; QT are read)
+    __align__(1024) char vtab[128 * Rows<T, D>::BYTES];
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>& m)
 {
     constexpr int KK = D / 16, DT = D / 32;
-    constexpr int QT = 32, RW = QT / 4;
-    constexpr int TAB = QT * Rows<T, D>::BYTES;
-    __shared__ __align__(1024) char vtab[128 * Rows<T, D>::BYTES];
-    __shared__ __align__(1024) char lds[2][2][TAB];
-    __shared__ __align__(256) float ld[2][2][64];  // lse2, delta of a tile (64 lanes' words; QT are read)
+    constexpr int QT = KeyLds<T, D>::QT, RW = QT / 4;
+    auto& vtab = m.vtab;
+    auto& lds = m.lds;
+    auto& ld = m.ld;
 
-    const int hk = blockIdx.x % a.Hkv;
-    const int rest = blockIdx.x / a.Hkv, part = rest % a.kparts;
+    const int hk = id % a.Hkv;
+    const int rest = id / a.Hkv, part = rest % a.kparts;
     Span s;
     if (!find_block<true>(a.cu, a.B, a.T, 1, 128, rest / a.kparts, s)) return;
     const int key0 = (s.blocks - 1 - s.level) * 128;  // the first keys have the most queries: they come first
@@ -181,7 +190,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
     }
 }
 
-// dq of 128 rows (token * G + head): four waves of 32 rows; tiles of KT keys go
+// The query pass: dq of 128 rows (token * G + head): four waves of 32 rows; tiles of KT keys go
 // through two LDS buffers.
 //
 // bf16: delta_i = do_i . o_i carries the rounding of the stored o, and an error
@@ -193,16 +202,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(
 // their own dq too.  (Error of dq and dk against 64 bits, in units of
 // the error of storing them: 1.7 and 1.8 at 16 tokens without this, 1.5 with it.)
 template <typename T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdArgs a)
+struct QueryLds {
+    static constexpr int KT = sizeof(T) == 2 ? 64 : 32;
+    char lds[2][2][KT * Rows<T, D>::BYTES];  // k, v
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T, D>& m)
 {
     constexpr int KK = D / 16, DT = D / 32;
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32, RW = KT / 4;
-    constexpr int TAB = KT * Rows<T, D>::BYTES;
+    constexpr int KT = QueryLds<T, D>::KT, RW = KT / 4;
     constexpr int SHORT = 512;
-    __shared__ __align__(1024) char lds[2][2][TAB];
+    auto& lds = m.lds;
 
-    const int hk = blockIdx.x % a.Hkv;
-    const int rest = blockIdx.x / a.Hkv, part = rest % a.qparts;
+    const int hk = id % a.Hkv;
+    const int rest = id / a.Hkv, part = rest % a.qparts;
     Span s;
     if (!find_block<true>(a.cu, a.B, a.T, a.G, 128, rest / a.qparts, s)) return;
     const int R = s.n * a.G, row0 = s.level * 128;
@@ -313,9 +327,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
     }
     const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
     round(t0, t1, std::false_type{});
-    if (part == 0) {
+    if (sizeof(T) == 2 && part == 0) {
         // a piece of the keys does not have the whole row sum
-        if (sizeof(T) == 2 && a.qparts == 1) delta += half_add(over);
+        if (a.qparts == 1) delta += half_add(over);
         if (row < R && h == 0) {
             a.lse2[(size_t)hq * a.T + at] = lse2;
             a.delta[(size_t)hq * a.T + at] = delta;
@@ -328,6 +342,57 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Bw
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) put4<T>((T*)a.dq, pq, out + 32 * dt + 8 * i + 4 * h, dq[dt], i, a.scale);
+    }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(BwdArgs a)
+{
+    __shared__ __align__(1024) QueryLds<T, D> m;
+    query_pass<T, D>(a, blockIdx.x, m);
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, 2) void attn_dkdv_kernel(BwdArgs a)
+{
+    __shared__ __align__(1024) KeyLds<T, D> m;
+    key_pass<T, D>(a, blockIdx.x, m);
+}
+
+// fp32, whose delta needs no correction: both passes in one launch, the first
+// `kblocks` workgroups for the keys.  A small batch (three prompts of up to 333
+// tokens, 6 heads of 64) does not fill the card with either: forward and backward
+// take 47 us, and 55 us in two launches.
+template <int D>
+__global__ __launch_bounds__(256, 1) void attn_grads_kernel(BwdArgs a, unsigned kblocks)
+{
+    __shared__ __align__(1024) union {
+        KeyLds<float, D> k;
+        QueryLds<float, D> q;
+    } m;
+    if (blockIdx.x < kblocks)
+        key_pass<float, D>(a, blockIdx.x, m.k);
+    else
+        query_pass<float, D>(a, blockIdx.x - kblocks, m.q);
+}
+
+// fp32: delta and the log-sums in base 2, by query head; a row by D / 4 lanes
+template <int D>
+__global__ __launch_bounds__(256) void attn_delta_kernel(BwdArgs a)
+{
+    constexpr int L = D / 4;
+    const size_t rows = (size_t)a.T * a.Hq;
+    const size_t row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int c = (threadIdx.x % L) * 4;
+    const size_t at = (row < rows ? row : rows - 1) * D + c;
+    const f32x4 x = *reinterpret_cast<const f32x4*>((const float*)a.o + at);
+    const f32x4 y = *reinterpret_cast<const f32x4*>((const float*)a.dO + at);
+    float sum = lane16_sum((x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]));
+    if (L == 32) sum += __shfl_xor(sum, 16);
+    if (c == 0 && row < rows) {
+        const size_t t = row / a.Hq, h = row % a.Hq;
+        a.delta[h * a.T + t] = sum;
+        a.lse2[h * a.T + t] = a.lse[row] * kLog2e;
     }
 }
 
@@ -364,10 +429,17 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ c
 template <typename T, int D>
 gdn_status launch(const BwdArgs& a, hipStream_t st)
 {
-    const size_t qblocks = (size_t)((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts;
-    GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3((unsigned)qblocks), dim3(256), st, a);
-    const size_t kblocks = (size_t)(a.T / 128 + a.B) * a.Hkv * a.kparts;
-    GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3((unsigned)kblocks), dim3(256), st, a);
+    const unsigned qblocks = (unsigned)(((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts);
+    const unsigned kblocks = (unsigned)((a.T / 128 + a.B) * (long long)a.Hkv * a.kparts);
+    if constexpr (sizeof(T) == 4) {
+        constexpr int RPB = 1024 / D;
+        const size_t rows = (size_t)a.T * a.Hq;
+        GDN_LAUNCH("attn_delta", attn_delta_kernel<D>, dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
+        GDN_LAUNCH("attn_grads", attn_grads_kernel<D>, dim3(kblocks + qblocks), dim3(256), st, a, kblocks);
+    } else {
+        GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3(qblocks), dim3(256), st, a);
+        GDN_LAUNCH("attn_dkdv", (attn_dkdv_kernel<T, D>), dim3(kblocks), dim3(256), st, a);
+    }
     SumArgs m{};
     int n = 0;
     size_t most = 0;

@@ -641,7 +641,7 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     p.blocks = (int)(rows / p.rows + s.B);
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
-    p.want = p.small ? 512 : 768;
+    p.want = p.small ? 512 : 896;
     if (paged) {
         const long long full = (rows + p.rows - 1) / p.rows, busy = full > s.B ? full : s.B, items = busy * s.Hkv;
         // room for twice the pieces that equal lengths would make
