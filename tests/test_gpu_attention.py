@@ -471,6 +471,37 @@ def test_graphs_streams():
     assert torch.equal(o, want)
 
 
+def test_two_streams_at_once():
+    """Two calls under way together, each with its own outputs and workspace, give
+    what each gives alone."""
+    import gated_delta_rule_52_amd as gdn
+    dt, jobs = torch.bfloat16, []
+    for i, lens in enumerate(([900, 300], [50, 700, 450])):
+        cu = cumulate(lens)
+        q, k, v = qkv(cu[-1], 8, 2, 128, dt, True)
+        jobs.append((q, k, v, ints(cu), rand(cu[-1], 8, 128, dtype=dt, seed=i)))
+    kc, vc, table = make_cache([3000, 500], 32, 2, 128, dt)
+    qd, cd, kv = rand(2, 8, 128, dtype=dt), ints([0, 1, 2]), ints([3000, 500])
+
+    def work(job):
+        q, k, v, cu, dO = job
+        o, lse = gdn.gdn_attn_forward(q, k, v, cu)
+        return (o, lse) + gdn.gdn_attn_backward(q, k, v, cu, o, lse, dO) + (
+            gdn.gdn_attn_paged(qd, kc, vc, table, cd, kv),)
+
+    want = [work(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = []
+    for _ in range(3):
+        for j, st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                got.append(work(j))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2])), i
+
+
 def test_refusals():
     import gated_delta_rule_52_amd as gdn
     dt = torch.bfloat16

@@ -145,6 +145,25 @@ def test_norm_gate(dtype, D, tokens, heads, stride):
     assert max(errs.values()) <= 1, errs
 
 
+def test_norm_gate_no_tokens_and_batches():
+    """No tokens: the weight's gradient is zero.  [B, T, H, D] with a gate whose
+    tokens have one stride is taken as it is, with two it is refused."""
+    import gated_delta_rule_52_amd as gdn
+    w = rand(32, mean=1.0)
+    e = torch.zeros(0, 2, 32, device="cuda")
+    y, r = gdn.gdn_norm_gate(e, e, w)
+    do, dz, dw = gdn.gdn_norm_gate_backward(e, e, e, w, r)
+    torch.cuda.synchronize()
+    assert y.shape == e.shape and torch.equal(dw, torch.zeros_like(w))
+    o = rand(3, 5, 2, 32)
+    z = rand(3, 5, 4, 32, seed=1)[:, :, 2:]
+    y, r = gdn.gdn_norm_gate(o, z, w)
+    want, _ = gdn.gdn_norm_gate(o.view(15, 2, 32), z.reshape(15, 2, 32), w)
+    assert torch.equal(y.view(15, 2, 32), want) and r.shape == (3, 5, 2)
+    with pytest.raises(ValueError):
+        gdn.gdn_norm_gate(o, rand(5, 3, 2, 32).transpose(0, 1), w)
+
+
 def test_norm_gate_extreme_gates():
     """Gates far out: silu is 0 below and the gate itself above, with no NaN."""
     import gated_delta_rule_52_amd as gdn
