@@ -293,26 +293,31 @@ __global__ __launch_bounds__(256, N <= 2 ? 4 : N == 3 ? 3 : 2) void norm_block_b
     }
 }
 
-// out[c] = sum over the nb rows of part[.][c]: 16 columns a workgroup, 16 row
-// strips, then the strips in order
-__global__ __launch_bounds__(256) void norm_finish_kernel(const float* __restrict__ part, float* __restrict__ out0,
-                                                          float* __restrict__ out1, int nb, int width)
+// out[c] = sum over the nb rows of part[.][c]: 16 columns a workgroup, 64 row
+// strips (a strip's loads are what it waits for; with 16 the gated norm's training
+// case took 74.6 us instead of 73.4), then the strips in order
+__global__ __launch_bounds__(1024) void norm_finish_kernel(const float* __restrict__ part, float* __restrict__ out0,
+                                                           float* __restrict__ out1, int nb, int width)
 {
-    __shared__ float tot[16][17];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), strip = threadIdx.x >> 4;
+    __shared__ float tot[64][17];
+    const int i = threadIdx.x & 15, c = blockIdx.x * 16 + i, strip = threadIdx.x >> 4;
     const float* p = part + (size_t)blockIdx.y * nb * width;
     float s = 0.f;
     if (c < width) {
 #pragma unroll 8
-        for (int r = strip; r < nb; r += 16) s += p[(size_t)r * width + c];
+        for (int r = strip; r < nb; r += 64) s += p[(size_t)r * width + c];
     }
-    tot[strip][threadIdx.x & 15] = s;
+    tot[strip][i] = s;
     __syncthreads();
-    if (strip == 0 && c < width) {
+    if (strip < 4) {
+        s = 0.f;
 #pragma unroll
-        for (int q = 1; q < 16; ++q) s += tot[q][threadIdx.x];
-        (blockIdx.y ? out1 : out0)[c] = s;
+        for (int q = 0; q < 16; ++q) s += tot[16 * strip + q][i];
     }
+    __syncthreads();
+    if (strip < 4) tot[strip][i] = s;
+    __syncthreads();
+    if (strip == 0 && c < width) (blockIdx.y ? out1 : out0)[c] = (tot[0][i] + tot[1][i]) + (tot[2][i] + tot[3][i]);
 }
 
 // ---------------------------------------------------------------------------
@@ -486,7 +491,7 @@ gdn_status block_bwd(const gdn_norm_shape& s, const void* dn, const void* dh, co
         return GDN_OK;
     });
     if (r != GDN_OK) return r;
-    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), a ? 2 : 1), dim3(256), st, part, dw, da,
+    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), a ? 2 : 1), dim3(1024), st, part, dw, da,
                nb, s.width);
     return GDN_OK;
 }
@@ -517,7 +522,7 @@ gdn_status gate_bwd(const gdn_norm_shape& s, const void* dy, const void* o, cons
         return GDN_OK;
     });
     if (r != GDN_OK) return r;
-    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), 1), dim3(256), st, part, dw,
+    GDN_LAUNCH("norm_finish", norm_finish_kernel, dim3(ceil_div(s.width, 16), 1), dim3(1024), st, part, dw,
                (float*)nullptr, nb, s.width);
     return GDN_OK;
 }
