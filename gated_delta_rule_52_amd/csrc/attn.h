@@ -103,9 +103,7 @@ __device__ __forceinline__ float half_add(float x)
     return p.x + p.y;
 }
 
-// dma16 (common.h) from a wave-uniform base plus a 32-bit byte offset a lane.  The
-// wait state between the write of m0 and the load that reads it is the
-// instruction set's rule for loads to LDS, which the compiler does not see here.
+// dma16 (common.h) from a wave-uniform base plus a 32-bit byte offset a lane
 __device__ __forceinline__ void dma16_at(const void* base, uint32_t off, const void* lds_wave_base)
 {
     const uint32_t m0v = __builtin_amdgcn_readfirstlane(
@@ -226,12 +224,10 @@ struct Rows {
     }
 };
 
-// the same for 4 bytes a lane: lane i's word lands at lds_wave_base + 4 i
+// 4-byte direct load into LDS: lane i's word lands at lds_wave_base + 4 i
 __device__ __forceinline__ void dma4(const void* gptr, const void* lds_wave_base)
 {
-    const uint32_t m0v = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds_wave_base);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0v), "v"(gptr) : "memory", "m0");
+    warm_line(gptr, lds_wave_base);
 }
 
 // Order of issue within a block of code: the next N LDS reads, the next N matrix

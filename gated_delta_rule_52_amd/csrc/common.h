@@ -147,11 +147,14 @@ __device__ __forceinline__ uint2 acc_colpairs(f32x4 v)
 // explicit vmcnt and a barrier before reading the words.  The memory clobber
 // keeps the compiler's memory operations on their side of the load, so the
 // number of vector memory operations issued after it is what the code shows.
+// The wait state between the write of m0 and the load that reads it is the
+// instruction set's rule for loads to LDS, which the compiler does not see here.
 __device__ __forceinline__ void dma16(const void* gptr, const void* lds_wave_base)
 {
     const uint32_t m0v = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds_wave_base);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0v), "v"(gptr) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0v), "v"(gptr)
+                 : "memory", "m0");
 }
 
 // Touch the 128-byte line holding gptr so that it is in the L2 when the real
@@ -161,7 +164,8 @@ __device__ __forceinline__ void warm_line(const void* gptr, const void* sink_wav
 {
     const uint32_t m0v = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)sink_wave_base);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0v), "v"(gptr) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0v), "v"(gptr)
+                 : "memory", "m0");
 }
 
 // s_waitcnt with only the vector memory count limited, 0 <= N < 64 (gfx9
