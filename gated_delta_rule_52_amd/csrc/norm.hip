@@ -14,8 +14,8 @@
 // norm unrounded (the backward forms it again from x and y, which it reads
 // anyway for da).  All of these are bound by HBM: each value is read once and
 // written once, as 16-byte words.  Forward and backward together move 503 MB at
-// 4.8 TB/s (block norm, 32768 x 768 bf16, 104 us) and 403 MB at 5.4 TB/s (gated
-// norm, 32768 x 6 x 128 bf16, 75 us); a copy of 256 MB reaches 5.4 TB/s.
+// 4.8 TB/s (block norm, 32768 x 768 bf16, 104 us) and 403 MB at 5.5 TB/s (gated
+// norm, 32768 x 6 x 128 bf16, 73 us); a copy of 256 MB reaches 5.4 TB/s.
 #include "common.h"
 #include "norm.h"
 
@@ -26,7 +26,7 @@ namespace {
 // A word of an output.  PAST: not to be kept in the L2, for outputs that it could
 // not hold until the next kernel anyway (past_l2).  At 32768 x 768 bf16 the block
 // norm forward and backward take 104 us with it and 113 us without, the gated
-// norm at 32768 x 6 x 128 75 us and 84 us.
+// norm at 32768 x 6 x 128 73 us and 84 us.
 template <bool PAST> __device__ __forceinline__ void put(u32x4* p, u32x4 w)
 {
     if constexpr (PAST)
