@@ -76,8 +76,11 @@ __global__ __launch_bounds__(256) void attn_append_kernel(AppendArgs a)
                 b += __popcll(__ballot(e <= tok));
             }
             if (b < a.B) {
-                const int st = a.cu[b], en = a.cu[b + 1];
-                if (tok >= st && st >= 0) {
+                // clamped as in the attention, so that both count a sequence's tokens alike
+                int st = a.cu[b], en = a.cu[b + 1];
+                st = st < 0 ? 0 : st;
+                en = en > a.T ? a.T : en;
+                if (tok >= st) {
                     const long long p = (long long)a.kv_len[b] - en + tok;  // kv_len - n + (tok - st)
                     if (p >= 0 && p < a.max_pos && p < ((long long)a.max_pages << a.page_shift)) {
                         pos = (int)p;
