@@ -83,7 +83,8 @@ gdn_status check_attn(const gdn_attn_shape* sh, AttnCall call, gdn_attn_shape& s
         if (s.rot_dim < 0 || s.rot_dim > s.D || s.rot_dim % 16) return GDN_ERR_INVALID_ARG;
         if (s.rot_dim && s.max_pos < 1) return GDN_ERR_INVALID_ARG;
         if (!s.rot_dim) s.max_pos = 0x7fffffff;
-        if (s.T >= (1 << 26)) return GDN_ERR_UNSUPPORTED;
+        // two tokens a workgroup of 256, below 2^32 work-items
+        if (s.T > (1 << 25) - 2) return GDN_ERR_UNSUPPORTED;
     } else {
         const AttnPlan p = attn_plan(s, call == CALL_PAGED);
         if (p.jobs * s.Hkv >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
