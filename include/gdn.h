@@ -365,9 +365,10 @@ gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, c
  * (q and q_out both NULL: not done; q_out may be q where q is dense).
  * cos, sin [max_pos, rot_dim / 2] float32, rot_dim a multiple of 16 up to D (0:
  * no rotation, cos, sin not read).  A token whose position is negative, not
- * below max_pos or behind the table is left out, q_out included; one whose page does not exist writes
- * no cache row.  Positions that two sequences of one call both write (pages
- * they share) end with either's values.
+ * below max_pos or behind the table is left out, q_out included; one whose page
+ * does not exist writes no cache row.  Positions that two sequences of one call
+ * both write (pages they share) end with either's values.  At most 2^25 - 2
+ * tokens a call.
  *
  * gdn_attn_paged: new token i attends to positions 0 .. kv_len[b] - n + i of
  * its sequence, i.e. the cache after gdn_attn_append; q already rotated.
