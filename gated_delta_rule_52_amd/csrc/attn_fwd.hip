@@ -646,7 +646,7 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
     const long long big = ((rows + 127) / 128) * s.Hkv;
     p.small = paged ? rows <= 32LL * s.B : big < 256;
     p.rows = p.small ? 32 : 128;
-    p.blocks = (int)(rows / p.rows + s.B);
+    p.blocks = rows / p.rows + s.B;
     p.splits = 1;
     const long long cap = (long long)s.max_pages * s.page_size;
     p.want = p.small ? 512 : 896;
@@ -658,7 +658,7 @@ AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
         n = n > most ? most : n;
         p.splits = n < 1 ? 1 : n > 128 ? 128 : (int)n;
     }
-    p.jobs = (long long)p.blocks * p.splits;
+    p.jobs = p.blocks * p.splits;
     // The sum of ceil(len / piece) over the blocks is at most one a block more than
     // the sum of len / piece, which a piece's length holds to want / Hkv (or to 256
     // / Hkv, where it is below 1024).

@@ -15,8 +15,8 @@ namespace gdn {
 // many as make `want` workgroups.
 struct AttnPlan {
     bool small;  // 32-row blocks whose waves share out the keys; else 128-row blocks
-    int rows, blocks, splits, want;
-    long long jobs;  // workgroups a key head
+    int rows, splits, want;
+    long long blocks, jobs;  // jobs: workgroups a key head
     size_t ws_bytes;  // partial outputs [splits][T * Hq][D] and log-sums [splits][T * Hq], fp32
 };
 

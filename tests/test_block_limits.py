@@ -15,3 +15,15 @@ def test_append_tokens_of_one_launch(T):
     more than a launch can have."""
     sh = attn(T=T, Hq=1, Hkv=1)
     assert gdn.lib().gdn_attn_append(sh, P, P, P, P, P, P, P, P, P, P, P, None) == 2
+
+
+@pytest.mark.parametrize("B", [0x7fffffff, 0x7fffffff - 1000])
+def test_sequences_near_the_last_int(B):
+    """The blocks of a call are more than an int holds: too many, not fewer than none."""
+    L = gdn.lib()
+    sh = attn(B=B, T=1 << 20)
+    assert L.gdn_attn_workspace_bytes(sh, gdn.GDN_ATTN_PAGED) == 0
+    assert L.gdn_attn_workspace_bytes(sh, gdn.GDN_ATTN_BACKWARD) == 0
+    assert L.gdn_attn_forward(sh, P, P, P, P, P, P, None) == 2
+    assert L.gdn_attn_paged(sh, P, P, P, P, P, P, P, P, BIG, None) == 2
+    assert L.gdn_attn_backward(sh, P, P, P, P, P, P, P, P, P, P, P, BIG, None) == 2
