@@ -428,15 +428,22 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(const int* __restrict__ c
     store4<T>(out + i, s[0] * f, s[1] * f, s[2] * f, s[3] * f);
 }
 
+// workgroups of a pass over `heads` rows a token (query pass: the query heads of a
+// key head, key pass: 1), each block's work cut into `parts`
+long long pass_blocks(int T, int heads, int B, int Hkv, int parts)
+{
+    return ((long long)T * heads / 128 + B) * Hkv * parts;
+}
+// workgroups of attn_delta_kernel
+long long delta_blocks(int T, int Hq, int D) { return ((long long)T * Hq + 1024 / D - 1) / (1024 / D); }
+
 template <typename T, int D>
 gdn_status launch(const BwdArgs& a, hipStream_t st)
 {
-    const unsigned qblocks = (unsigned)(((long long)a.T * a.G / 128 + a.B) * a.Hkv * a.qparts);
-    const unsigned kblocks = (unsigned)((a.T / 128 + a.B) * (long long)a.Hkv * a.kparts);
+    const unsigned qblocks = (unsigned)pass_blocks(a.T, a.G, a.B, a.Hkv, a.qparts);
+    const unsigned kblocks = (unsigned)pass_blocks(a.T, 1, a.B, a.Hkv, a.kparts);
     if constexpr (sizeof(T) == 4) {
-        constexpr int RPB = 1024 / D;
-        const size_t rows = (size_t)a.T * a.Hq;
-        GDN_LAUNCH("attn_delta", attn_delta_kernel<D>, dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(256), st, a);
+        GDN_LAUNCH("attn_delta", attn_delta_kernel<D>, dim3((unsigned)delta_blocks(a.T, a.Hq, D)), dim3(256), st, a);
         GDN_LAUNCH("attn_grads", attn_grads_kernel<D>, dim3(kblocks + qblocks), dim3(256), st, a, kblocks);
     } else {
         GDN_LAUNCH("attn_dq", (attn_dq_kernel<T, D>), dim3(qblocks), dim3(256), st, a);
@@ -501,6 +508,16 @@ BwdPlan bwd_plan(const gdn_attn_shape& s)
 }  // namespace
 
 size_t attn_backward_ws(const gdn_attn_shape& s) { return bwd_plan(s).bytes; }
+
+bool attn_backward_fits(const gdn_attn_shape& s)
+{
+    const BwdPlan p = bwd_plan(s);
+    const long long most = (1LL << 24) - 1;  // of 256 work-items each
+    const long long kb = pass_blocks(s.T, 1, s.B, s.Hkv, p.kparts);
+    const long long qb = pass_blocks(s.T, s.Hq / s.Hkv, s.B, s.Hkv, p.qparts);
+    if (s.dtype == GDN_F32) return kb + qb <= most && delta_blocks(s.T, s.Hq, s.D) <= most;
+    return kb <= most && qb <= most;
+}
 
 gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const void* k, const void* v, const int* cu,
                                   const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,

@@ -27,6 +27,8 @@ gdn_status attn_forward_dispatch(const gdn_attn_shape& s, const void* q, const v
                                  hipStream_t st);
 
 size_t attn_backward_ws(const gdn_attn_shape& s);
+// whether the launches of the gradients stay below 2^32 work-items
+bool attn_backward_fits(const gdn_attn_shape& s);
 gdn_status attn_backward_dispatch(const gdn_attn_shape& s, const void* q, const void* k, const void* v, const int* cu,
                                   const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
                                   void* ws, hipStream_t st);

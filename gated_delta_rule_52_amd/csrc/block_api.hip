@@ -50,7 +50,7 @@ size_t norm_ws(const gdn_norm_shape& s, bool gate)
     return n < 256 ? 256 : n;
 }
 
-enum AttnCall { CALL_PROMPT, CALL_PAGED, CALL_APPEND };
+enum AttnCall { CALL_PROMPT, CALL_BACKWARD, CALL_PAGED, CALL_APPEND };
 
 // Validate an attention shape and fill in the defaults.
 gdn_status check_attn(const gdn_attn_shape* sh, AttnCall call, gdn_attn_shape& s)
@@ -74,7 +74,7 @@ gdn_status check_attn(const gdn_attn_shape* sh, AttnCall call, gdn_attn_shape& s
         // a run of 16 token rows is addressed with 32-bit offsets from its first
         if (*st[i] > (1LL << 24)) return GDN_ERR_UNSUPPORTED;
     }
-    if (call != CALL_PROMPT) {
+    if (call == CALL_PAGED || call == CALL_APPEND) {
         if (s.num_pages < 1 || s.max_pages < 1 || s.page_size < 1) return GDN_ERR_INVALID_ARG;
         if (s.page_size < 16 || s.page_size > 1024 || (s.page_size & (s.page_size - 1))) return GDN_ERR_UNSUPPORTED;
         if ((long long)s.max_pages * s.page_size > (1LL << 30)) return GDN_ERR_UNSUPPORTED;
@@ -88,6 +88,7 @@ gdn_status check_attn(const gdn_attn_shape* sh, AttnCall call, gdn_attn_shape& s
     } else {
         const AttnPlan p = attn_plan(s, call == CALL_PAGED);
         if (p.jobs * s.Hkv >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
+        if (call == CALL_BACKWARD && !attn_backward_fits(s)) return GDN_ERR_UNSUPPORTED;
     }
     return GDN_OK;
 }
@@ -171,7 +172,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape* sh, int call)
     if (call == GDN_ATTN_PAGED)
         return check_attn(sh, CALL_PAGED, s) == GDN_OK ? at_least_256(attn_plan(s, true).ws_bytes) : 0;
     if (call == GDN_ATTN_BACKWARD)
-        return check_attn(sh, CALL_PROMPT, s) == GDN_OK ? at_least_256(attn_backward_ws(s)) : 0;
+        return check_attn(sh, CALL_BACKWARD, s) == GDN_OK ? at_least_256(attn_backward_ws(s)) : 0;
     return 0;
 }
 
@@ -193,7 +194,7 @@ gdn_status gdn_attn_backward(const gdn_attn_shape* sh, const void* q, const void
                              void* dk, void* dv, void* ws, size_t ws_bytes, void* stream)
 {
     gdn_attn_shape s;
-    gdn_status r = check_attn(sh, CALL_PROMPT, s);
+    gdn_status r = check_attn(sh, CALL_BACKWARD, s);
     if (r != GDN_OK) return r;
     if (s.T == 0) return GDN_OK;
     if (any_null(q, k, v, (const void*)cu_seqlens, o, (const void*)lse, dO, (const void*)dq, (const void*)dk,

@@ -348,7 +348,9 @@ gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, c
  * lse = log sum exp(scale q.k) over them (may be NULL; the backward needs it).
  * gdn_attn_backward: dq, dk, dv from dO; ws holds
  * gdn_attn_workspace_bytes(shape, GDN_ATTN_BACKWARD) bytes.  A key head's
- * gradient is the sum over its query heads.
+ * gradient is the sum over its query heads.  In float32 T * Hq (at D = 128) is at most
+ * 2^27 - 8, and the blocks of 128 keys and of 128 query rows, (T / 128 + B) Hkv
+ * and (T (Hq / Hkv) / 128 + B) Hkv, are together below 2^24.
  *
  * The paged cache: k_cache, v_cache [num_pages, page_size, Hkv, D] (dtype),
  * page_size a power of two from 16 to 1024; position p of sequence b lies in

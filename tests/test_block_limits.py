@@ -27,3 +27,27 @@ def test_sequences_near_the_last_int(B):
     assert L.gdn_attn_forward(sh, P, P, P, P, P, P, None) == 2
     assert L.gdn_attn_paged(sh, P, P, P, P, P, P, P, P, BIG, None) == 2
     assert L.gdn_attn_backward(sh, P, P, P, P, P, P, P, P, P, P, P, BIG, None) == 2
+
+
+@pytest.mark.parametrize("shape", [
+    dict(T=(1 << 27) - 1, Hq=1, Hkv=1, D=128),        # a row by 32 lanes, to the last of 2^32 work-items
+    dict(T=((1 << 27) - 1) // 7, Hq=7, Hkv=1, D=128),
+    dict(B=1 << 23, T=1 << 20, Hq=1, Hkv=1),          # blocks of keys and of queries in one launch
+    dict(B=1 << 22, T=1 << 20, Hq=2, Hkv=2),
+])
+def test_fp32_gradients_of_one_launch(shape):
+    """The fp32 backward's two launches (a row's delta, and both gradient passes in
+    one) stay below 2^32 work-items or the call is refused."""
+    L = gdn.lib()
+    sh = attn(dtype=0, **shape)
+    assert L.gdn_attn_workspace_bytes(sh, gdn.GDN_ATTN_BACKWARD) == 0
+    assert L.gdn_attn_backward(sh, P, P, P, P, P, P, P, P, P, P, P, BIG, None) == 2
+
+
+@pytest.mark.parametrize("shape", [
+    dict(dtype=0, T=(1 << 27) - 8, Hq=1, Hkv=1, D=128), dict(dtype=0, T=(1 << 27) - 1, Hq=1, Hkv=1, D=64),
+    dict(dtype=1, T=(1 << 27) - 1, Hq=1, Hkv=1, D=128), dict(dtype=1, B=1 << 23, T=1 << 20, Hq=1, Hkv=1),
+    dict(dtype=0, B=1 << 22, T=1 << 20, Hq=1, Hkv=1),
+])
+def test_gradients_below_the_limit(shape):
+    assert gdn.lib().gdn_attn_workspace_bytes(attn(**shape), gdn.GDN_ATTN_BACKWARD) > 0
