@@ -60,6 +60,12 @@ def declare(L):
         fn.argtypes, fn.restype = args, res
 
 
+def _too_large(*counts):
+    """The C shapes hold 32-bit counts, and ctypes drops higher bits silently: every
+    call refuses a size with any of them first, (a | b | ...) >> 31."""
+    return ValueError(f"sizes must be at most 2147483647, got {counts}")
+
+
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
 
@@ -154,6 +160,9 @@ def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):
     dt, dev = _dtype(x, "x"), _gpu(x, "x")
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     lead, channels = shape[:-1], shape[-1:]
+    tokens, width = lead.numel(), shape[-1]
+    if (tokens | width) >> 31:
+        raise _too_large(tokens, width)
     if res_scale is not None and y is None:
         raise ValueError("res_scale scales y: pass y too")
     if out is None:
@@ -166,7 +175,7 @@ def gdn_norm_block(x, weight, y=None, res_scale=None, *, eps=1e-6, out=None):
     _alike(dev, shape, dtype, ("x", "y", "h", "n"), x, y, h, n)
     _alike(dev, channels, f32, ("weight", "res_scale"), weight, res_scale)
     _alike(dev, lead, f32, ("rstd",), rstd)
-    sh = GdnNormShape(lead.numel(), 1, shape[-1], dt, eps, 0)
+    sh = GdnNormShape(tokens, 1, width, dt, eps, 0)
     _run(lib().gdn_norm_block, "gdn_norm_block", dev, ctypes.byref(sh), _p(x), _p(y), _p(res_scale), _p(weight), _p(h),
          _p(n), _p(rstd))
     return (x if h is None and y is None else h), n, rstd
@@ -179,6 +188,9 @@ def gdn_norm_block_backward(dn, x, weight, rstd, y=None, res_scale=None, *, dh=N
     dt, dev = _dtype(x, "x"), _gpu(x, "x")
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     lead, channels, scaled = shape[:-1], shape[-1:], res_scale is not None
+    tokens, width = lead.numel(), shape[-1]
+    if (tokens | width) >> 31:
+        raise _too_large(tokens, width)
     if scaled and y is None:
         raise ValueError("res_scale scales y: pass y too")
     if out is None:
@@ -192,7 +204,7 @@ def gdn_norm_block_backward(dn, x, weight, rstd, y=None, res_scale=None, *, dh=N
     _alike(dev, shape, dtype, ("x", "dn", "y", "dh", "dx", "dy"), x, dn, y, dh, dx, dy)
     _alike(dev, channels, f32, ("weight", "res_scale", "dweight", "dres_scale"), weight, res_scale, dw, da)
     _alike(dev, lead, f32, ("rstd",), rstd)
-    sh = GdnNormShape(lead.numel(), 1, shape[-1], dt, 1e-6, 0)  # the saved rstd holds the forward's eps
+    sh = GdnNormShape(tokens, 1, width, dt, 1e-6, 0)  # the saved rstd holds the forward's eps
     L = lib()
     ws, n = _workspace(L.gdn_norm_workspace_bytes, sh, 0, ws, dev, "gdn_norm_workspace_bytes")
     _run(L.gdn_norm_block_backward, "gdn_norm_block_backward", dev, ctypes.byref(sh), _p(dn), _p(dh), _p(x), _p(y),
@@ -205,6 +217,8 @@ def _gate_shape(o, gate, weight, dev, eps):
     if len(shape) < 3:
         raise ValueError(f"o must be [..., H, D], got {tuple(shape)}")
     tokens, (H, D) = shape[:-2].numel(), shape[-2:]
+    if (tokens | H | D) >> 31:
+        raise _too_large(tokens, H, D)
     if gate.shape != shape:
         raise ValueError(f"gate must have shape {tuple(shape)}, got {tuple(gate.shape)}")
     if not gate.is_contiguous() and len(shape) > 3:
@@ -274,6 +288,8 @@ def _prompt_shape(q, k, v, cu, scale):
     ks = _take(k, "k", (T, Hkv, D), q.dtype, dev, stride=True)
     vs = _take(v, "v", (T, Hkv, D), q.dtype, dev, stride=True)
     B = _sequences(cu, dev)
+    if (B | T | Hq | Hkv | D) >> 31:
+        raise _too_large(B, T, Hq, Hkv, D)
     return GdnAttnShape(B, T, Hq, Hkv, D, dt, 0.0 if scale is None else scale, qs, ks, vs), dev
 
 
@@ -322,6 +338,8 @@ def _cache(sh, k_cache, v_cache, page_table, kv_len, dtype, dev):
     _alike(dev, shape, dtype, ("k_cache", "v_cache"), k_cache, v_cache)
     _take(page_table, "page_table", table, torch.int32, dev)
     _take(kv_len, "kv_len", (sh.B,), torch.int32, dev)
+    if (shape[0] | shape[1] | table[1]) >> 31:
+        raise _too_large(shape[0], shape[1], table[1])
     sh.num_pages, sh.page_size, sh.max_pages = shape[0], shape[1], table[1]
 
 
@@ -342,7 +360,10 @@ def gdn_attn_append(q, k, v, cos, sin, cu_seqlens, kv_len, page_table, k_cache, 
         _take(q_out, "q_out", q.shape, k.dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    sh = GdnAttnShape(_sequences(cu_seqlens, dev), T, Hq, Hkv, D, dt, 0.0, qs, ks, vs)
+    B = _sequences(cu_seqlens, dev)
+    if (B | T | Hq | Hkv | D) >> 31:
+        raise _too_large(B, T, Hq, Hkv, D)
+    sh = GdnAttnShape(B, T, Hq, Hkv, D, dt, 0.0, qs, ks, vs)
     _cache(sh, k_cache, v_cache, page_table, kv_len, k.dtype, dev)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
@@ -351,6 +372,8 @@ def gdn_attn_append(q, k, v, cos, sin, cu_seqlens, kv_len, page_table, k_cache, 
         if len(angles) != 2:
             raise ValueError(f"cos must be [max_pos, rot_dim / 2], got {tuple(angles)}")
         _alike(dev, angles, torch.float32, ("cos", "sin"), cos, sin)
+        if (angles[0] | 2 * angles[1]) >> 31:
+            raise _too_large(*angles)
         sh.max_pos, sh.rot_dim = angles[0], 2 * angles[1]
     _run(lib().gdn_attn_append, "gdn_attn_append", dev, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(cos), _p(sin),
          _p(cu_seqlens), _p(kv_len), _p(page_table), _p(k_cache), _p(v_cache), _p(q_out))
@@ -365,7 +388,10 @@ def gdn_attn_paged(q, k_cache, v_cache, page_table, cu_seqlens, kv_len, *, scale
     qs = _take(q, "q", q.shape, q.dtype, dev, stride=True)
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache must be [num_pages, page_size, Hkv, D], got {tuple(k_cache.shape)}")
-    sh = GdnAttnShape(_sequences(cu_seqlens, dev), T, Hq, k_cache.shape[2], D, dt, 0.0 if scale is None else scale, qs)
+    B, Hkv = _sequences(cu_seqlens, dev), k_cache.shape[2]
+    if (B | T | Hq | Hkv | D) >> 31:
+        raise _too_large(B, T, Hq, Hkv, D)
+    sh = GdnAttnShape(B, T, Hq, Hkv, D, dt, 0.0 if scale is None else scale, qs)
     _cache(sh, k_cache, v_cache, page_table, kv_len, q.dtype, dev)
     if o is None:
         o = torch.zeros(q.shape, dtype=q.dtype, device=dev)
