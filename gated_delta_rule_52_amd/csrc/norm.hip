@@ -112,11 +112,13 @@ template <int L> __device__ __forceinline__ float group_sum(float x, float (*red
 // ---------------------------------------------------------------------------
 // residual add and norm.  A row is held by L lanes, N words each.
 // ---------------------------------------------------------------------------
+// x and y are not __restrict__: h may be either of them.  A lane stores only the
+// words of its own row that it has loaded; the groups behind the last row load that
+// row without using it.
 template <typename T, int L, int N, bool PAST>
-__global__ __launch_bounds__(256) void norm_block_kernel(const T* __restrict__ x, const T* __restrict__ y,
-                                                         const float* __restrict__ a, const float* __restrict__ w,
-                                                         T* h, T* n, float* __restrict__ rstd, int rows, int width,
-                                                         float eps)
+__global__ __launch_bounds__(256) void norm_block_kernel(const T* x, const T* y, const float* __restrict__ a,
+                                                         const float* __restrict__ w, T* h, T* n,
+                                                         float* __restrict__ rstd, int rows, int width, float eps)
 {
     constexpr int VE = Vec<T>::VE, R = 256 / L;
     __shared__ float red[2][4];
