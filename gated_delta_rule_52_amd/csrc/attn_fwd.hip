@@ -153,9 +153,12 @@ struct Lengths {
 // for 16 of them: 30 us, against 83 us).  A multiple of 128 and no more pieces
 // than there is room for; below 1024 keys, where writing and joining the partial
 // outputs begins to count, only as far as one workgroup for each compute unit
-// asks for it.
+// asks for it.  The kernel and the join of its pieces each form it and have to
+// find the same bits: nothing is contracted here, since whether a product (rounded
+// from 2^24 on) goes into its sum unrounded would be the compiler's choice in each.
 __device__ __forceinline__ int piece_keys(const FwdArgs& a, const Lengths& first)
 {
+#pragma clang fp contract(off)
     float work = wave_sum((float)first.nb * (float)first.len);
     int most = wave_max(first.len);
     for (int b0 = 64; b0 < a.B; b0 += 64) {
