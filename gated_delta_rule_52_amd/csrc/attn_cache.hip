@@ -140,11 +140,17 @@ __global__ __launch_bounds__(256) void attn_append_kernel(AppendArgs a)
 template <typename T>
 gdn_status launch(const AppendArgs& a, hipStream_t st)
 {
-    // A workgroup a token while there are at most eight for a compute unit; then
-    // two tokens share one, and what is written, more than the L2 holds, is not
-    // kept there (17.7 thousand tokens: 47 us; one token 48 us, four 49 us; kept, 54 us)
+    // A workgroup a token while there are at most eight for a compute unit; then two
+    // tokens share one (17.7 thousand tokens: 47 us; one token 48 us, four 49 us) and,
+    // where they write more than the L2 holds (4 MB on each of 8 dies), it is not kept
+    // there (192 MB: 59 us, kept 71 us; with the attention that then reads it 624 and
+    // 621 us).  Up to there it is kept: this kernel takes longer (24 MB: 9.9 us, not kept
+    // 8.1) and the attention gains more (62.4 us together, not kept 63.8).
+    const long long words = (long long)a.T * ((a.qo ? a.Hq : 0) + 2 * a.Hkv) * a.D;
     if (a.T <= 2048)
         GDN_LAUNCH("attn_append", (attn_append_kernel<T, 1, false>), dim3(a.T), dim3(256), st, a);
+    else if (words * (long long)sizeof(T) <= (32LL << 20))
+        GDN_LAUNCH("attn_append", (attn_append_kernel<T, 2, false>), dim3((a.T + 1) / 2), dim3(256), st, a);
     else
         GDN_LAUNCH("attn_append", (attn_append_kernel<T, 2, true>), dim3((a.T + 1) / 2), dim3(256), st, a);
     return GDN_OK;

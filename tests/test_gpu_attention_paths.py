@@ -2,8 +2,8 @@
 pieces of the key axis longer than the window of page numbers that a wave holds,
 with pages missing behind its refill; pieces of sequences past the first waves of
 64; fp32 prompts in 128-row blocks, their keys whole and cut up; products of rows
-and keys that 24 bits do not hold.  Against the plain 64-bit forms, within the
-bounds that block_reference.py derives."""
+and keys that 24 bits do not hold; appends that write more than the L2 holds.
+Against the plain 64-bit forms, within the bounds that block_reference.py derives."""
 import pytest
 import torch
 
@@ -146,3 +146,29 @@ def test_fp32_error_in_the_norm(D, heads, lens):
         here, there = float((got.double() - want[name]).norm() / size), float((plain[name].double() - want[name]).norm() / size)
         log(f"  D={D} {lens} {name}: {here:.1e} against {there:.1e}")
         assert here <= 4 * there, name
+
+
+@pytest.mark.parametrize("dtype,tokens", [("bf16", 7001), ("f32", 3501)])
+def test_append_past_the_l2(dtype, tokens):
+    """More than 32 MB written: 24 heads of 128 a token."""
+    import gated_delta_rule_52_amd as gdn
+    dt, new = DT[dtype], [tokens, 1, 500]
+    log(f"append past the L2 {dtype} {new}")
+    cu, whole = cumulate(new), [tokens, 65, 700]
+    q, k, v = qkv(cu[-1], 16, 4, 128, dt, True)
+    kc, vc, table = make_cache(whole, 64, 4, 128, dt, poison=3.0)
+    table[2, 9] = -1
+    ang = torch.rand(max(whole), 64, generator=torch.Generator().manual_seed(1)).double() * 1e4
+    cos, sin = ang.cos().float().cuda(), ang.sin().float().cuda()
+    qo = torch.full_like(q, 5.0, memory_format=torch.contiguous_format)
+    assert (qo.numel() + 2 * k.numel()) * qo.element_size() > 32 << 20
+    wk, wv, wq = ref.append(q, k, v, cos, sin, cu, whole, table, kc, vc, qo)
+    gdn.gdn_attn_append(q, k, v, cos, sin, ints(cu), ints(whole), table, kc, vc, q_out=qo)
+    torch.cuda.synchronize()
+    # a rotated value: two products and a sum in fp32, then half a step
+    size = 2 * max(float(q.float().abs().max()), float(k.float().abs().max()))
+    lim = lambda w: ref.HALF[dt] * w.abs() + 3 * ref.U32 * size
+    e = worst(qo, wq, lim(wq)), worst(kc, wk, lim(wk))
+    log(f"  q={e[0]:.2f} k={e[1]:.2f}")
+    assert max(e) <= 1, e
+    assert torch.equal(ref.f64(vc), wv)
