@@ -30,6 +30,9 @@ template <> struct FragOf<bf16> { typedef bf16x8 type; };
 template <> struct FragOf<float> { typedef f32x8 type; };
 template <typename T> using Frag = typename FragOf<T>::type;
 
+__device__ __forceinline__ __bf16 frag_value(bf16 x) { return __builtin_bit_cast(__bf16, x.bits); }
+__device__ __forceinline__ float frag_value(float x) { return x; }
+
 __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -72,6 +75,75 @@ template <> __device__ __forceinline__ f32x8 load_frag<float>(const float* p)
 {
     const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Masked pairs.  A value that a row does not depend on must not reach it, and a
+// product of an infinity or a NaN with the pair's 0 would.  So where a masked tile
+// holds such values, its products take finite ones instead (finite_only), and the
+// rows that do depend on them get them after the last tile (add_nonfinite).  Tiles
+// without a masked pair go through the products as they are.
+//
+// Whether all of a wave's fragments are finite.  bf16: by their products with 0,
+// which are 0 or NaN (in any assignment of rows), a matrix instruction a fragment.
+template <int N> __device__ __forceinline__ bool all_finite(const bf16x8 (&v)[N])
+{
+    f32x4 z = zero4();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[i], __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0}), z, 0, 0, 0);
+    const float s = (z[0] + z[1]) + (z[2] + z[3]);
+    return !__any(s != s);
+}
+// fp32: by the sum of the products with 0, an operation a value.
+template <int N> __device__ __forceinline__ bool all_finite(const f32x8 (&v)[N])
+{
+    f32x4 z = zero4();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j & 3] = __builtin_fmaf(v[i][j], 0.f, z[j & 3]);
+    const float s = (z[0] + z[1]) + (z[2] + z[3]);
+    return !__any(s != s);
+}
+
+// a fragment with infinities and NaN as finite values of the largest magnitude,
+// whose product with the 0 of a masked pair is 0
+__device__ __forceinline__ bf16x8 finite_only(bf16x8 v)
+{
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // without the sign bit a signed minimum, with it an unsigned one
+        const uint32_t x = w[i];
+        const s16x2 a = __builtin_elementwise_min(__builtin_bit_cast(s16x2, x), s16x2{0x7f7f, 0x7f7f});
+        const u16x2 b = __builtin_elementwise_min(__builtin_bit_cast(u16x2, a), u16x2{0xff7f, 0xff7f});
+        w[i] = __builtin_bit_cast(uint32_t, b);
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ f32x8 finite_only(f32x8 v)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(v[i], -3.402823466e38f, 3.402823466e38f);
+    return v;
+}
+
+// The infinities and NaN of a row of D values into the accumulators of the lanes
+// whose column depends on it.  Where the products did take them, that changes nothing.
+template <typename T, int D>
+__device__ __forceinline__ void add_nonfinite(f32x16 (&acc)[D / 32], const T* row, bool depends)
+{
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) {
+        __builtin_amdgcn_sched_barrier(0);  // rare: with few registers, not fast
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float x = to_f32(row[32 * dt + 8 * (r >> 2) + 4 * h + (r & 3)]);
+            if (depends && !(fabsf(x) < INFINITY)) acc[dt][r] += x;
+        }
+    }
 }
 
 // four accumulator rows of one column, stored as four neighbours

@@ -75,6 +75,7 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
     const int wkey = key0 + 32 * w;
     const int key = wkey + (l & 31);
     const int kc = key < s.n ? key : s.n - 1;
+    const unsigned seen = key < s.n ? s.n - key : 0;  // queries that see the key
 
     Frag<T> kf[KK];
     {
@@ -114,6 +115,7 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
         }
     };
     int cq = fq;  // query tile of the one being multiplied
+    int later = i1;  // masked tiles from this one on are left for the end (attn.h)
     const uint32_t along = Rows<T, D>::along_at();
     auto tile = [&](int it, auto BUF) {
         constexpr int buf = BUF();
@@ -150,10 +152,15 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
             }
         }
         if (qs < wkey + 31 || qs + 32 > s.n) {
+            // a query's q that is not finite leaves its log-sum, its do its delta neither
+            const bool finite = fabsf(ld[buf][h][l & 31]) < INFINITY;
+            if (__builtin_expect(!__all(finite) || later < i1, 0)) {
+                later = later < it ? later : it;
+                return;
+            }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int q = qs + 8 * (r >> 2) + 4 * h + (r & 3);
-                const bool in = key <= q && q < s.n;
+                const bool in = (unsigned)(qs - key + 4 * h + 8 * (r >> 2) + (r & 3)) < seen;  // key <= query < s.n
                 sc[r] = in ? sc[r] : 0.f;
                 dp[r] = in ? dp[r] : 0.f;
             }
@@ -176,6 +183,55 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
         if (it + 1 < i1) tile(it + 1, std::integral_constant<int, 1>{});
     }
     wait_vm<0>();  // a piece without tiles still has its values under way
+    // The masked tiles that were left: the same steps, with finite operands in the
+    // products and everything but v straight from memory.
+#pragma unroll 1
+    for (int it = later; it < i1; ++it) {
+        const int h4 = opaque(4 * h);  // of this loop alone: nothing is formed ahead of the other
+        const int g = it / ntq, qs = (tq0 + it - g * ntq) * QT, hq = hk * a.G + g;
+        if (qs + 31 < wkey || !(qs < wkey + 31 || qs + 32 > s.n)) continue;
+        auto row = [&](int q) { return (size_t)(s.start + (q < s.n ? q : s.n - 1)); };
+        auto q_at = [&](int q) { return (const T*)((const char*)a.q + row(q) * a.q_bytes) + (size_t)hq * D; };
+        auto o_at = [&](int q) { return (const T*)((const char*)a.dO + row(q) * a.o_bytes) + (size_t)hq * D; };
+        f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const int c = 16 * kk + 2 * h4;
+            sc = mma32(load_frag<T>(q_at(qs + (l & 31)) + c), kf[kk], sc);
+            dp = mma32(load_frag<T>(o_at(qs + (l & 31)) + c), Rows<T, D>::along(vtab + 32 * w * Rows<T, D>::BYTES, along, 0, kk), dp);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int q = qs + 8 * (r >> 2) + h4 + (r & 3);
+            const size_t st = (size_t)hq * a.T + row(q);
+            const bool in = (unsigned)(q - key) < seen;
+            const float p = exp2_hw(sc[r] * sl2 - a.lse2[st]), ds = p * (dp[r] - a.delta[st]);
+            sc[r] = in ? p : 0.f;
+            dp[r] = in ? ds : 0.f;
+        }
+        // columns d .. d + 31 of 16 rows from q0 on, as Rows::down reads them, one
+        // after the other: no registers of the loop above are for this
+        auto down = [&](auto at, int q0, int d) {
+            Frag<T> v;
+            __builtin_amdgcn_sched_barrier(0);
+            q0 = opaque(q0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = frag_value(at(q0 + 8 * (j >> 2) + h4 + (j & 3))[d + (l & 31)]);
+            return finite_only(v);
+        };
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const Frag<T> p = acc_frag<T>(sc, b), ds = acc_frag<T>(dp, b);
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                dv[dt] = mma32(down(o_at, qs + 16 * b, 32 * dt), p, dv[dt]);
+                dk[dt] = mma32(down(q_at, qs + 16 * b, 32 * dt), ds, dk[dt]);
+            }
+        }
+        // (of a query whose q is not finite no p is: dk has it from the products)
+#pragma unroll 1
+        for (int q = qs; q < qs + 32 && q < s.n; ++q) add_nonfinite<T, D>(dv, o_at(q), key <= q);
+    }
     if (key < s.n) {
         const size_t at = ((size_t)(s.start + key) * a.Hkv + hk) * D, all = (size_t)a.T * a.Hkv * D;
         float* pk = a.kparts > 1 ? a.part_k + part * all : nullptr;
@@ -262,6 +318,7 @@ __device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T,
         Rows<T, D>::template fetch<RW>(lds[buf][1], w * RW, vb + (size_t)kat * a.v_bytes, a.v_bytes, s.n - 1 - kat);
     };
     float over = 0.f;  // sum_j ds_ij of this lane's keys
+    int rest0 = 0x7fffffff;  // from which key on the products may have left out keys (attn.h)
     // one tile; FIRST: only the row sums
     auto tile = [&](int t, int end, auto BUF, auto FIRST) {
         constexpr int buf = BUF();
@@ -277,10 +334,9 @@ __device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T,
             for (int kk = 0; kk < KK; ++kk) sc = mma32(Rows<T, D>::along(lds[buf][0], 32 * sub, kk), qf[kk], sc);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) dp = mma32(Rows<T, D>::along(lds[buf][1], 32 * sub, kk), df[kk], dp);
-            // bf16: the keys' columns are read now, to arrive under the exponentials
-            constexpr bool AHEAD = sizeof(T) == 2 && !FIRST();
+            // the keys' columns are read now, to arrive under the exponentials
             Frag<T> kd[2 * DT];
-            if (AHEAD) {
+            if (!FIRST()) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -289,11 +345,22 @@ __device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T,
             }
             if (sizeof(T) == 2) {
                 order_products<2 * KK, 1, 4>();
-                if (AHEAD) order_reads<4 * DT>();
+                if (!FIRST()) order_reads<4 * DT>();
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] = exp2_hw(sc[r] * sl2 - lse2) * (dp[r] - delta);
             if (key0 + 32 > wmin) {
+                if (!FIRST()) {
+                    // a key that is not finite shows in its scores
+                    float z = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) z = fmaf(sc[r], 0.f, z);
+                    if (__builtin_expect(__any(z != z), 0)) {
+                        rest0 = rest0 < key0 ? rest0 : key0;
+#pragma unroll
+                        for (int i = 0; i < 2 * DT; ++i) kd[i] = finite_only(kd[i]);
+                    }
+                }
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     dp[r] = key0 + 8 * (r >> 2) + 4 * h + (r & 3) < limit ? dp[r] : 0.f;
@@ -307,9 +374,7 @@ __device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T,
                 for (int b = 0; b < 2; ++b) {
                     const Frag<T> ds = acc_frag<T>(dp, b);
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-                        dq[dt] = mma32(AHEAD ? kd[b * DT + dt] : Rows<T, D>::down(lds[buf][0], 32 * sub + 16 * b, 32 * dt),
-                                       ds, dq[dt]);
+                    for (int dt = 0; dt < DT; ++dt) dq[dt] = mma32(kd[b * DT + dt], ds, dq[dt]);
                 }
             }
         }
@@ -329,6 +394,10 @@ __device__ __forceinline__ void query_pass(const BwdArgs& a, int id, QueryLds<T,
     }
     const int t0 = (int)((long long)tiles * part / a.qparts), t1 = (int)((long long)tiles * (part + 1) / a.qparts);
     round(t0, t1, std::false_type{});
+    if (__builtin_expect(rest0 < wmax, 0)) {
+#pragma unroll 1
+        for (int j = rest0; j < wmax; ++j) add_nonfinite<T, D>(dq, (const T*)(kb + (size_t)j * a.k_bytes), j < limit);
+    }
     if (sizeof(T) == 2 && part == 0) {
         // a piece of the keys does not have the whole row sum
         if (a.qparts == 1) delta += half_add(over);

@@ -38,6 +38,7 @@ struct Queries {
     f32x16 o[DT];
     float m, l;   // running maximum of the raw scores; sum of this lane's own keys
     int limit;    // keys [0, limit) are seen
+    int rest;     // uniform: from which key on values may be left out (add_rest)
 
     __device__ __forceinline__ void load(const T* row)
     {
@@ -48,6 +49,7 @@ struct Queries {
         for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
         m = -INFINITY;
         l = 0.f;
+        rest = 0x7fffffff;
     }
 
     // 32 keys of the tables from row r0; key0 is the position of the first.
@@ -61,18 +63,25 @@ struct Queries {
         f32x16 s = zero16();
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) s = mma32(Rows<T, D>::along(ktab, r0, kk), q[kk], s);
-        // bf16: the values are read now, to arrive under the exponentials
-        constexpr bool AHEAD = sizeof(T) == 2;
+        // the values are read now, to arrive under the exponentials
         Frag<T> v[2 * DT];
-        if (AHEAD) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) v[b * DT + dt] = Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt);
+            for (int dt = 0; dt < DT; ++dt) v[b * DT + dt] = Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt);
+        if (sizeof(T) == 2) {
             order_products<KK, 1, 4>();
             order_reads<4 * DT>();
         }
         if (mask) {
+            // A value that a row does not see must not reach it, and 0 x infinity would:
+            // where there is any, the products take finite ones, and what they leave out
+            // is added in the end.
+            if (__builtin_expect(!all_finite(v), 0)) {
+                rest = rest < key0 ? rest : key0;
+#pragma unroll
+                for (int i = 0; i < 2 * DT; ++i) v[i] = finite_only(v[i]);
+            }
             const int left = limit - key0 - 4 * h;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -113,8 +122,19 @@ struct Queries {
         for (int b = 0; b < 2; ++b) {
             const Frag<T> p = acc_frag<T>(s, b);
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-                o[dt] = mma32(AHEAD ? v[b * DT + dt] : Rows<T, D>::down(vtab, r0 + 16 * b, 32 * dt), p, o[dt]);
+            for (int dt = 0; dt < DT; ++dt) o[dt] = mma32(v[b * DT + dt], p, o[dt]);
+        }
+    }
+
+    // What the products left out of the values of keys rest .. end - 1.  `at`: a
+    // key's values, null for an absent one.
+    template <typename F>
+    __device__ __forceinline__ void add_rest(int end, F&& at)
+    {
+#pragma unroll 1
+        for (int key = rest; key < end; ++key) {
+            const T* v = at(key);
+            if (v) add_nonfinite<T, D>(o, v, key < limit);
         }
     }
 };
@@ -254,6 +274,14 @@ struct Keys {
         const int p = pages[(key < len ? key : len - 1) >> a.page_shift];
         return p >= 0 && p < a.num_pages ? p : -1;
     }
+    // the values of key `key`, below len; null: absent
+    __device__ __forceinline__ const T* value(const FwdArgs& a, int key) const
+    {
+        const int p = page(a, key);
+        if (PAGED && p < 0) return nullptr;
+        const long long row = PAGED ? ((long long)p << a.page_shift) + (key & ((1 << a.page_shift) - 1)) : key;
+        return (const T*)(v + row * a.v_bytes);
+    }
     // the run from `key` into rows r0 .. r0 + CH - 1 of both tables
     __device__ __forceinline__ void fetch(const FwdArgs& a, int key, int page, void* ktab, void* vtab, int r0) const
     {
@@ -355,6 +383,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
         if (t + 1 < t1) tile(t + 1, std::integral_constant<int, 1>{});
     }
 
+    if (__builtin_expect(qs.rest < wmax, 0))
+        qs.add_rest(t1 * KT < wmax ? t1 * KT : wmax, [&](int key) { return keys.value(a, key); });
     const float sum = half_add(qs.l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (row < R) {
@@ -486,6 +516,8 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
         }
     }
 
+    if (__builtin_expect(qs.rest < upto, 0))
+        qs.add_rest(t1 * 32 < upto ? t1 * 32 : upto, [&](int key) { return keys.value(a, key); });
     // join: out = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w
     __syncthreads();
     float* ot = reinterpret_cast<float*>(lds);

@@ -340,9 +340,9 @@ gdn_status gdn_norm_gate_backward(const gdn_norm_shape *shape, const void *dy, c
  * scale 0 means D^-0.5.  D in {64, 128}; Hq a multiple of Hkv, at most 1024;
  * T * Hq < 2^27.
  *
- * Sequences do not touch each other: a non-finite value in one token's rows can
- * reach results of its own sequence only (there also those of earlier tokens,
- * which share a tile of keys with it).
+ * A value that is not finite reaches the results that depend on it and no
+ * others: not those of other sequences, nor of earlier tokens (gradients: of
+ * later keys).
  *
  * gdn_attn_forward: token i of a sequence attends to its tokens 0 .. i.
  * lse = log sum exp(scale q.k) over them (may be NULL; the backward needs it).
