@@ -177,9 +177,14 @@ __global__ __launch_bounds__(256) void norm_block_kernel(const T* x, const T* y,
 // order in every run.  A row's words are held as they were loaded and opened
 // twice, for the row's sum and for its gradients: with four rows' worth of
 // floats instead a lane took 192 registers and the card had too few loads in
-// flight (32768 x 768 bf16, forward and backward: 131 us, against 113 us).
+// flight (32768 x 768 bf16, forward and backward: 131 us, against 113 us).  The
+// bounds are as many waves as that leaves room for; <bf16, 16, 2> and <bf16, 16, 3>
+// spill 8 registers each under them, which costs less than a wave (65536 rows of
+// 256: 43 us, without 49; of 384: 60 and 71).  Eight words of bf16 a lane need more
+// than the 256 registers of two waves (114 spilled): they have one (2048 rows of
+// 16384: 142 us, with two waves 204).
 template <typename T, int L, int N, bool PAST>
-__global__ __launch_bounds__(256, N <= 2 ? 4 : N == 3 ? 3 : 2) void norm_block_bwd_kernel(
+__global__ __launch_bounds__(256, N <= 2 ? 4 : N == 3 ? 3 : N == 8 && sizeof(T) == 2 ? 1 : 2) void norm_block_bwd_kernel(
     const T* __restrict__ dn, const T* __restrict__ dh, const T* __restrict__ x, const T* __restrict__ y,
     const float* __restrict__ a, const float* __restrict__ w, const float* __restrict__ rstd, T* dx, T* dy,
     float* __restrict__ part, int rows, int width)
@@ -539,7 +544,7 @@ int norm_partials(const gdn_norm_shape& s, bool gate)
     const int ve = s.dtype == GDN_BF16 ? 8 : 4;
     const Split sp = gate ? Split{s.width / ve, 1} : pick_split(s.width / ve, s.tokens);
     const int blocks = ceil_div((long long)s.tokens * s.heads, 256 / sp.L);
-    const int most = sp.N <= 2 ? 1024 : sp.N == 3 ? 768 : 512;
+    const int most = sp.N <= 2 ? 1024 : sp.N == 3 ? 768 : sp.N == 8 && ve == 8 ? 256 : 512;
     return blocks < most ? blocks : most;
 }
 
