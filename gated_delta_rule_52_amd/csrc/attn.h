@@ -390,11 +390,11 @@ struct Span {
 // BY_LEVEL, up to 64 sequences: the blocks come in the order of their level, the
 // highest first, across sequences: a causal prompt's block has work in
 // proportion to its level, and the largest pieces first is what lets a grid end
-// evenly (eight packed prompts of up to 4096 tokens, forward and backward: 737 us
-// with the sequences one after the other, 668 us by level).  Otherwise the
-// sequences come one after the other, each from its highest level down, which
-// keeps the blocks that share keys together (new tokens over a cache: 295 us by
-// level, 241 us so).
+// evenly (eight packed prompts of up to 4096 tokens, forward and backward, take 10 %
+// longer with the sequences one after the other).  Otherwise the sequences come
+// one after the other, each from its highest level down, which keeps the blocks
+// that share keys together (chunks of new tokens over a cache take 22 % longer by
+// level).
 template <bool BY_LEVEL>
 __device__ __forceinline__ bool find_block(const int* __restrict__ cu, int B, int T, int G, int BR, int id, Span& s)
 {

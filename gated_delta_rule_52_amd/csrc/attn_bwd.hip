@@ -46,9 +46,9 @@ __device__ __forceinline__ void put4(T* out, float* part, size_t at, const f32x1
 
 // The key pass: dk, dv of 128 keys: four waves of 32 keys.  The keys stay in registers, the
 // values in LDS (with both in registers a wave would need more than the 256 that
-// two waves a SIMD have: 536 us instead of 1220); tiles of 32 tokens of one query
-// head after the other go through two LDS buffers.  Four products for a pair:
-// 8192 tokens, 16 heads over 4 of 128, bf16, take 520 us, 1.06 PFLOP/s.
+// two waves a SIMD have, and spills: 2.3 times the time); tiles of 32 tokens of one
+// query head after the other go through two LDS buffers.  Four products for a pair:
+// 8192 tokens, 16 heads over 4 of 128, bf16, take 530 us, 1.04 PFLOP/s.
 template <typename T, int D>
 struct KeyLds {
     static constexpr int QT = 32, TAB = QT * Rows<T, D>::BYTES;
@@ -248,7 +248,7 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
 }
 
 // The query pass: dq of 128 rows (token * G + head): four waves of 32 rows; tiles
-// of KT keys go through two LDS buffers.  Three products for a pair: 398 us, 1.04
+// of KT keys go through two LDS buffers.  Three products for a pair: 395 us, 1.04
 // PFLOP/s at the sizes above.
 //
 // bf16: delta_i = do_i . o_i carries the rounding of the stored o, and an error
@@ -257,8 +257,11 @@ __device__ __forceinline__ void key_pass(const BwdArgs& a, int id, KeyLds<T, D>&
 // summed on the way and delta + sum_j ds_ij goes to the key pass.  Rows that see
 // at most SHORT keys, where o is as large as the values it averages and its
 // rounding counts most, take a first round over their keys for it and use it in
-// their own dq too.  (Error of dq and dk against 64 bits, in units of
-// the error of storing them: 1.7 and 1.8 at 16 tokens without this, 1.5 with it.)
+// their own dq too.  (Error of dq and dk against 64 bits, in units of the error of
+// storing them: 1.7 and 1.8 at 16 tokens without this, 1.4 with it; two tokens,
+// whose gradients are a product or two, have up to 2.2.)  Where the keys are cut
+// into pieces no piece has the whole row sum, and the longer rows keep the given
+// delta: 1.4 with scores of deviation 1, 2.0 with 4, where few keys take the weight.
 template <typename T, int D>
 struct QueryLds {
     static constexpr int KT = sizeof(T) == 2 ? 64 : 32;
@@ -538,8 +541,8 @@ gdn_status launch(const BwdArgs& a, hipStream_t st)
 }
 
 // How the work of a block is cut up: until there are `want` workgroups (key pass of
-// eight packed prompts, 288 blocks: 571 us in all with four pieces, 598 us with
-// three, 796 us whole), but
+// eight packed prompts, 288 blocks, 563 us in all with four pieces: with three 5 %
+// longer, whole 39 %), but
 // pieces of `least` tiles at least (on average: `tiles` are those of a middle block).
 int parts_for(long long blocks, long long want, long long tiles, long long least, int most)
 {

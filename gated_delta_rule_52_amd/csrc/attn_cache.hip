@@ -5,9 +5,9 @@
 //
 // for i < R / 2, R the rotated width (the rest of a head passes through), p the
 // token's position in its sequence; fp32, rounded once.  Bound by HBM: q, k, v
-// are read once and written once (297 MB in 47 us, 6.3 TB/s, for 17.7 thousand
-// tokens of 16 + 2 x 4 heads of 128, bf16); single tokens are bound by the launch
-// (256 tokens: 3.9 us).
+// are read once and written once (17.7 thousand tokens of 16 + 2 x 4 heads of 128,
+// bf16, 297 MB: 51 us a pass on data that no cache holds, 5.9 TB/s); single tokens
+// are bound by the launch (256 tokens: 4.0 us).
 #include "attn.h"
 
 namespace gdn {
@@ -141,8 +141,10 @@ template <typename T>
 gdn_status launch(const AppendArgs& a, hipStream_t st)
 {
     // A workgroup a token while there are at most eight for a compute unit; then two
-    // tokens share one (17.7 thousand tokens: 47 us; one token 48 us, four 49 us) and,
-    // where they write more than the L2 holds (4 MB on each of 8 dies), it is not kept
+    // tokens share one, which few heads need (65536 tokens of one head of 64: 26 us,
+    // one a workgroup 42) and many do not mind (17.7 thousand of 24 heads of 128: 35
+    // and 33 us on warm caches, on cold ones 51.5 and 50.7, four a workgroup 54).
+    // Where they write more than the L2 holds (4 MB on each of 8 dies), it is not kept
     // there (192 MB: 59 us, kept 71 us; with the attention that then reads it 624 and
     // 621 us).  Up to there it is kept: this kernel takes longer (24 MB: 9.9 us, not kept
     // 8.1) and the attention gains more (62.4 us together, not kept 63.8).

@@ -305,7 +305,7 @@ struct Keys {
 // keeps the scores, the outputs and the queries of a row within the 256
 // registers that two waves a SIMD have (64 keys at once spilled: 412 us instead of
 // 295 us).  Bound by the matrix units and the card's power: 8192 tokens, 16 heads
-// over 4 of 128, bf16, take 297 us, 925 TFLOP/s.
+// over 4 of 128, bf16, take 297 to 312 us, 880 to 925 TFLOP/s.
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool PAGED>
 __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void attn_fwd_kernel(FwdArgs a)
@@ -421,8 +421,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
 // wave streams tiles of 32 keys of its own (every NW-th) through two LDS
 // buffers of its own, with no barrier between waves, and the waves' results
 // are joined at the end.  Bound by HBM over a cache: 256 sequences of up to 4097
-// keys, 16 heads over 4 of 128, bf16, take 261 us, 5.2 TB/s; two of up to 131073,
-// heads over 2, 39 us, 6.2 TB/s.
+// keys, 16 heads over 4 of 128, bf16, take 264 us, 5.1 TB/s; two of up to 131073,
+// heads over 2, 40 us, 6.1 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 struct Small {
@@ -673,7 +673,10 @@ gdn_status launch(const FwdArgs& a, const AttnPlan& p, bool paged, hipStream_t s
 // The key axis of a cache is cut into pieces where the blocks alone do not fill
 // the card: two workgroups of 32-row blocks fit a compute unit, and the 128-row
 // ones, whose work is uneven, end together best with somewhat more (chunks of 512
-// on 16384: 223 us for 896 workgroups, 231 us for 768, 240 us for 640).
+// on 16384, 219 us for 896 workgroups: 768 take 4 % longer, 640 8 %).  The room for
+// partial outputs bounds the pieces: it is laid out for all rows alike, so that a
+// long sequence among many short ones is cut into no more pieces than their number
+// leaves (none from 513 pairs of a sequence and a key head on).
 AttnPlan attn_plan(const gdn_attn_shape& s, bool paged)
 {
     AttnPlan p{};

@@ -14,8 +14,8 @@
 // norm unrounded (the backward forms it again from x and y, which it reads
 // anyway for da).  All of these are bound by HBM: each value is read once and
 // written once, as 16-byte words.  Forward and backward together move 503 MB at
-// 4.8 TB/s (block norm, 32768 x 768 bf16, 104 us) and 403 MB at 5.5 TB/s (gated
-// norm, 32768 x 6 x 128 bf16, 73 us); a copy of 256 MB reaches 5.4 TB/s.
+// 4.8 TB/s (block norm, 32768 x 768 bf16, 104 us) and 403 MB at 5.4 TB/s (gated
+// norm, 32768 x 6 x 128 bf16, 75 us); a copy of 256 MB reaches 5.5 TB/s.
 #include "common.h"
 #include "norm.h"
 
@@ -26,7 +26,7 @@ namespace {
 // A word of an output.  PAST: not to be kept in the L2, for outputs that it could
 // not hold until the next kernel anyway (past_l2).  At 32768 x 768 bf16 the block
 // norm forward and backward take 104 us with it and 113 us without, the gated
-// norm at 32768 x 6 x 128 75 us and 84 us (both with sums in 16 strips).
+// norm at 32768 x 6 x 128 75 us and 84 us.
 template <bool PAST> __device__ __forceinline__ void put(u32x4* p, u32x4 w)
 {
     if constexpr (PAST)
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(256, N <= 2 ? 4 : N == 3 ? 3 : N == 8 && sizeof(T) 
 
 // out[c] = sum over the nb rows of part[.][c]: 16 columns a workgroup, 64 row
 // strips (a strip's loads are what it waits for; with 16 the gated norm's training
-// case took 74.6 us instead of 73.4), then the strips in order
+// case took 1.6 % longer), then the strips in order
 __global__ __launch_bounds__(1024) void norm_finish_kernel(const float* __restrict__ part, float* __restrict__ out0,
                                                            float* __restrict__ out1, int nb, int width)
 {
