@@ -38,7 +38,7 @@ struct Queries {
     f32x16 o[DT];
     float m, l;   // running maximum of the raw scores; sum of this lane's own keys
     int limit;    // keys [0, limit) are seen
-    int rest;     // uniform: from which key on values may be left out (add_rest)
+    int rest0, rest1;  // uniform: the keys whose values the products may have left out (add_rest)
 
     __device__ __forceinline__ void load(const T* row)
     {
@@ -49,7 +49,7 @@ struct Queries {
         for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
         m = -INFINITY;
         l = 0.f;
-        rest = 0x7fffffff;
+        rest0 = 0x7fffffff, rest1 = 0;
     }
 
     // 32 keys of the tables from row r0; key0 is the position of the first.
@@ -78,7 +78,8 @@ struct Queries {
             // where there is any, the products take finite ones, and what they leave out
             // is added in the end.
             if (__builtin_expect(!all_finite(v), 0)) {
-                rest = rest < key0 ? rest : key0;
+                rest0 = rest0 < key0 ? rest0 : key0;
+                rest1 = key0 + 32;
 #pragma unroll
                 for (int i = 0; i < 2 * DT; ++i) v[i] = finite_only(v[i]);
             }
@@ -126,13 +127,14 @@ struct Queries {
         }
     }
 
-    // What the products left out of the values of keys rest .. end - 1.  `at`: a
-    // key's values, null for an absent one.
+    // What the products left out of the values, below key `end`.  `at`: a key's
+    // values, null for an absent one.
     template <typename F>
     __device__ __forceinline__ void add_rest(int end, F&& at)
     {
+        end = end < rest1 ? end : rest1;
 #pragma unroll 1
-        for (int key = rest; key < end; ++key) {
+        for (int key = rest0; key < end; ++key) {
             const T* v = at(key);
             if (v) add_nonfinite<T, D>(o, v, key < limit);
         }
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(256, (sizeof(T) == 4 && D == 128) ? 1 : 2) void att
         if (t + 1 < t1) tile(t + 1, std::integral_constant<int, 1>{});
     }
 
-    if (__builtin_expect(qs.rest < wmax, 0))
+    if (__builtin_expect(qs.rest1, 0))
         qs.add_rest(t1 * KT < wmax ? t1 * KT : wmax, [&](int key) { return keys.value(a, key); });
     const float sum = half_add(qs.l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -516,7 +518,7 @@ __global__ __launch_bounds__((Small<T, D>::NW * 64), 1) void attn_small_kernel(F
         }
     }
 
-    if (__builtin_expect(qs.rest < upto, 0))
+    if (__builtin_expect(qs.rest1, 0))
         qs.add_rest(t1 * 32 < upto ? t1 * 32 : upto, [&](int key) { return keys.value(a, key); });
     // join: out = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w
     __syncthreads();

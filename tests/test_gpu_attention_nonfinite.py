@@ -170,3 +170,30 @@ def test_paged_values(dtype, D, heads, new, whole):
         same(o, clean, slice(0, i), i)
         same(o, clean, slice(cu[1], None), i)
         seen_column(o, clean, slice(i, cu[1]), mine, col, i)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 150])
+def test_paged_beside_a_missing_page(dtype, new):
+    """Values of cached tokens in tiles that a missing page makes masked ones: seen
+    by every new token, in their column alone; in a missing page itself: by none."""
+    import gated_delta_rule_52_amd as gdn
+    dt, D, page, whole = DT[dtype], 64, 16, [400, 700]
+    log(f"not finite beside a missing page {dtype} new={new}")
+    kc, vc, table = make_cache(whole, page, 2, D, dt)
+    gone = vc.clone()
+    gone[int(table[0, 2]), 3, 1, 9] = NAN  # in page 2 of sequence 0, which is taken out
+    table[0, 2] = table[1, 7] = -1
+    q, cu = rand(2 * new, 4, D, dtype=dt), ints([0, new, 2 * new])
+    clean = gdn.gdn_attn_paged(q, kc, vc, table, cu, ints(whole))
+    assert torch.isfinite(clean.float()).all()
+    assert torch.equal(gdn.gdn_attn_paged(q, kc, gone, table, cu, ints(whole)), clean)
+    for n, (b, pos) in enumerate([(0, 50), (0, 63), (1, 96), (1, 111)]):  # pages 3 and 6, beside the missing ones
+        value = list(VALUES.values())[n % 3]
+        bad = vc.clone()
+        bad[int(table[b, pos // page]), pos % page, 1, 5] = value
+        o = gdn.gdn_attn_paged(q, kc, bad, table, cu, ints(whole))
+        rows, others = slice(b * new, (b + 1) * new), slice((1 - b) * new, (2 - b) * new)
+        same(o, clean, others, (b, pos))
+        assert torch.equal(o[rows, :2], clean[rows, :2])
+        seen_column(o, clean, rows, [2, 3], 5, (b, pos))
