@@ -26,7 +26,9 @@ The operators that stand around the layer in a stack with softmax-attention
 layers (norms before and after a block, packed attention with its gradients, a
 paged cache) are in block.py and are names of this package too: gdn_norm_block,
 gdn_norm_gate, gdn_attn_forward, gdn_attn_append, gdn_attn_paged and the
-backward calls.
+backward calls.  The short causal convolution, the selective state space scan and
+the page step of the paged cache (gdn_conv_*, gdn_ssm_*, gdn_pages_*) are in
+mixer.py.
 """
 from __future__ import annotations
 
@@ -53,7 +55,11 @@ EXPORTS = ("gdn_new_state", "gdn_workspace_bytes", "gdn_forward", "gdn_forward_n
            # the operators around the layer (block.py)
            "gdn_norm_workspace_bytes", "gdn_norm_block", "gdn_norm_block_backward", "gdn_norm_gate",
            "gdn_norm_gate_backward", "gdn_attn_workspace_bytes", "gdn_attn_forward",
-           "gdn_attn_backward", "gdn_attn_append", "gdn_attn_paged")
+           "gdn_attn_backward", "gdn_attn_append", "gdn_attn_paged",
+           # a state-space layer and the page step (mixer.py)
+           "gdn_conv_workspace_bytes", "gdn_conv_forward", "gdn_conv_backward", "gdn_conv_step",
+           "gdn_ssm_workspace_bytes", "gdn_ssm_forward", "gdn_ssm_backward", "gdn_ssm_step",
+           "gdn_pages_release", "gdn_pages_take")
 # include/gdn_profile.h: exported by the measurement build only
 PROFILE_EXPORTS = ("gdn_profile_begin", "gdn_profile_end", "gdn_profile_launch_name")
 
@@ -128,6 +134,7 @@ def lib():
         L.gdn_status_string.argtypes = [i]
         L.gdn_status_string.restype = ctypes.c_char_p
         block.declare(L)
+        mixer.declare(L)
         _lib = L
     return _lib
 
@@ -444,3 +451,7 @@ from . import block  # noqa: E402  (it takes the names above)
 from .block import (GDN_ATTN_BACKWARD, GDN_ATTN_PAGED, GdnAttnShape, GdnNormShape,  # noqa: E402,F401
                     gdn_attn_append, gdn_attn_backward, gdn_attn_forward, gdn_attn_paged, gdn_norm_block,
                     gdn_norm_block_backward, gdn_norm_gate, gdn_norm_gate_backward)
+from . import mixer  # noqa: E402
+from .mixer import (GDN_SSM_BACKWARD, GDN_SSM_FORWARD, GdnConvShape, GdnPagesShape, GdnSsmShape,  # noqa: E402,F401
+                    gdn_conv_backward, gdn_conv_forward, gdn_conv_step, gdn_pages_release, gdn_pages_take,
+                    gdn_ssm_backward, gdn_ssm_forward, gdn_ssm_step)

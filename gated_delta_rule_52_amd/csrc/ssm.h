@@ -1,0 +1,60 @@
+// ssm.h -- arguments, plans and dispatch of the selective state space scan
+// (ssm_*.hip), for mixer_api.hip.
+//
+// The scan, of head h in group h / (H / G):
+//   delta = softplus(dt + bias) or dt + bias,  g = delta A,
+//   S_t = exp(g_t) S_{t-1} + delta_t B_t x_t^T,   y_t = S_t^T C_t + D x_t
+// is computed in chunks of L tokens.  With c the running sum of g in a chunk and
+// E_ts = exp(c_t - c_s) for s <= t, 0 otherwise,
+//   y = (E o C B^T) (delta x) + exp(c) C S_in + D x,
+//   S_out = exp(c_L) S_in + B^T (exp(c_L - c) delta x):
+// all of it matrix products.  A head's P values are independent of one another,
+// so everything is done in slices of 64 of them.  The states between chunks
+// (ssm_walk.hip) are formed first; outputs (ssm_out.hip) and gradients
+// (ssm_grad.hip) are then independent chunk by chunk.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+constexpr int kSlice = 64;  // values of a head that are worked on together
+
+struct SsmArgs {
+    const void *x, *B, *C, *dy;
+    const float *dt, *A, *D, *bias;
+    const int* cu;
+    const float *h0, *dhT;
+    void* y;
+    float *hT, *dh0;
+    void *dx, *dB, *dC;
+    float *ddt, *dA, *dD, *dbias;
+    long long xs, bs, cs;  // elements between tokens of x, B, C
+    int nb, T, H, G, P, softplus;
+};
+
+// How a call is laid out, from its sizes alone (the lengths are device data).
+struct SsmPlan {
+    int L;              // tokens of a chunk
+    int slices;         // H P / 64
+    long long chunks;   // at most, over all sequences
+    long long between;  // states between chunks, at most
+    int seg;            // chunks of a segment; 0: a sequence is one segment
+    long long segs;     // at most, over all sequences
+    int splits;         // parts into which the heads of a group are dealt in the gradients
+    size_t seg_at, tot_at, fwd_at, back_at, sum_at, part_at, bytes;  // offsets in the workspace
+};
+SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward);
+
+// Walk over the chunks (see ssm_walk.hip): states between chunks into `between`,
+// the last one into hT / dh0.
+enum { WALK_OUT = 0, WALK_GRAD = 1, WALK_BACK = 2 };
+gdn_status ssm_walk(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, int kind, char* ws, hipStream_t st);
+gdn_status ssm_out(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
+gdn_status ssm_grad(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
+gdn_status ssm_step(const gdn_ssm_shape& s, const SsmArgs& a, float* state, hipStream_t st);
+
+}  // namespace gdn

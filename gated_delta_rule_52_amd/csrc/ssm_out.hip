@@ -1,0 +1,185 @@
+// ssm_out.hip -- outputs of the selective state space scan, chunk by chunk, from
+// the states between them (ssm_walk.hip):
+//
+//   y_t = sum_{s <= t} exp(c_t - c_s) (C_t . B_s) delta_s x_s + exp(c_t) C_t S_in + D x_t
+//
+// A workgroup has a chunk and some of the slices (64 values of a head) of a group;
+// a wave has 32 of the chunk's tokens.  It computes B C^T, so that a lane is one t
+// and its registers are the s: the decay, the causal limit and delta are applied
+// there, and the result is the next product's operand as it stands.  That product
+// gives y^T, so that a lane stores neighbouring values of its token.
+#include "ssm_tile.h"
+
+#include "common.h"
+
+namespace gdn {
+
+namespace {
+
+struct OutArgs {
+    const void *x, *B, *C;
+    const float *dt, *A, *D, *bias;
+    const int* cu;
+    const void* between;  // [states][slices][64][N], then each sequence's first
+    void* y;
+    long long xs, bs, cs, firsts;
+    int nb, T, H, P, per_group, slices, parts, plus, first;
+};
+
+template <typename T, int N>
+__global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(OutArgs a)
+{
+    constexpr int L = SsmTile<T>::L, NW = L / 32, KN = N / 16;
+    using NTab = Rows<T, N>;
+    using VTab = Rows<T, kSlice>;
+    __shared__ __align__(16) char b_s[L * NTab::BYTES];
+    __shared__ __align__(16) char x_s[L * VTab::BYTES];
+    __shared__ __align__(16) char s_s[kSlice * NTab::BYTES];
+    __shared__ __align__(16) float hi_s[L], lo_s[L], d_s[L];
+
+    long long id;
+    int part;
+    deal(blockIdx.x, a.parts, id, part);
+    Unit u;
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, id, u)) return;
+    const int c = u.at, live = u.n - c * L < L ? u.n - c * L : L;
+    const size_t row0 = (size_t)u.start + (size_t)c * L;
+    const int l = lane_id(), h = l >> 5, w = uniform(wave_id());
+    // later rows have more to do: the order is turned round from block to block,
+    // for the waves of two workgroups on one SIMD
+    const int rb = (blockIdx.x >> 3) & 1 ? NW - 1 - w : w;
+    const int per_head = a.P / kSlice, s_first = (int)((long long)part * a.slices / a.parts),
+              s_last = (int)((long long)(part + 1) * a.slices / a.parts);
+
+    Frag<T> cf[KN];
+    int group = -1;
+    for (int slice = s_first; slice < s_last; ++slice) {
+        const int head = slice / per_head, p0 = (slice - head * per_head) * kSlice, g = head / a.per_group;
+        const bool state = c > 0 || a.first;
+        if (slice != s_first) __syncthreads();  // the tables are read
+        if (g != group) {
+            group = g;
+            const T* b = (const T*)a.B + row0 * a.bs + (size_t)g * N;
+            for (int r = 16 * w; r < L; r += 16 * NW) {
+                const int rr = r < live ? r : live - 1;
+                NTab::template fetch<16>(b_s, r, b + (size_t)rr * a.bs, (uint32_t)(a.bs * sizeof(T)), live - 1 - rr);
+            }
+            const int t = 32 * rb + (l & 31);
+            const T* cp = (const T*)a.C + (row0 + (t < live ? t : live - 1)) * a.cs + (size_t)g * N + 8 * h;
+#pragma unroll
+            for (int kk = 0; kk < KN; ++kk) cf[kk] = load_frag<T>(cp + 16 * kk);
+        }
+        {
+            const T* x = (const T*)a.x + row0 * a.xs + (size_t)head * a.P + p0;
+            for (int r = 16 * w; r < L; r += 16 * NW) {
+                const int rr = r < live ? r : live - 1;
+                VTab::template fetch<16>(x_s, r, x + (size_t)rr * a.xs, (uint32_t)(a.xs * sizeof(T)), live - 1 - rr);
+            }
+        }
+        if (state) {
+            const T* s = (const T*)a.between + ((size_t)(c > 0 ? u.between + c - 1 : a.firsts + u.b) * a.slices + slice) * kSlice * N;
+            for (int r = 16 * w; r < kSlice; r += 16 * NW)
+                NTab::template fetch<16>(s_s, r, s + (size_t)r * N, (uint32_t)(N * sizeof(T)), 15);
+        }
+        if (w == 0) {
+            Decays<L> dec;
+            dec.load(a.dt + row0 * a.H + head, a.H, live, a.bias ? a.bias[head] : 0.f);
+            dec.scan(a.A[head], a.plus, live);
+#pragma unroll
+            for (int k = 0; k < Decays<L>::K; ++k) {
+                const int t = Decays<L>::K * l + k;
+                const float hi = (float)dec.c[k];
+                hi_s[t] = hi;
+                lo_s[t] = (float)(dec.c[k] - (double)hi);
+                d_s[t] = dec.d[k];
+            }
+        }
+        wait_vm<0>();
+        __syncthreads();
+        if (32 * rb >= live) continue;  // no token of this wave's
+
+        const int t = 32 * rb + (l & 31);
+        const float ht = hi_s[t], lt = lo_s[t], skip = a.D ? a.D[head] : 0.f;
+        f32x16 acc[2] = {zero16(), zero16()};
+        if (state) {
+#pragma unroll
+            for (int kk = 0; kk < KN; ++kk)
+#pragma unroll
+                for (int pt = 0; pt < 2; ++pt) acc[pt] = mma32(NTab::along(s_s, 32 * pt, kk), cf[kk], acc[pt]);
+            const float e = exp2_hw(ht + lt);
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[pt][r] *= e;
+        }
+        for (int sb = 0; sb <= rb; ++sb) {
+            f32x16 m = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KN; ++kk) m = mma32(NTab::along(b_s, 32 * sb, kk), cf[kk], m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int s = 32 * sb + acc_rows(i);
+                const f32x4 hs = *reinterpret_cast<const f32x4*>(hi_s + s), ls = *reinterpret_cast<const f32x4*>(lo_s + s),
+                            ds = *reinterpret_cast<const f32x4*>(d_s + s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float v = m[4 * i + j] * (exp2_hw((ht - hs[j]) + (lt - ls[j])) * ds[j]);
+                    m[4 * i + j] = s + j <= t ? v : 0.f;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const Frag<T> v = acc_frag<T>(m, b);
+#pragma unroll
+                for (int pt = 0; pt < 2; ++pt) acc[pt] = mma32(VTab::down(x_s, 32 * sb + 16 * b, 32 * pt), v, acc[pt]);
+            }
+        }
+        if (t < live) {
+            T* y = (T*)a.y + ((row0 + t) * a.H + head) * a.P + p0;
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = 32 * pt + acc_rows(i);
+                    f32x4 v{acc[pt][4 * i], acc[pt][4 * i + 1], acc[pt][4 * i + 2], acc[pt][4 * i + 3]};
+                    if (a.D) {
+                        const f32x4 x = row4<T, kSlice>(x_s, t, p);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(skip, x[j], v[j]);
+                    }
+                    store4<T>(y + p, v[0], v[1], v[2], v[3]);
+                }
+        }
+    }
+}
+
+template <typename T, int N> gdn_status out(const SsmPlan& p, OutArgs a, hipStream_t st)
+{
+    // slices of a chunk that share its B and C: as many workgroups as there are
+    // slices while they are few, then about four a compute unit
+    int parts = a.slices;
+    while (parts > 1 && p.chunks * (parts / 2) >= 1024) parts /= 2;
+    a.parts = parts;
+    const dim3 grid((unsigned)((p.chunks + 7) / 8 * 8 * parts));
+    GDN_LAUNCH("ssm_out", (ssm_out_kernel<T, N>), grid, dim3(64 * (SsmTile<T>::L / 32)), st, a);
+    return GDN_OK;
+}
+
+}  // namespace
+
+gdn_status ssm_out(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& x, char* ws, hipStream_t st)
+{
+    OutArgs a{};
+    a.x = x.x; a.B = x.B; a.C = x.C;
+    a.dt = x.dt; a.A = x.A; a.D = x.D; a.bias = x.bias; a.cu = x.cu;
+    a.between = ws + p.fwd_at;
+    a.firsts = p.between;
+    a.first = x.h0 != nullptr;
+    a.y = x.y;
+    a.xs = x.xs; a.bs = x.bs; a.cs = x.cs;
+    a.nb = s.B; a.T = s.T; a.H = s.H; a.P = s.P; a.per_group = s.H / s.G; a.slices = p.slices; a.plus = s.softplus;
+    if (s.dtype == GDN_BF16) return s.N == 64 ? out<bf16, 64>(p, a, st) : out<bf16, 128>(p, a, st);
+    return s.N == 64 ? out<float, 64>(p, a, st) : out<float, 128>(p, a, st);
+}
+
+}  // namespace gdn

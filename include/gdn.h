@@ -407,6 +407,143 @@ gdn_status gdn_attn_paged(const gdn_attn_shape *shape, const void *q, const void
                           const void *v_cache, const int *page_table, const int *cu_seqlens,
                           const int *kv_len, void *o, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A state-space layer's operators, and the page step that feeds all layers.  The
+ * conventions of the part above hold: sequences are packed, cu_seqlens and every
+ * other int array are device data, clamped or checked where they are used, and
+ * rows of no sequence are neither used nor written.  Weights, steps and states of
+ * the scan are float32 (4-byte aligned where they are per head).
+ * ---------------------------------------------------------------------------
+ *
+ * Short causal convolution along the tokens, every channel by itself: with e the
+ * W - 1 rows of a sequence's state (NULL: zeros) followed by its rows of x,
+ *   z_t = bias + sum_j weight[.][j] e_{t+j},   y = z / (1 + exp(-z)) (silu) or z,
+ * and the new state is the last W - 1 rows of e, as they are.
+ *   x [T, C] (dtype) with x_stride elements between tokens (0 = dense), y, dy, dx
+ *   [T, C] dense; weight, dweight [C, W], bias, dbias [C] float32 (bias may be
+ *   NULL); states [B, W - 1, C] (dtype), oldest row first.
+ * W is 2, 3 or 4; C a multiple of 8 (bf16) or 4 (float32), at most 2^20; T at most
+ * 2^28, B at most 2^26.  y may not be x, nor dx x or dy.
+ *
+ * gdn_conv_forward: state_out (NULL: not written) may be state.  A sequence
+ * without rows keeps its state.
+ * gdn_conv_backward: dx, dweight, dbias (may be NULL) and dstate (may be NULL) from
+ * dy and dstate_out, the gradient that arrives at the new state (NULL = zero).  ws
+ * holds gdn_conv_workspace_bytes(shape) bytes.
+ * gdn_conv_step: one row a sequence (T = B, row b is sequence b's); state is
+ * updated in place.
+ */
+typedef struct {
+    int B, T, C, W;
+    int dtype;          /* gdn_dtype */
+    int silu;           /* 1: y = z / (1 + exp(-z)); 0: y = z */
+    long long x_stride; /* elements between tokens of x, 0 = C */
+} gdn_conv_shape;
+
+size_t gdn_conv_workspace_bytes(const gdn_conv_shape *shape);
+gdn_status gdn_conv_forward(const gdn_conv_shape *shape, const void *x, const float *weight,
+                            const float *bias, const int *cu_seqlens, const void *state, void *y,
+                            void *state_out, void *stream);
+gdn_status gdn_conv_backward(const gdn_conv_shape *shape, const void *x, const float *weight,
+                             const float *bias, const int *cu_seqlens, const void *state,
+                             const void *dy, const void *dstate_out, void *dx, float *dweight,
+                             float *dbias, void *dstate, void *ws, size_t ws_bytes, void *stream);
+gdn_status gdn_conv_step(const gdn_conv_shape *shape, const void *x, const float *weight,
+                         const float *bias, void *state, void *y, void *stream);
+
+/*
+ * Selective state space scan.  Head h of H, in group h / (H / G) of G, keeps a
+ * state S [N x P] and for each token applies
+ *   delta = log(1 + exp(dt + dt_bias)) (softplus) or dt + dt_bias,
+ *   S <- exp(delta A) S + delta B x^T,   y = S^T C + D x.
+ *   x, y, dy, dx [T, H, P], B, C, dB, dC [T, G, N] (dtype): x, B and C dense within
+ *   a token, with x_stride, b_stride, c_stride elements between tokens (0 = dense;
+ *   slices of a convolution's output otherwise), the others dense; dt, ddt [T, H],
+ *   A, D, dt_bias and their gradients [H], states [B, H, N, P] float32.
+ * D, dt_bias and h0 (zero state) may be NULL; A is meant to be negative, but is
+ * not tested.  N and P in {64, 128}; H a multiple of G, at most 1024; T * H < 2^27,
+ * B * H < 2^23; strides at most 2^24.
+ * A value that is not finite reaches no other sequence and no other head's output;
+ * within a sequence and head it may reach the other results of its chunk of 128
+ * tokens (float32: 64), the earlier ones among them.
+ *
+ * gdn_ssm_forward: y, and hT the state behind each sequence (NULL: not written; may
+ * be h0; a sequence without rows keeps its state).
+ * gdn_ssm_backward: gradients of sum(y dy) + sum(hT dhT) (dhT NULL = zero); dD,
+ * ddt_bias and dh0 may be NULL, and dh0 may not be dhT.  The states are formed
+ * again; nothing is kept between the calls.  Float32 results, and hT, are as exact
+ * for bf16 inputs as for the same values in float32.
+ * Both: ws holds gdn_ssm_workspace_bytes(shape, GDN_SSM_...) bytes; calls that
+ * overlap must not share one.
+ * gdn_ssm_step: one token a sequence (T = B, row b is sequence b's), the state
+ * updated in place.
+ */
+typedef struct {
+    int B, T, H, G, N, P;
+    int dtype;    /* gdn_dtype */
+    int softplus; /* 1: delta = softplus(dt + dt_bias); 0: dt + dt_bias */
+    long long x_stride, b_stride, c_stride; /* elements between tokens, 0 = dense */
+} gdn_ssm_shape;
+
+enum { GDN_SSM_FORWARD = 0, GDN_SSM_BACKWARD = 1 };
+
+size_t gdn_ssm_workspace_bytes(const gdn_ssm_shape *shape, int call);
+gdn_status gdn_ssm_forward(const gdn_ssm_shape *shape, const void *x, const float *dt,
+                           const float *A, const void *B, const void *C, const float *D,
+                           const float *dt_bias, const int *cu_seqlens, const float *h0, void *y,
+                           float *hT, void *ws, size_t ws_bytes, void *stream);
+gdn_status gdn_ssm_backward(const gdn_ssm_shape *shape, const void *x, const float *dt,
+                            const float *A, const void *B, const void *C, const float *D,
+                            const float *dt_bias, const int *cu_seqlens, const float *h0,
+                            const void *dy, const float *dhT, void *dx, float *ddt, float *dA,
+                            void *dB, void *dC, float *dD, float *ddt_bias, float *dh0, void *ws,
+                            size_t ws_bytes, void *stream);
+gdn_status gdn_ssm_step(const gdn_ssm_shape *shape, const void *x, const float *dt, const float *A,
+                        const void *B, const void *C, const float *D, const float *dt_bias,
+                        float *state, void *y, void *stream);
+
+/*
+ * The page step of continuous batching, for the paged cache above.  A pool of
+ * num_pages pages; the free ones are free_pages[0 .. free_count[0] - 1], a stack
+ * whose top is its end.  kv_len [B] counts the positions that each sequence has;
+ * its pages are the first ceil(kv_len / page_size) entries of its row of page_table
+ * [B, max_pages].  All arrays int32 device memory, but for slots (int64).
+ *
+ * gdn_pages_release: the pages of every sequence with done[b] != 0 go on the stack,
+ * in the order of the sequences and of their tables, and its length becomes 0 (the
+ * table keeps its entries, which no position names any more).
+ *
+ * gdn_pages_take: sequence b asks for want[b] new tokens (below 0: none) and gets
+ * all of them or none.  It gets them if its pages fit its row of the table; if the
+ * stack holds the pages that it and those before it whose rows fit need (or it
+ * needs none); and if `rows` holds the tokens of it and of those before it that
+ * pass the first two tests.  Its new pages come from the top of the stack, one
+ * after the other, and are entered in the table.  kv_out = kv_len + the tokens it
+ * gets; cu_seqlens [B + 1] their running sum, from 0; and for the tokens, packed in
+ * that order, positions [rows] (in the sequence) and slots [rows] (page *
+ * page_size + place in the page, -1 without a page), either of which may be NULL;
+ * rows behind the last token stay as they were.  kv_out, cu_seqlens and page_table
+ * are what gdn_attn_append and gdn_attn_paged take.
+ *
+ * kv_out and count_out may be kv_len and free_count: then both are updated in
+ * place, by a launch of its own.  B at most 8192, page_size and max_pages as above.
+ * A free_count outside 0 .. num_pages is taken as the nearest of them, a length
+ * below 0 as 0.
+ */
+typedef struct {
+    int B, num_pages, page_size, max_pages;
+    int rows; /* gdn_pages_take: the most tokens */
+} gdn_pages_shape;
+
+gdn_status gdn_pages_release(const gdn_pages_shape *shape, const int *done, const int *kv_len,
+                             const int *page_table, int *free_pages, const int *free_count,
+                             int *kv_out, int *count_out, void *stream);
+gdn_status gdn_pages_take(const gdn_pages_shape *shape, const int *want, const int *kv_len,
+                          int *page_table, const int *free_pages, const int *free_count,
+                          int *kv_out, int *count_out, int *cu_seqlens, int *positions,
+                          long long *slots, void *stream);
+
 /* gdn_status_string -- static, human-readable name of a status code. */
 const char *gdn_status_string(gdn_status status);
 
