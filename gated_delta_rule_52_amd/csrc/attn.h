@@ -267,9 +267,9 @@ struct Rows {
     // the same in all lanes.  Away from a sequence's end the lanes' offsets do
     // not change from call to call: only the scalar base moves.
     template <int N>
-    static __device__ __forceinline__ void fetch(void* tab, int r0, const void* base, uint32_t stride, int last)
+    static __device__ __forceinline__ void fetch(void* tab, int r0, const void* base, uint32_t stride, int last,
+                                                 int l = lane_id())
     {
-        const int l = lane_id();
         char* to = reinterpret_cast<char*>(tab) + r0 * BYTES;
         if (last >= N - 1) {
 #pragma unroll

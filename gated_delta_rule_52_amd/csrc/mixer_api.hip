@@ -171,7 +171,9 @@ gdn_status gdn_ssm_forward(const gdn_ssm_shape* sh, const void* x, const float* 
     a.x = x; a.B = B; a.C = C; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.y = y; a.hT = hT;
     a.xs = s.x_stride; a.bs = s.b_stride; a.cs = s.c_stride;
-    r = ssm_walk(s, p, a, WALK_OUT, (char*)ws, (hipStream_t)stream);
+    r = ssm_prep(s, p, a, (char*)ws, (hipStream_t)stream);
+    if (r != GDN_OK) return r;
+    r = ssm_walk(s, p, a, false, (char*)ws, (hipStream_t)stream);
     if (r != GDN_OK || !s.T) return r;
     return ssm_out(s, p, a, (char*)ws, (hipStream_t)stream);
 }
@@ -198,11 +200,13 @@ gdn_status gdn_ssm_backward(const gdn_ssm_shape* sh, const void* x, const float*
     a.x = x; a.B = B; a.C = C; a.dy = dy; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.dhT = dhT; a.dx = dx; a.dB = dB; a.dC = dC; a.ddt = ddt; a.dA = dA; a.dD = dD; a.dbias = ddt_bias; a.dh0 = dh0;
     a.xs = s.x_stride; a.bs = s.b_stride; a.cs = s.c_stride;
-    r = ssm_walk(s, p, a, WALK_GRAD, (char*)ws, (hipStream_t)stream);
+    r = ssm_prep(s, p, a, (char*)ws, (hipStream_t)stream);
     if (r != GDN_OK) return r;
-    r = ssm_walk(s, p, a, WALK_BACK, (char*)ws, (hipStream_t)stream);
+    r = ssm_walk(s, p, a, true, (char*)ws, (hipStream_t)stream);
     if (r != GDN_OK) return r;
-    return ssm_grad(s, p, a, (char*)ws, (hipStream_t)stream);
+    r = ssm_grad(s, p, a, (char*)ws, (hipStream_t)stream);
+    if (r != GDN_OK) return r;
+    return ssm_finish(s, p, a, (char*)ws, (hipStream_t)stream);
 }
 
 gdn_status gdn_ssm_step(const gdn_ssm_shape* sh, const void* x, const float* dt, const float* A, const void* B,

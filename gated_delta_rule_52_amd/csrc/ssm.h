@@ -9,8 +9,8 @@
 //   y = (E o C B^T) (delta x) + exp(c) C S_in + D x,
 //   S_out = exp(c_L) S_in + B^T (exp(c_L - c) delta x):
 // all of it matrix products.  A head's P values are independent of one another,
-// so everything is done in slices of 64 of them.  The states between chunks
-// (ssm_walk.hip) are formed first; outputs (ssm_out.hip) and gradients
+// so everything is done in slices of 64 of them.  The decays
+// (ssm_prep.hip) and the states between chunks (ssm_walk.hip) are formed first; outputs (ssm_out.hip) and gradients
 // (ssm_grad.hip) are then independent chunk by chunk.
 #pragma once
 
@@ -45,16 +45,18 @@ struct SsmPlan {
     int seg;            // chunks of a segment; 0: a sequence is one segment
     long long segs;     // at most, over all sequences
     int splits;         // parts into which the heads of a group are dealt in the gradients
-    size_t seg_at, tot_at, fwd_at, back_at, sum_at, part_at, bytes;  // offsets in the workspace
+    size_t dec_at, seg_at, tot_at, fwd_at, back_at, token_at, sum_at, part_at, bytes;  // offsets in the workspace
 };
 SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward);
 
-// Walk over the chunks (see ssm_walk.hip): states between chunks into `between`,
-// the last one into hT / dh0.
-enum { WALK_OUT = 0, WALK_GRAD = 1, WALK_BACK = 2 };
-gdn_status ssm_walk(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, int kind, char* ws, hipStream_t st);
+// The decays of every chunk and head; the walk over the chunks (states between them,
+// and the last one into hT; for the gradients forward and backward, and dh0).
+gdn_status ssm_prep(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
+gdn_status ssm_walk(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, bool backward, char* ws, hipStream_t st);
 gdn_status ssm_out(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
 gdn_status ssm_grad(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
+// the gradients of dt, A, D and dt_bias, behind ssm_grad
+gdn_status ssm_finish(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& a, char* ws, hipStream_t st);
 gdn_status ssm_step(const gdn_ssm_shape& s, const SsmArgs& a, float* state, hipStream_t st);
 
 }  // namespace gdn

@@ -18,12 +18,12 @@ namespace {
 
 struct OutArgs {
     const void *x, *B, *C;
-    const float *dt, *A, *D, *bias;
+    const float *dec, *D;
     const int* cu;
     const void* between;  // [states][slices][64][N], then each sequence's first
     void* y;
     long long xs, bs, cs, firsts;
-    int nb, T, H, P, per_group, slices, parts, plus, first;
+    int nb, T, H, P, per_group, slices, parts, first;
 };
 
 template <typename T, int N>
@@ -32,10 +32,11 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
     constexpr int L = SsmTile<T>::L, NW = L / 32, KN = N / 16;
     using NTab = Rows<T, N>;
     using VTab = Rows<T, kSlice>;
+    using VRead = Reads<T, kSlice>;
     __shared__ __align__(16) char b_s[L * NTab::BYTES];
     __shared__ __align__(16) char x_s[L * VTab::BYTES];
     __shared__ __align__(16) char s_s[kSlice * NTab::BYTES];
-    __shared__ __align__(16) float hi_s[L], lo_s[L], d_s[L];
+    __shared__ __align__(16) float hi_s[L], lo_s[L], d_s[L], behind_s[L];
 
     long long id;
     int part;
@@ -81,24 +82,21 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
             for (int r = 16 * w; r < kSlice; r += 16 * NW)
                 NTab::template fetch<16>(s_s, r, s + (size_t)r * N, (uint32_t)(N * sizeof(T)), 15);
         }
-        if (w == 0) {
-            Decays<L> dec;
-            dec.load(a.dt + row0 * a.H + head, a.H, live, a.bias ? a.bias[head] : 0.f);
-            dec.scan(a.A[head], a.plus, live);
-#pragma unroll
-            for (int k = 0; k < Decays<L>::K; ++k) {
-                const int t = Decays<L>::K * l + k;
-                const float hi = (float)dec.c[k];
-                hi_s[t] = hi;
-                lo_s[t] = (float)(dec.c[k] - (double)hi);
-                d_s[t] = dec.d[k];
-            }
+        const float* dec = a.dec + ((size_t)id * a.H + head) * kDecays<L>;
+        if (threadIdx.x < L) {
+            const int t = threadIdx.x;
+            const float d = dec[DEC_DELTA * L + t];
+            hi_s[t] = dec[DEC_HI * L + t];
+            lo_s[t] = dec[DEC_LO * L + t];
+            d_s[t] = d;
+            behind_s[t] = dec[DEC_BEHIND * L + t] * d;
         }
+        const int t = 32 * rb + (l & 31);
+        const float et = dec[DEC_E * L + t], ahead = dec[DEC_AHEAD * L + t];
         wait_vm<0>();
         __syncthreads();
         if (32 * rb >= live) continue;  // no token of this wave's
 
-        const int t = 32 * rb + (l & 31);
         const float ht = hi_s[t], lt = lo_s[t], skip = a.D ? a.D[head] : 0.f;
         f32x16 acc[2] = {zero16(), zero16()};
         if (state) {
@@ -106,25 +104,39 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
             for (int kk = 0; kk < KN; ++kk)
 #pragma unroll
                 for (int pt = 0; pt < 2; ++pt) acc[pt] = mma32(NTab::along(s_s, 32 * pt, kk), cf[kk], acc[pt]);
-            const float e = exp2_hw(ht + lt);
+            if (sizeof(T) == 2) order_products<2 * KN, 1, 4>();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[pt][r] *= e;
+                for (int r = 0; r < 16; ++r) acc[pt][r] *= et;
         }
         for (int sb = 0; sb <= rb; ++sb) {
             f32x16 m = zero16();
 #pragma unroll
             for (int kk = 0; kk < KN; ++kk) m = mma32(NTab::along(b_s, 32 * sb, kk), cf[kk], m);
+            if (sizeof(T) == 2) order_products<KN, 1, 4>();
+            __builtin_amdgcn_sched_barrier(0);
+            if (sb < rb) {
+                const int end = 32 * sb + 31, from = 32 * rb - 1;  // c from the one block's end to the other's start
+                const float f = ahead * exp2_hw((hi_s[from] - hi_s[end]) + (lo_s[from] - lo_s[end]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = 32 * sb + acc_rows(i);
-                const f32x4 hs = *reinterpret_cast<const f32x4*>(hi_s + s), ls = *reinterpret_cast<const f32x4*>(lo_s + s),
-                            ds = *reinterpret_cast<const f32x4*>(d_s + s);
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 bs = *reinterpret_cast<const f32x4*>(behind_s + 32 * sb + acc_rows(i));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float v = m[4 * i + j] * (exp2_hw((ht - hs[j]) + (lt - ls[j])) * ds[j]);
-                    m[4 * i + j] = s + j <= t ? v : 0.f;
+                    for (int j = 0; j < 4; ++j) m[4 * i + j] *= f * bs[j];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int s = 32 * sb + acc_rows(i);
+                    const f32x4 hs = *reinterpret_cast<const f32x4*>(hi_s + s), ls = *reinterpret_cast<const f32x4*>(lo_s + s),
+                                ds = *reinterpret_cast<const f32x4*>(d_s + s);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // pairs that are none: exp2(-inf)
+                        m[4 * i + j] *= exp2_hw(s + j <= t ? (ht - hs[j]) + (lt - ls[j]) : -INFINITY) * ds[j];
+                    }
                 }
             }
 #pragma unroll
@@ -133,9 +145,12 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
 #pragma unroll
                 for (int pt = 0; pt < 2; ++pt) acc[pt] = mma32(VTab::down(x_s, 32 * sb + 16 * b, 32 * pt), v, acc[pt]);
             }
+            if (sizeof(T) == 2) order_products<4, 2, 4>();
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (t < live) {
             T* y = (T*)a.y + ((row0 + t) * a.H + head) * a.P + p0;
+            const uint32_t xr = VRead::row_at(t);
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
@@ -143,7 +158,7 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
                     const int p = 32 * pt + acc_rows(i);
                     f32x4 v{acc[pt][4 * i], acc[pt][4 * i + 1], acc[pt][4 * i + 2], acc[pt][4 * i + 3]};
                     if (a.D) {
-                        const f32x4 x = row4<T, kSlice>(x_s, t, p);
+                        const f32x4 x = VRead::row4(x_s, xr, pt, i);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(skip, x[j], v[j]);
                     }
@@ -171,13 +186,14 @@ gdn_status ssm_out(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& x, c
 {
     OutArgs a{};
     a.x = x.x; a.B = x.B; a.C = x.C;
-    a.dt = x.dt; a.A = x.A; a.D = x.D; a.bias = x.bias; a.cu = x.cu;
+    a.dec = (const float*)(ws + p.dec_at);
+    a.D = x.D; a.cu = x.cu;
     a.between = ws + p.fwd_at;
     a.firsts = p.between;
     a.first = x.h0 != nullptr;
     a.y = x.y;
     a.xs = x.xs; a.bs = x.bs; a.cs = x.cs;
-    a.nb = s.B; a.T = s.T; a.H = s.H; a.P = s.P; a.per_group = s.H / s.G; a.slices = p.slices; a.plus = s.softplus;
+    a.nb = s.B; a.T = s.T; a.H = s.H; a.P = s.P; a.per_group = s.H / s.G; a.slices = p.slices;
     if (s.dtype == GDN_BF16) return s.N == 64 ? out<bf16, 64>(p, a, st) : out<bf16, 128>(p, a, st);
     return s.N == 64 ? out<float, 64>(p, a, st) : out<float, 128>(p, a, st);
 }

@@ -112,21 +112,26 @@ SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward)
     p.between = s.T / p.L;  // n tokens have ceil(n / L) - 1 <= n / L states between their chunks
     // Segments: where whole sequences are fewer than 512 workgroups (two a compute
     // unit), about as many segments as make them, of 4 chunks or more.
-    const long long whole = (long long)s.B * p.slices;
-    long long seg = 0;
-    if (whole < 512) {
-        const long long want = (512 + p.slices - 1) / p.slices;
-        seg = (p.between + want - 1) / want;
+    // Segments: the first launch walks all but the last of a sequence's, the second
+    // all but the first, and a workgroup begins with a sum over those before its own;
+    // so as many as make one workgroup for each half of a compute unit (they take half of
+    // its LDS), at most 32, and none below 4 chunks.
+    const long long whole = (long long)s.B * p.slices * (backward ? 2 : 1);
+    const long long each = (p.between + s.B - 1) / s.B;  // chunks of a sequence, if they are alike
+    long long seg = 0, want = 1 + 512 / whole;
+    if (want > 32) want = 32;
+    if (want > 1) {
+        seg = (each + want - 1) / want;
         if (seg < 4) seg = 4;
         if (seg >= p.between) seg = 0;  // no sequence has more than one
     }
     p.seg = (int)seg;
     p.segs = seg ? s.T / (seg * p.L) + s.B : s.B;
-    // Parts of a group's heads in the gradients: until there are two workgroups a
-    // compute unit.
+    // Parts of a group's heads in the gradients: until there is a workgroup for every
+    // compute unit (it takes nearly all of its LDS).
     p.splits = 1;
     const int per_group = s.H / s.G;
-    while (backward && p.chunks && p.splits * 2 <= per_group && p.chunks * s.G * p.splits < 512) p.splits *= 2;
+    while (backward && p.chunks && p.splits * 2 <= per_group && p.chunks * s.G * p.splits < 256) p.splits *= 2;
     size_t at = 0;
     auto take = [&](long long bytes) {
         const size_t was = at;
@@ -134,11 +139,14 @@ SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward)
         return was;
     };
     const long long state = (long long)p.slices * s.N * kSlice;
-    p.seg_at = take(p.seg ? p.segs * state * 4 : 0);
-    p.tot_at = take(p.seg ? p.segs * p.slices * 4 : 0);
+    const int ways = backward ? 2 : 1;
+    p.dec_at = take(p.chunks * s.H * (p.L == 128 ? kDecays<128> : kDecays<64>) * 4);
+    p.seg_at = take(p.seg ? ways * p.segs * state * 4 : 0);
+    p.tot_at = take(p.seg ? ways * p.segs * p.slices * 4 : 0);
     p.fwd_at = take(backward ? p.between * state * 4 : (p.between + s.B) * state * e);
     if (backward) {
         p.back_at = take(p.between * state * 4);
+        p.token_at = take(p.chunks * s.H * (p.L == 128 ? kTokens<128> : kTokens<64>) * 4);
         p.sum_at = take(p.chunks * s.H * 12);
         p.part_at = take(p.splits > 1 ? 2LL * p.splits * s.T * s.G * s.N * 4 : 0);
     }

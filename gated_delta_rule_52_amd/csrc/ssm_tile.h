@@ -22,17 +22,18 @@ template <> struct SsmTile<float> {
 
 // Units of `len` tokens (chunks, segments) of packed sequences, in the order of
 // the sequences.  Unit `id`: the at-th of `count` of sequence b, whose rows are
-// start .. start + n - 1; chunks: of the sequence; between: states between chunks
-// in all sequences before it.  Every sequence has `least` units or more.
+// start .. start + n - 1; chunks: of the sequence; before, between: the chunks, and
+// the states between chunks, of all sequences before it.  Every sequence has `least`
+// units or more.
 struct Unit {
     int b, at, count, start, n, chunks;
-    long long between;
+    long long before, between;
 };
 template <int L>
 __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int T, int len, int least, long long id, Unit& u)
 {
     const int l = lane_id();
-    long long before = 0, between = 0;
+    long long before = 0, between = 0, chunks = 0;
     for (int b0 = 0; b0 < B; b0 += 64) {
         const int b = b0 + l < B ? b0 + l : B - 1;
         int st = cu[b], en = cu[b + 1];
@@ -42,7 +43,7 @@ __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int
         int nu = (n + len - 1) / len;
         nu = b0 + l < B ? (nu < least ? least : nu) : 0;
         const int nbt = b0 + l < B && ch > 1 ? ch - 1 : 0;
-        const int inc = wave_scan(nu), incb = wave_scan(nbt);
+        const int nch = b0 + l < B ? ch : 0, inc = wave_scan(nu), incb = wave_scan(nbt), incc = wave_scan(nch);
         const uint64_t hit = __ballot(before + inc > id);
         if (hit) {
             const int first = __builtin_ctzll(hit);
@@ -52,11 +53,13 @@ __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int
             u.start = __builtin_amdgcn_readlane(st, first);
             u.n = __builtin_amdgcn_readlane(n, first);
             u.chunks = __builtin_amdgcn_readlane(ch, first);
+            u.before = chunks + __builtin_amdgcn_readlane(incc, first) - u.chunks;
             u.between = between + __builtin_amdgcn_readlane(incb, first) - __builtin_amdgcn_readlane(nbt, first);
             return true;
         }
         before += __builtin_amdgcn_readlane(inc, 63);
         between += __builtin_amdgcn_readlane(incb, 63);
+        chunks += __builtin_amdgcn_readlane(incc, 63);
     }
     return false;
 }
@@ -73,105 +76,118 @@ __device__ __forceinline__ void deal(long long id, int slices, long long& unit, 
 // log(1 + exp(v)), v itself from where they agree in fp32
 __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
 
-__device__ __forceinline__ double shift_up(double x, int d) { return __shfl_up(x, d); }
+// What ssm_prep.hip leaves of a chunk and head, a row of L values each, and behind
+// them exp(c_L) and its logarithm.  c is the running sum of log2 exp(g): its
+// differences are small and it is not, so it comes as two floats whose sum has
+// 48 bits.  Blocks are of 32 tokens; E_ts of t in a later block than s is
+// AHEAD_t exp(c at the start of t's block - c at the end of s's) BEHIND_s, factors
+// that decay throughout, so that a pair costs a product and no exponential.
+enum { DEC_HI, DEC_LO, DEC_DELTA, DEC_E, DEC_F, DEC_AHEAD, DEC_BEHIND, DEC_ROWS };
+template <int L> constexpr int kDecays = DEC_ROWS * L + 4;  // floats a chunk and head
+enum { DEC_KEEP, DEC_TOTAL };
+//   E: exp(c), F: exp(c_L - c), AHEAD: exp(c - c before the block), BEHIND: exp(c at
+//   the block's end - c); behind the last token delta is 0 and c stays as it is
 
-// Decays of a chunk of L tokens, K of them a lane: token K l + k.  raw: dt + bias,
-// d: delta (0 behind the chunk's end, where nothing changes), c: the running sum of
-// log2 exp(g), in 64 bits: its differences are small, it is not.
-template <int L> struct Decays {
-    static constexpr int K = L / 64;
-    float raw[K], d[K];
-    double c[K], total;
-    // `dt`: of the chunk's first token and the head, tokens H apart; live: tokens of the chunk
-    __device__ __forceinline__ void load(const float* __restrict__ dt, int H, int live, float bias)
-    {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = K * lane_id() + k;
-            raw[k] = dt[(size_t)(t < live ? t : live - 1) * H] + bias;
-        }
-    }
-    __device__ __forceinline__ void scan(float A, int plus, int live)
-    {
-        const double a2 = (double)A * 1.4426950408889634;
-        double run = 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool in = K * lane_id() + k < live;
-            d[k] = in ? (plus ? softplus(raw[k]) : raw[k]) : 0.f;
-            run += in ? (double)d[k] * a2 : 0.0;
-            c[k] = run;
-        }
-        double s = run;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double up = shift_up(s, o);
-            if (lane_id() >= o) s += up;
-        }
-        total = __shfl(s, 63);
-#pragma unroll
-        for (int k = 0; k < K; ++k) c[k] += s - run;
-    }
-};
+// What ssm_grad.hip leaves of a chunk and head for the steps' gradients, a row of L
+// values each: sums of r from the state before and from earlier blocks, of q / delta
+// into the state behind and into later blocks, the pairs of the token's own block
+// that pass over it, x . du and x . dy.  Behind them <S, dS> by wave, and, in chunks of
+// four blocks, the sums of the pairs between blocks (2, 0), (3, 0), and (3, 0) + (3, 1).
+enum { TOK_R_STATE, TOK_R_BLOCKS, TOK_Q_STATE, TOK_Q_BLOCKS, TOK_OWN, TOK_XDU, TOK_XDY, TOK_ROWS };
+template <int L> constexpr int kTokens = TOK_ROWS * L + 12;  // floats a chunk and head
 
-// v as PARTS fragments that sum up to it
+// v as three bf16 each: the upper 8 bits of its 24, the next, the rest.  Cut off and
+// not rounded, which leaves all bits and takes fewer instructions.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b)  // of a in the low half
+{
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float upper(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&w)[3])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a = v[2 * i], b = v[2 * i + 1];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            const uint32_t x = cvt2_bf16(a, b);
-            w[p][i] = x;
-            a -= __uint_as_float(x << 16);
-            b -= __uint_as_float(x & 0xffff0000u);
-        }
+        w[0][i] = upper_halves(a, b);
+        a -= upper(a), b -= upper(b);
+        w[1][i] = upper_halves(a, b);
+        a -= upper(a), b -= upper(b);
+        w[2][i] = upper_halves(a, b);
     }
 }
 
-// Rows::down, in plain order: to go with operands read along their rows
-template <typename T, int D>
-__device__ __forceinline__ Frag<T> down_plain(const void* tab, int k0, int d0)
-{
+// Reads of a row table (Rows) from a lane's byte offset, all others of a kind being
+// that offset with bits of the word index flipped: a kernel short of registers keeps
+// the offset opaque in its loops, so that the others are formed on the way.
+//   along:  an operand's rows along their values          (plain order, Rows::along)
+//   down:   an operand's columns down 16 rows             (permuted order, Rows::down)
+//   plain:  the same in plain order, to go with along
+//   row4:   four values of a lane's own row, those of accumulator registers 4 i .. + 3
+template <typename T, int D> struct Reads {
     using R = Rows<T, D>;
-    const int l = lane_id(), h = l >> 5;
-    if constexpr (sizeof(T) == 2) {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        const int i = l & 15, c = d0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
+    static constexpr int BYTES = R::BYTES;
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+    static __device__ __forceinline__ uint32_t down_at() { return lane_at(4 * (lane_id() >> 5)); }
+    static __device__ __forceinline__ uint32_t plain_at() { return lane_at(8 * (lane_id() >> 5)); }
+    static __device__ __forceinline__ Frag<T> down(const void* tab, uint32_t at, int k0, int d0)
+    {
+        if constexpr (sizeof(T) == 2)
+            return pair<8, 2>(tab, at, k0, d0);  // rows 8 t + 4 h + .. : bit 1 of the row's flips is t
+        else
+            return R::down(tab, k0, d0);
+    }
+    static __device__ __forceinline__ Frag<T> plain(const void* tab, uint32_t at, int k0, int d0)
+    {
+        if constexpr (sizeof(T) == 2) {
+            return pair<4, 1>(tab, at, k0, d0);  // rows 8 h + 4 t + ..
+        } else {
+            const int l = lane_id(), c = d0 + (l & 31);
+            const float* t = reinterpret_cast<const float*>(tab) + k0 * R::U * 4;
+            f32x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = t[R::word(8 * (l >> 5) + j, c >> 2) * 4 + (c & 3)];
+            return v;
+        }
+    }
+    static __device__ __forceinline__ uint32_t row_at(int r)
+    {
+        const uint32_t h = lane_id() >> 5;
+        return sizeof(T) == 2 ? (uint32_t)R::word(r, 0) * 16 + 8 * h : (uint32_t)R::word(r, h) * 16;
+    }
+    // values 32 i + 8 q + 4 h .. + 3
+    static __device__ __forceinline__ f32x4 row4(const void* tab, uint32_t at, int i, int q)
+    {
+        const char* p = reinterpret_cast<const char*>(tab);
+        if constexpr (sizeof(T) == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + (at ^ ((4 * i + q) << 4)));
+            return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                         __uint_as_float(w.y & 0xffff0000u)};
+        } else {
+            return *reinterpret_cast<const f32x4*>(p + (at ^ ((8 * i + 2 * q) << 4)));
+        }
+    }
+
+private:
+    static __device__ __forceinline__ uint32_t lane_at(int row)
+    {
+        const int l = lane_id(), i = l & 15, c = 16 * ((l >> 4) & 1) + 4 * (i & 3);
+        return (uint32_t)R::word(row + (i >> 2), c >> 3) * 16 + (c & 7) * 2;
+    }
+    template <int ROWS, int FLIP>
+    static __device__ __forceinline__ bf16x8 pair(const void* tab, uint32_t at, int k0, int d0)
+    {
+        const char* p = reinterpret_cast<const char*>(tab) + k0 * BYTES;
         s16x4 v[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int r = 8 * h + 4 * t + (i >> 2);
-            const char* p = reinterpret_cast<const char*>(tab) + k0 * R::BYTES + R::word(r, c >> 3) * 16 + (c & 7) * 2;
-            v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-        }
+        for (int t = 0; t < 2; ++t)
+            v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(p + t * ROWS * BYTES + (at ^ (uint32_t)(((d0 >> 3) ^ (t * FLIP)) << 4))));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-        const int c = d0 + (l & 31);
-        const float* t = reinterpret_cast<const float*>(tab) + k0 * R::U * 4;
-        f32x8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = t[R::word(8 * h + j, c >> 2) * 4 + (c & 3)];
-        return v;
     }
-}
-
-// four values of row r at column c (a multiple of 4) of a table
-template <typename T, int D>
-__device__ __forceinline__ f32x4 row4(const void* tab, int r, int c)
-{
-    using R = Rows<T, D>;
-    if constexpr (sizeof(T) == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(tab) + R::word(r, c >> 3) * 16 + (c & 7) * 2);
-        return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u)};
-    } else {
-        return *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(tab) + R::word(r, c >> 2) * 16);
-    }
-}
+};
 
 // rows of a tile's accumulator registers 4 i .. 4 i + 3: 8 i + 4 h + 0 .. 3
-__device__ __forceinline__ int acc_rows(int i) { return 8 * i + 4 * (lane_id() >> 5); }
+__device__ __forceinline__ int acc_rows(int i, int l = lane_id()) { return 8 * i + 4 * (l >> 5); }
 
 }  // namespace gdn
