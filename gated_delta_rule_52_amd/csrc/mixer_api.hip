@@ -69,11 +69,12 @@ gdn_status check_ssm(const gdn_ssm_shape* sh, SsmCall call, gdn_ssm_shape& s)
         if (*st[i] > (1LL << 24)) return GDN_ERR_UNSUPPORTED;
     }
     if (call != CALL_STEP) {
-        // below 2^32 work-items: 512 a chunk (or segment) and slice, whole eights of chunks
+        // below 2^32 work-items: 512 a chunk (or segment) and slice or part, in whole
+        // eights of chunks and 32s of workgroups a die
         const SsmPlan p = ssm_plan(s, call == CALL_BACKWARD);
         const long long most = p.chunks > p.segs ? p.chunks : p.segs;
         const long long jobs = p.slices > s.G * p.splits ? p.slices : s.G * p.splits;
-        if ((most + 8) * jobs >= (1LL << 23)) return GDN_ERR_UNSUPPORTED;
+        if ((most + 8) * jobs + 256 >= (1LL << 23)) return GDN_ERR_UNSUPPORTED;
     }
     return GDN_OK;
 }

@@ -19,11 +19,14 @@
 // summed up to and from every t by a product with 0s and 1s.
 //
 // A workgroup has a chunk, a group and some of its heads, whose slices of 64
-// values it takes one after the other: dB and dC stay in registers.  Half of the
-// waves are a 32-token block of t each (dC, r), the others one of s (dx, dB, q);
-// the states' parts share one table: first S, read by the former while the latter
-// go through the chunk's pairs, then dS the other way round.  Each sum is formed
-// within a lane and its other half, in one order.
+// values it takes one after the other, and one of two parts: that of the t (dC, r)
+// or that of the s (dx, dB, q), a wave each 32 of the chunk's tokens.  The sum over
+// the heads stays in registers, and so do the wave's own rows of C and dy, or B and
+// x; the other side's rows and half of a state at a time are in LDS, so that two
+// workgroups share a compute unit and one computes while the other loads.  A t has
+// the s before it and an s the t behind it, so the parts' waves complement one
+// another on a SIMD.  Each sum is formed within a lane and its other half, in one
+// order.
 #include "ssm_tile.h"
 
 #include "common.h"
@@ -87,270 +90,199 @@ template <typename T> __device__ __forceinline__ Frag<T> ones_below(int b, int l
     }
 }
 
-template <typename T, int N>
-__global__ __launch_bounds__(128 * (SsmTile<T>::L / 32)) void ssm_grad_kernel(GradArgs a)
+// an operand in plain order as in permuted order (attn.h): 4 of each half's values change places
+template <typename T> __device__ __forceinline__ Frag<T> permuted(const Frag<T>& f)
 {
-    constexpr int L = SsmTile<T>::L, NB = L / 32, NTH = 128 * NB, PARTS = SsmTile<T>::PARTS, KN = N / 16, TN = N / 32;
-    constexpr bool HOLD = sizeof(T) == 2;  // operands that are used again stay in registers
+    constexpr int W = sizeof(Frag<T>) / 4;
+    typedef uint32_t words __attribute__((ext_vector_type(W)));
+    words v = __builtin_bit_cast(words, f);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v[i], v[i + W / 2], false, false);
+        v[i] = r[0], v[i + W / 2] = r[1];
+    }
+    return __builtin_bit_cast(Frag<T>, v);
+}
+
+template <typename T, int N> struct GradLds {
+    static constexpr int L = SsmTile<T>::L;
+    char rows[L * Rows<T, N>::BYTES], vals[L * Rows<T, kSlice>::BYTES];  // B and x, or C and dy
+    char st[SsmTile<T>::PARTS][64 * Rows<T, kSlice>::BYTES];              // half of a state
+    float dec[DEC_ROWS * L];
+};
+
+// what both parts know of their chunk
+struct Chunk {
+    Unit u;
+    long long id;
+    size_t row0;
+    int c, live, g, sp, h_first, h_last;
+};
+
+template <typename T, int N> struct Grad {
+    static constexpr int L = SsmTile<T>::L, NB = L / 32, NTH = 64 * NB, PARTS = SsmTile<T>::PARTS, KN = N / 16, TN = N / 32, NH = N / 64;
+    static constexpr int SW = 64 * 8 / NTH;  // runs of 8 values of half a state a thread stages
     using NTab = Rows<T, N>;
     using VTab = Rows<T, kSlice>;
     using NRead = Reads<T, N>;
     using VRead = Reads<T, kSlice>;
-    constexpr int SW = N * 8 / NTH;  // runs of 8 values of a state a thread stages
-    __shared__ __align__(16) char b_s[L * NTab::BYTES], c_s[L * NTab::BYTES];
-    __shared__ __align__(16) char x_s[L * VTab::BYTES], y_s[L * VTab::BYTES];
-    __shared__ __align__(16) char st_s[PARTS][N * VTab::BYTES];
-    __shared__ __align__(16) float dec_s[DEC_ROWS * L], tok_s[kTokens<L>];
+    using State = f32x4[SW][2];
 
-    long long id;
-    int job;
-    deal(blockIdx.x, a.G * a.splits, id, job);
-    Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, id, u)) return;
-    const int c = u.at, live = u.n - c * L < L ? u.n - c * L : L;
-    const size_t row0 = (size_t)u.start + (size_t)c * L;
-    const int w = uniform(wave_id());
-    const bool is_s = w >= NB;
-    const int rb = is_s ? w - NB : w;  // the lanes' tokens: 32 rb + l % 32
-    const int per_head = a.P / kSlice, per_group = a.H / a.G, g = job / a.splits, sp = job - g * a.splits;
-    const int h_first = g * per_group + (int)((long long)per_group * sp / a.splits),
-              h_last = g * per_group + (int)((long long)per_group * (sp + 1) / a.splits);
-    const bool has_s = c > 0 || a.h0, has_d = c < u.chunks - 1 || a.dhT;
-
-    auto rows_of = [&](char* tab, auto rows, const T* base, long long stride, int l) {
-        using R = decltype(rows);
-        for (int r = 16 * w; r < L; r += 32 * NB) {
+    template <typename R> static __device__ __forceinline__ void fetch(char* tab, const T* base, long long stride, int live, int l)
+    {
+        for (int r = 16 * uniform(wave_id()); r < L; r += 16 * NB) {
             const int rr = r < live ? r : live - 1;
             R::template fetch<16>(tab, r, base + (size_t)rr * stride, (uint32_t)(stride * sizeof(T)), live - 1 - rr, l);
         }
-    };
-    rows_of(b_s, NTab{}, (const T*)a.B + row0 * a.bs + (size_t)g * N, a.bs, lane_id());
-    rows_of(c_s, NTab{}, (const T*)a.C + row0 * a.cs + (size_t)g * N, a.cs, lane_id());
-
-    f32x16 acc[TN];  // dC of 32 t or dB of 32 s
+    }
+    // half hh of a state: between chunks [N][64], at a sequence's edge [N][P]
+    static __device__ __forceinline__ void load_state(const GradArgs& a, const Chunk& k, const float* between, long long which,
+                                                      const float* edge, int slice, int hh, int tid, State& v)
+    {
+        const int per_head = a.P / kSlice, head = slice / per_head;
+        const float* s = edge ? edge + (((size_t)k.u.b * a.H + head) * N + 64 * hh) * a.P + (slice - head * per_head) * kSlice
+                              : between + (((size_t)which * a.slices + slice) * N + 64 * hh) * kSlice;
+        const int stride = edge ? a.P : kSlice;
 #pragma unroll
-    for (int i = 0; i < TN; ++i) acc[i] = zero16();
-    // a lane's offsets for the reads below; opaque, each loop's are formed in it
-    const uint32_t na = NTab::along_at(), va = VTab::along_at(), nd = NRead::down_at(), vd = VRead::down_at(),
-                   vp = VRead::plain_at(), nr = NRead::row_at(32 * rb + (lane_id() & 31)), vr = VRead::row_at(32 * rb + (lane_id() & 31));
-    Frag<T> own[HOLD ? KN : 1], val[HOLD ? 4 : 1];  // the lane's rows of C or B, and of dy or x
-    auto own_at = [&](int kk) {
-        if constexpr (HOLD) return own[kk];
-        else return NTab::along(is_s ? b_s : c_s, opaque(na), 32 * rb, kk);
-    };
-    auto val_at = [&](int kk) {
-        if constexpr (HOLD) return val[kk];
-        else return VTab::along(is_s ? x_s : y_s, opaque(va), 32 * rb, kk);
-    };
-
-    for (int slice = h_first * per_head; slice < h_last * per_head; ++slice) {
-        const int head = slice / per_head, sub = slice - head * per_head, p0 = sub * kSlice;
-        // the lane, opaque: what follows from it is formed here and not held from slice to slice
-        const int l = (int)opaque(lane_id()), h = l >> 5, tid = 64 * w + l, at = 32 * rb + (l & 31);
-        rows_of(x_s, VTab{}, (const T*)a.x + row0 * a.xs + (size_t)head * a.P + p0, a.xs, l);
-        rows_of(y_s, VTab{}, (const T*)a.dy + (row0 * a.H + head) * a.P + p0, (long long)a.H * a.P, l);
-        // run i of this thread: row n of the state, values 8 q .. 8 q + 7
-        auto run = [&](int i, int& n, int& q) {
-            const int x = i * NTH + tid;
-            n = x >> 3, q = x & 7;
-        };
-        auto state_of = [&](const float* between, long long which, const float* edge, f32x4 (&v)[SW][2]) {
-            // between chunks [N][64]; at a sequence's edge [N][P]
-            const float* s = edge ? edge + ((size_t)u.b * a.H + head) * N * a.P + p0
-                                  : between + ((size_t)which * a.slices + slice) * N * kSlice;
-            const int stride = edge ? a.P : kSlice;
+        for (int i = 0; i < SW; ++i) {
+            const int x = i * NTH + tid, n = x >> 3, q = x & 7;
+            v[i][0] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q);
+            v[i][1] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q + 4);
+        }
+    }
+    static __device__ __forceinline__ void put_state(GradLds<T, N>& m, int tid, const State& v)
+    {
 #pragma unroll
-            for (int i = 0; i < SW; ++i) {
-                int n, q;
-                run(i, n, q);
-                v[i][0] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q);
-                v[i][1] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q + 4);
+        for (int i = 0; i < SW; ++i) {
+            const int x = i * NTH + tid, n = x >> 3, q = x & 7;
+            if constexpr (sizeof(T) == 2) {
+                u32x4 parts[3];
+                const float f[8] = {v[i][0][0], v[i][0][1], v[i][0][2], v[i][0][3], v[i][1][0], v[i][1][1], v[i][1][2], v[i][1][3]};
+                split(f, parts);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(m.st[p] + VTab::word(n, q) * 16) = parts[p];
+            } else {
+                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(n, 2 * q) * 16) = v[i][0];
+                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(n, 2 * q + 1) * 16) = v[i][1];
             }
-        };
-        auto put_state = [&](const f32x4 (&v)[SW][2]) {
+        }
+    }
+    // exp(c) from the end of block `from` to the start of block `to`
+    static __device__ __forceinline__ float between(const float* dec, int from, int to)
+    {
+        const int e = 32 * from + 31, s = 32 * to - 1;
+        return exp2_hw((dec[DEC_HI * L + s] - dec[DEC_HI * L + e]) + (dec[DEC_LO * L + s] - dec[DEC_LO * L + e]));
+    }
+    static __device__ __forceinline__ void store(const GradArgs& a, const Chunk& k, const f32x16 (&acc)[TN], bool is_s, int at)
+    {
+        if (at >= k.live) return;
+        const size_t o = ((k.row0 + at) * a.G + k.g) * N;
+        T* out = (T*)(is_s ? a.dB : a.dC) + o;
+        float* part = a.part + ((size_t)(is_s ? 0 : a.splits) + k.sp) * a.T * a.G * N + o;
 #pragma unroll
-            for (int i = 0; i < SW; ++i) {
-                int n, q;
-                run(i, n, q);
-                if constexpr (sizeof(T) == 2) {
-                    u32x4 parts[3];
-                    const float f[8] = {v[i][0][0], v[i][0][1], v[i][0][2], v[i][0][3], v[i][1][0], v[i][1][1], v[i][1][2], v[i][1][3]};
-                    split(f, parts);
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st_s[p] + VTab::word(n, q) * 16) = parts[p];
-                } else {
-                    *reinterpret_cast<f32x4*>(st_s[0] + VTab::word(n, 2 * q) * 16) = v[i][0];
-                    *reinterpret_cast<f32x4*>(st_s[0] + VTab::word(n, 2 * q + 1) * 16) = v[i][1];
-                }
+            for (int q = 0; q < 4; ++q) {
+                const int n = 32 * i + acc_rows(q);
+                const float v0 = acc[i][4 * q], v1 = acc[i][4 * q + 1], v2 = acc[i][4 * q + 2], v3 = acc[i][4 * q + 3];
+                if (a.splits == 1)
+                    store4<T>(out + n, v0, v1, v2, v3);
+                else
+                    store4<float>(part + n, v0, v1, v2, v3);
             }
-        };
-        // what put_state has put there, times v
-        auto dot_state = [&](const f32x4 (&v)[SW][2]) {
-            float dot = 0.f;
+    }
+
+    // the part of the t: dC and r
+    static __device__ __forceinline__ void of_t(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
+    {
+        const int w = uniform(wave_id()), rb = w, live = k.live, per_head = a.P / kSlice;
+        const bool has_s = k.c > 0 || a.h0, has_d = k.c < k.u.chunks - 1 || a.dhT;
+        fetch<NTab>(m.rows, (const T*)a.B + k.row0 * a.bs + (size_t)k.g * N, a.bs, live, lane_id());
+        const uint32_t na = NTab::along_at(), va = VTab::along_at(), nd = NRead::down_at();
+        const int mine = 32 * rb + (lane_id() & 31), row = mine < live ? mine : live - 1;
+        Frag<T> own[KN], val[4];  // the lane's rows of C and dy
 #pragma unroll
-            for (int i = 0; i < SW; ++i) {
-                int n, q;
-                run(i, n, q);
+        for (int kk = 0; kk < KN; ++kk)
+            own[kk] = load_frag<T>((const T*)a.C + (k.row0 + row) * a.cs + (size_t)k.g * N + 16 * kk + 8 * (lane_id() >> 5));
+        f32x16 acc[TN];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    f32x4 s{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < TN; ++i) acc[i] = zero16();
+        float r_state = 0.f, r_blocks = 0.f, over_own = 0.f, dot = 0.f, cross0 = 0.f, cross1 = 0.f;
+
+        for (int slice = k.h_first * per_head; slice < k.h_last * per_head; ++slice) {
+            const int head = slice / per_head, sub = slice - head * per_head, p0 = sub * kSlice;
+            // the lane, opaque: what follows from it is formed here and not held from slice to slice
+            const int l = (int)opaque(lane_id()), h = l >> 5, tid = 64 * w + l, at = 32 * rb + (l & 31);
+            fetch<VTab>(m.vals, (const T*)a.x + k.row0 * a.xs + (size_t)head * a.P + p0, a.xs, live, l);
+            const float* dec = a.dec + ((size_t)k.id * a.H + head) * kDecays<L>;
+            if (sub == 0) {
+                r_state = r_blocks = over_own = dot = cross0 = cross1 = 0.f;
+                for (int i = tid; i < DEC_ROWS * L; i += NTH) m.dec[i] = dec[i];
+            }
+            {
+                const int t = at < live ? at : live - 1;
+                const T* dy = (const T*)a.dy + ((k.row0 + t) * a.H + head) * a.P + p0 + 8 * h;
 #pragma unroll
-                    for (int p = PARTS - 1; p >= 0; --p) {
-                        if constexpr (sizeof(T) == 2) {
-                            const uint2 w = *reinterpret_cast<const uint2*>(st_s[p] + VTab::word(n, q) * 16 + 8 * j);
-                            s += f32x4{__uint_as_float(w.x << 16), upper(__uint_as_float(w.x)), __uint_as_float(w.y << 16),
-                                       upper(__uint_as_float(w.y))};
-                        } else {
-                            s = *reinterpret_cast<const f32x4*>(st_s[p] + VTab::word(n, 2 * q + j) * 16);
-                        }
+                for (int kk = 0; kk < 4; ++kk) val[kk] = load_frag<T>(dy + 16 * kk);
+            }
+            const float e_t = dec[DEC_E * L + at];
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                if (hh) __syncthreads();  // the half before is read
+                if (has_s) {
+                    State sv, dv;
+                    load_state(a, k, a.fwd, k.u.between + k.c - 1, k.c > 0 ? nullptr : a.h0, slice, hh, tid, sv);
+                    if (has_d) load_state(a, k, a.back, k.u.between + k.c, k.c < k.u.chunks - 1 ? nullptr : a.dhT, slice, hh, tid, dv);
+                    put_state(m, tid, sv);
+                    if (has_d) {
+#pragma unroll
+                        for (int i = 0; i < SW; ++i)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(sv[i][j >> 2][j & 3], dv[i][j >> 2][j & 3], dot);
                     }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dot = __builtin_fmaf(s[k], v[i][j][k], dot);
                 }
-            }
-            return dot;
-        };
-        f32x4 sv[SW][2];
-        if (has_s) {
-            state_of(a.fwd, u.between + c - 1, c > 0 ? nullptr : a.h0, sv);
-            put_state(sv);
-        }
-        if (sub == 0) {
-            const float* dec = a.dec + ((size_t)id * a.H + head) * kDecays<L>;
-            for (int i = tid; i < DEC_ROWS * L; i += NTH) dec_s[i] = dec[i];
-        }
-        if (has_d) state_of(a.back, u.between + c, c < u.chunks - 1 ? nullptr : a.dhT, sv);
-        wait_vm<0>();
-        __syncthreads();
-
-        if constexpr (HOLD) {
-            if (slice == h_first * per_head) {
+                if (hh == 0) wait_vm<0>();
+                __syncthreads();
+                if (!has_s) continue;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int kk = 0; kk < KN; ++kk) own[kk] = NTab::along(is_s ? b_s : c_s, na, 32 * rb, kk);
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) val[kk] = VTab::along(is_s ? x_s : y_s, va, 32 * rb, kk);
-        }
-        const float *hi_s = dec_s + DEC_HI * L, *lo_s = dec_s + DEC_LO * L, *d_s = dec_s + DEC_DELTA * L,
-                    *ahead_s = dec_s + DEC_AHEAD * L, *behind_s = dec_s + DEC_BEHIND * L;
-        const float dc = d_s[at];
-        // a sum of this slice onto those of the head's before it
-        auto leave = [&](int i, float v) { tok_s[i] = sub ? tok_s[i] + v : v; };
-        // exp(c) from the end of block `from` to the start of block `to`
-        auto between = [&](int from, int to) {
-            const int e = 32 * from + 31, s = 32 * to - 1;
-            return exp2_hw((hi_s[s] - hi_s[e]) + (lo_s[s] - lo_s[e]));
-        };
-        f32x16 du[2] = {zero16(), zero16()};
-        float qo = 0.f, xdu = 0.f, zd = 0.f;
-        __builtin_amdgcn_sched_barrier(0);
-        if (!is_s) {
-            float r = 0.f;
-            if (has_s) {
-                const float e = dec_s[DEC_E * L + at];
-#pragma unroll
-                for (int i = 0; i < TN; ++i) {
-                    f32x16 m = zero16();
-                    const uint32_t al = opaque(va), row = opaque(nr);
+                for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
+                    f32x16 z = zero16();
+                    const uint32_t al = opaque(va);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) m = mma32(VTab::along(st_s[p], al, 32 * i, kk), val_at(kk), m);
+                        for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.st[p], al, 32 * (i - 2 * hh), kk), val[kk], z);
                     ordered<T, 4 * PARTS, 1>();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x4 cv = NRead::row4(c_s, row, i, q);
+                    for (int b = 0; b < 2; ++b) {
+                        const Frag<T> cv = permuted<T>(own[2 * i + b]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float v = m[4 * q + j] * e;
-                            acc[i][4 * q + j] += v;
-                            r = __builtin_fmaf(cv[j], v, r);
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = z[8 * b + j] * e_t;
+                            acc[i][8 * b + j] += v;
+                            r_state = __builtin_fmaf((float)cv[j], v, r_state);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            r = half_add(r);
-            if (h == 0) leave(TOK_R_STATE * L + at, r);
-        } else if (32 * rb < live) {
-            const float behind = behind_s[at];
-            for (int tb = rb; tb < NB && 32 * tb < live; ++tb) {
-                f32x16 m = zero16(), z = zero16();
-                const uint32_t nal = opaque(na), val4 = opaque(va), ndn = opaque(nd), vdn = opaque(vd);
-#pragma unroll
-                for (int kk = 0; kk < KN; ++kk) m = mma32(NTab::along(c_s, nal, 32 * tb, kk), own_at(kk), m);
-                ordered<T, KN, 1>();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(y_s, val4, 32 * tb, kk), val_at(kk), z);
-                ordered<T, 4, 1>();
-                if (tb > rb) {
-                    const float f = behind * between(rb, tb);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = 32 * tb + acc_rows(i, l);
-                        const f32x4 as = *reinterpret_cast<const f32x4*>(ahead_s + t);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float e = t + j < live ? as[j] * f : 0.f;  // no copies of the last token
-                            m[4 * i + j] *= e;
-                            qo = __builtin_fmaf(m[4 * i + j], z[4 * i + j], qo);
-                            z[4 * i + j] *= e * dc;
-                        }
-                    }
-                } else {
-                    const float hc = hi_s[at], lc = lo_s[at];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = 32 * tb + acc_rows(i, l);
-                        const f32x4 ht = *reinterpret_cast<const f32x4*>(hi_s + t), lt = *reinterpret_cast<const f32x4*>(lo_s + t);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // pairs that are none: exp2(-inf)
-                            const float e = exp2_hw(at <= t + j && t + j < live ? (ht[j] - hc) + (lt[j] - lc) : -INFINITY);
-                            const float eg = e * m[4 * i + j], zv = z[4 * i + j];
-                            xdu = __builtin_fmaf(eg, zv, xdu);
-                            zd = t + j == at ? zv : zd;
-                            m[4 * i + j] = eg;
-                            z[4 * i + j] = e * zv * dc;
-                        }
-                    }
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const Frag<T> mv = acc_frag<T>(m, b), zv = acc_frag<T>(z, b);
-#pragma unroll
-                    for (int pt = 0; pt < 2; ++pt) du[pt] = mma32(VRead::down(y_s, vdn, 32 * tb + 16 * b, 32 * pt), mv, du[pt]);
-#pragma unroll
-                    for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(c_s, ndn, 32 * tb + 16 * b, 32 * i), zv, acc[i]);
-                    ordered<T, 2 + TN, 2>();
-                }
-            }
-            qo = half_add(qo);
-            xdu = half_add(xdu) + qo;
-            zd = half_add(zd);  // the pair t = s is one half's
-        }
-        __syncthreads();
-        const float dot = wave_sum(has_s && has_d ? dot_state(sv) : 0.f);
-        if (l == 0) leave(TOK_ROWS * L + w, dot);
-        if (has_d) put_state(sv);
-        __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
-        if (!is_s) {
-            float r = 0.f, own_sum = 0.f;
             if (32 * rb < live) {
-                const float ahead = ahead_s[at];
+                const float *hi_s = m.dec + DEC_HI * L, *lo_s = m.dec + DEC_LO * L, *d_s = m.dec + DEC_DELTA * L,
+                            *behind_s = m.dec + DEC_BEHIND * L;
+                const float ahead = m.dec[DEC_AHEAD * L + at];
+                float r = 0.f;
                 for (int sb = 0; sb <= rb; ++sb) {
-                    f32x16 m = zero16(), z = zero16();
+                    f32x16 gm = zero16(), z = zero16();
                     const uint32_t nal = opaque(na), val4 = opaque(va), ndn = opaque(nd);
 #pragma unroll
-                    for (int kk = 0; kk < KN; ++kk) m = mma32(NTab::along(b_s, nal, 32 * sb, kk), own_at(kk), m);
+                    for (int kk = 0; kk < KN; ++kk) gm = mma32(NTab::along(m.rows, nal, 32 * sb, kk), own[kk], gm);
                     ordered<T, KN, 1>();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(x_s, val4, 32 * sb, kk), val_at(kk), z);
+                    for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.vals, val4, 32 * sb, kk), val[kk], z);
                     ordered<T, 4, 1>();
                     if (sb < rb) {
-                        const float f = ahead * between(sb, rb);
+                        const float f = ahead * between(m.dec, sb, rb);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int s = 32 * sb + acc_rows(i, l);
@@ -358,14 +290,13 @@ __global__ __launch_bounds__(128 * (SsmTile<T>::L / 32)) void ssm_grad_kernel(Gr
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 z[4 * i + j] *= f * bs[j] * ds[j];
-                                r = __builtin_fmaf(z[4 * i + j], m[4 * i + j], r);
+                                r = __builtin_fmaf(z[4 * i + j], gm[4 * i + j], r);
                             }
                         }
-                        if constexpr (NB == 4) {  // pairs that pass over blocks 1 and 2
-                            if (sb + 1 < rb) {
-                                const float all = wave_sum(at < live ? r : 0.f);
-                                if (l == 0) leave(TOK_ROWS * L + 2 * NB + (sb ? 2 : rb - 2), all);
-                            }
+                        if (NB == 4 && sb + 1 < rb) {  // pairs that pass over blocks 1 and 2
+                            const float all = wave_sum(at < live ? r : 0.f);
+                            cross0 += sb ? 0.f : all;
+                            cross1 += sb ? all : 0.f;
                         }
                     } else {
                         const float hc = hi_s[at], lc = lo_s[at];
@@ -376,8 +307,9 @@ __global__ __launch_bounds__(128 * (SsmTile<T>::L / 32)) void ssm_grad_kernel(Gr
                                         ds = *reinterpret_cast<const f32x4*>(d_s + s);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
+                                // pairs that are none: exp2(-inf)
                                 z[4 * i + j] *= exp2_hw(s + j <= at ? (hc - hs[j]) + (lc - ls[j]) : -INFINITY) * ds[j];
-                                m[4 * i + j] *= s + j < at && at < live ? z[4 * i + j] : 0.f;
+                                gm[4 * i + j] *= s + j < at && at < live ? z[4 * i + j] : 0.f;
                             }
                         }
                         // over[t][t'] = sum_{s < t} M_t's, then for every t the sum over t' >= t
@@ -385,122 +317,251 @@ __global__ __launch_bounds__(128 * (SsmTile<T>::L / 32)) void ssm_grad_kernel(Gr
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             Frag<T> parts[PARTS];
-                            acc_parts<T>(m, b, parts);
+                            acc_parts<T>(gm, b, parts);
                             const Frag<T> ones = ones_below<T>(b, l);
 #pragma unroll
                             for (int p = 0; p < PARTS; ++p) over = mma32(ones, parts[p], over);
                         }
+                        float mine = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float v = lane16_sum((l & 31) >= acc_rows(k >> 2, l) + (k & 3) ? over[k] : 0.f);
-                            own_sum = (l & 15) == k ? v : own_sum;
+                        for (int q = 0; q < 16; ++q) {
+                            const float v = lane16_sum((l & 31) >= acc_rows(q >> 2, l) + (q & 3) ? over[q] : 0.f);
+                            mine = (l & 15) == q ? v : mine;
                         }
-                        own_sum += __shfl_xor(own_sum, 16);
+                        over_own += mine + __shfl_xor(mine, 16);
                     }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const Frag<T> zv = acc_frag<T>(z, b);
 #pragma unroll
-                        for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(b_s, ndn, 32 * sb + 16 * b, 32 * i), zv, acc[i]);
+                        for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * sb + 16 * b, 32 * i), zv, acc[i]);
                         ordered<T, TN, 2>();
                     }
                 }
+                r_blocks += r;
             }
-            if (NB == 4 && 32 * rb >= live && rb > 1 && l < rb - 1) leave(TOK_ROWS * L + 2 * NB + rb - 2 + l, 0.f);
-            r = half_add(r);
-            if (h == 0) leave(TOK_R_BLOCKS * L + at, r);
-            // lane k of 16 has the sum of register k's t
-            if (!(l & 16)) leave(TOK_OWN * L + 32 * rb + acc_rows((l & 15) >> 2, l) + (l & 3), own_sum);
-        } else {
-            float qi = 0.f;
-            if (has_d) {
-                const float e = dec_s[DEC_F * L + at];
+            if (sub == per_head - 1) {  // the head's sums are complete
+                float* o = a.token + ((size_t)k.id * a.H + head) * kTokens<L>;
+                const float rs = half_add(r_state), rk = half_add(r_blocks), all = wave_sum(dot);
+                if (h == 0) {
+                    o[TOK_R_STATE * L + at] = rs;
+                    o[TOK_R_BLOCKS * L + at] = rk;
+                }
+                // lane q of 16 has the sum of register q's t
+                if (!(l & 16)) o[TOK_OWN * L + 32 * rb + acc_rows((l & 15) >> 2, l) + (l & 3)] = over_own;
+                if (l == 0) {
+                    o[TOK_ROWS * L + w] = all;
+                    if (NB == 4 && rb == 2) o[TOK_ROWS * L + 4] = cross0;
+                    if (NB == 4 && rb == 3) {
+                        o[TOK_ROWS * L + 5] = cross0;
+                        o[TOK_ROWS * L + 6] = cross1;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        store(a, k, acc, false, 32 * rb + (lane_id() & 31));
+    }
+
+    // the part of the s: dx, dB and q
+    static __device__ __forceinline__ void of_s(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
+    {
+        const int w = uniform(wave_id()), rb = w, live = k.live, per_head = a.P / kSlice;
+        const bool has_d = k.c < k.u.chunks - 1 || a.dhT;
+        fetch<NTab>(m.rows, (const T*)a.C + k.row0 * a.cs + (size_t)k.g * N, a.cs, live, lane_id());
+        const uint32_t na = NTab::along_at(), va = VTab::along_at(), nd = NRead::down_at(), vd = VRead::down_at(),
+                       vp = VRead::plain_at();
+        const int mine = 32 * rb + (lane_id() & 31), row = mine < live ? mine : live - 1;
+        Frag<T> own[KN], val[4];  // the lane's rows of B and x
+#pragma unroll
+        for (int kk = 0; kk < KN; ++kk)
+            own[kk] = load_frag<T>((const T*)a.B + (k.row0 + row) * a.bs + (size_t)k.g * N + 16 * kk + 8 * (lane_id() >> 5));
+        f32x16 acc[TN];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) acc[i] = zero16();
+        float q_blocks = 0.f, q_state = 0.f, xdu = 0.f, xdy = 0.f;
+
+        for (int slice = k.h_first * per_head; slice < k.h_last * per_head; ++slice) {
+            const int head = slice / per_head, sub = slice - head * per_head, p0 = sub * kSlice;
+            const int l = (int)opaque(lane_id()), h = l >> 5, tid = 64 * w + l, at = 32 * rb + (l & 31);
+            fetch<VTab>(m.vals, (const T*)a.dy + (k.row0 * a.H + head) * a.P + p0, (long long)a.H * a.P, live, l);
+            const float* dec = a.dec + ((size_t)k.id * a.H + head) * kDecays<L>;
+            if (sub == 0) {
+                q_blocks = q_state = xdu = xdy = 0.f;
+                for (int i = tid; i < DEC_ROWS * L; i += NTH) m.dec[i] = dec[i];
+            }
+            {
+                const int s = at < live ? at : live - 1;
+                const T* x = (const T*)a.x + (k.row0 + s) * a.xs + (size_t)head * a.P + p0 + 8 * h;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) val[kk] = load_frag<T>(x + 16 * kk);
+            }
+            const float f_s = dec[DEC_F * L + at], d_s = dec[DEC_DELTA * L + at];
+            f32x16 du[2] = {zero16(), zero16()};
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                if (hh) __syncthreads();  // the half before is read
+                if (has_d) {
+                    State dv;
+                    load_state(a, k, a.back, k.u.between + k.c, k.c < k.u.chunks - 1 ? nullptr : a.dhT, slice, hh, tid, dv);
+                    put_state(m, tid, dv);
+                }
+                if (hh == 0) wait_vm<0>();
+                __syncthreads();
+                if (!has_d) continue;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int pt = 0; pt < 2; ++pt) {
-                    f32x16 m = zero16();
-                    const uint32_t pl = opaque(vp), row = opaque(vr);
+                    f32x16 z = zero16();
+                    const uint32_t pl = opaque(vp);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                        for (int kk = 0; kk < KN; ++kk) m = mma32(VRead::plain(st_s[p], pl, 16 * kk, 32 * pt), own_at(kk), m);
-                    ordered<T, PARTS * KN, 2>();
+                        for (int kk = 0; kk < 4; ++kk)
+                            z = mma32(VRead::plain(m.st[p], pl, 16 * kk, 32 * pt), own[4 * hh + kk], z);
+                    ordered<T, 4 * PARTS, 2>();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x4 xv = VRead::row4(x_s, row, pt, q);
+                    for (int b = 0; b < 2; ++b) {
+                        const Frag<T> xv = permuted<T>(val[2 * pt + b]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float v = m[4 * q + j] * e;
-                            du[pt][4 * q + j] += v;
-                            qi = __builtin_fmaf(xv[j], v, qi);
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = z[8 * b + j] * f_s;
+                            du[pt][8 * b + j] += v;
+                            q_state = __builtin_fmaf((float)xv[j], v, q_state);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-                for (int i = 0; i < TN; ++i) {
-                    f32x16 m = zero16();
+                for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
+                    f32x16 z = zero16();
                     const uint32_t al = opaque(va);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) m = mma32(VTab::along(st_s[0], al, 32 * i, kk), val_at(kk), m);
+                    for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.st[0], al, 32 * (i - 2 * hh), kk), val[kk], z);
                     ordered<T, 4, 1>();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[i][j] = __builtin_fmaf(m[j], e * dc, acc[i][j]);
+                    for (int j = 0; j < 16; ++j) acc[i][j] = __builtin_fmaf(z[j], f_s * d_s, acc[i][j]);
                 }
             }
-            qi = half_add(qi);
-            if (h == 0) {
-                leave(TOK_Q_BLOCKS * L + at, qo);
-                leave(TOK_Q_STATE * L + at, qi);
-                leave(TOK_XDU * L + at, xdu + qi);
-                leave(TOK_XDY * L + at, zd);
+            if (32 * rb < live) {
+                const float *hi_s = m.dec + DEC_HI * L, *lo_s = m.dec + DEC_LO * L, *ahead_s = m.dec + DEC_AHEAD * L;
+                const float behind = m.dec[DEC_BEHIND * L + at];
+                for (int tb = rb; tb < NB && 32 * tb < live; ++tb) {
+                    f32x16 gm = zero16(), z = zero16();
+                    const uint32_t nal = opaque(na), val4 = opaque(va), ndn = opaque(nd), vdn = opaque(vd);
+#pragma unroll
+                    for (int kk = 0; kk < KN; ++kk) gm = mma32(NTab::along(m.rows, nal, 32 * tb, kk), own[kk], gm);
+                    ordered<T, KN, 1>();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.vals, val4, 32 * tb, kk), val[kk], z);
+                    ordered<T, 4, 1>();
+                    if (tb > rb) {
+                        const float f = behind * between(m.dec, rb, tb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int t = 32 * tb + acc_rows(i, l);
+                            const f32x4 as = *reinterpret_cast<const f32x4*>(ahead_s + t);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float e = t + j < live ? as[j] * f : 0.f;  // no copies of the last token
+                                gm[4 * i + j] *= e;
+                                q_blocks = __builtin_fmaf(gm[4 * i + j], z[4 * i + j], q_blocks);
+                                z[4 * i + j] *= e * d_s;
+                            }
+                        }
+                    } else {
+                        const float hc = hi_s[at], lc = lo_s[at];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int t = 32 * tb + acc_rows(i, l);
+                            const f32x4 ht = *reinterpret_cast<const f32x4*>(hi_s + t), lt = *reinterpret_cast<const f32x4*>(lo_s + t);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                // pairs that are none: exp2(-inf)
+                                const float e = exp2_hw(at <= t + j && t + j < live ? (ht[j] - hc) + (lt[j] - lc) : -INFINITY);
+                                const float eg = e * gm[4 * i + j], zv = z[4 * i + j];
+                                xdu = __builtin_fmaf(eg, zv, xdu);
+                                xdy += t + j == at ? zv : 0.f;
+                                gm[4 * i + j] = eg;
+                                z[4 * i + j] = e * zv * d_s;
+                            }
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const Frag<T> mv = acc_frag<T>(gm, b), zv = acc_frag<T>(z, b);
+#pragma unroll
+                        for (int pt = 0; pt < 2; ++pt) du[pt] = mma32(VRead::down(m.vals, vdn, 32 * tb + 16 * b, 32 * pt), mv, du[pt]);
+#pragma unroll
+                        for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * tb + 16 * b, 32 * i), zv, acc[i]);
+                        ordered<T, 2 + TN, 2>();
+                    }
+                }
             }
             if (at < live) {
                 const float skip = a.D ? a.D[head] : 0.f;
-                T* dx = (T*)a.dx + ((row0 + at) * a.H + head) * a.P + p0;
-                const uint32_t row = opaque(vr);
+                T* dx = (T*)a.dx + ((k.row0 + at) * a.H + head) * a.P + p0;
+                const uint32_t vr = VRead::row_at(at);
 #pragma unroll
                 for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int p = 32 * pt + acc_rows(q, l);
-                        const f32x4 yv = VRead::row4(y_s, row, pt, q);
+                        const f32x4 yv = VRead::row4(m.vals, vr, pt, q);
                         float v[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            v[j] = dc * du[pt][4 * q + j];
+                            v[j] = d_s * du[pt][4 * q + j];
                             if (a.D) v[j] = __builtin_fmaf(skip, yv[j], v[j]);
                         }
-                        store4<T>(dx + p, v[0], v[1], v[2], v[3]);
+                        store4<T>(dx + 32 * pt + acc_rows(q, l), v[0], v[1], v[2], v[3]);
                     }
             }
+            if (sub == per_head - 1) {  // the head's sums are complete
+                float* o = a.token + ((size_t)k.id * a.H + head) * kTokens<L>;
+                const float qb = half_add(q_blocks), qs = half_add(q_state), xd = half_add(xdu), xy = half_add(xdy);
+                if (h == 0) {
+                    o[TOK_Q_BLOCKS * L + at] = qb;
+                    o[TOK_Q_STATE * L + at] = qs;
+                    o[TOK_XDU * L + at] = (qb + xd) + qs;
+                    o[TOK_XDY * L + at] = xy;  // the pair t = s is one half's
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (sub == per_head - 1) {  // the head's sums are complete
-            float* o = a.token + ((size_t)id * a.H + head) * kTokens<L>;
-            for (int i = tid; i < kTokens<L>; i += NTH) o[i] = tok_s[i];
-            if (slice + 1 < h_last * per_head) __syncthreads();
-        }
+        store(a, k, acc, true, 32 * rb + (lane_id() & 31));
     }
-    const int at = 32 * rb + (lane_id() & 31);
-    if (at < live) {
-        const size_t o = ((row0 + at) * a.G + g) * N;
-        if (a.splits == 1) {
-            T* out = (T*)(is_s ? a.dB : a.dC) + o;
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    store4<T>(out + 32 * i + acc_rows(q), acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
-        } else {
-            float* out = a.part + ((size_t)(is_s ? 0 : a.splits) + sp) * a.T * a.G * N + o;
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    store4<float>(out + 32 * i + acc_rows(q), acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
-        }
-    }
+};
+
+template <typename T, int N>
+__global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), sizeof(T) == 2 ? 2 : 1) void ssm_grad_kernel(GradArgs a)
+{
+    constexpr int L = SsmTile<T>::L;
+    __shared__ __align__(16) GradLds<T, N> m;
+    // Parts in turn by 32 workgroups of a die: as many as it has compute units, each
+    // of which then gets one of either.
+    const long long j = blockIdx.x >> 3;
+    const bool is_s = (j >> 5) & 1;
+    const int jobs = a.G * a.splits;
+    long long unit;
+    int job;
+    Chunk k;
+    deal((((j >> 6) << 5 | (j & 31)) << 3) | (blockIdx.x & 7), jobs, unit, job);
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, unit, k.u)) return;
+    const int per_group = a.H / a.G;
+    k.id = unit;
+    k.c = k.u.at;
+    k.live = k.u.n - k.c * L < L ? k.u.n - k.c * L : L;
+    k.row0 = (size_t)k.u.start + (size_t)k.c * L;
+    k.g = job / a.splits;
+    k.sp = job - k.g * a.splits;
+    k.h_first = k.g * per_group + (int)((long long)per_group * k.sp / a.splits);
+    k.h_last = k.g * per_group + (int)((long long)per_group * (k.sp + 1) / a.splits);
+    if (is_s)
+        Grad<T, N>::of_s(a, k, m);
+    else
+        Grad<T, N>::of_t(a, k, m);
 }
 
 // dB and dC from the parts of a group's heads, in order: a word of 4 values a thread
@@ -522,8 +583,10 @@ template <typename T, int N> gdn_status grad(const gdn_ssm_shape& s, const SsmPl
 {
     constexpr int L = SsmTile<T>::L;
     if (p.chunks) {
-        const dim3 grid((unsigned)((p.chunks + 7) / 8 * 8 * s.G * p.splits));
-        GDN_LAUNCH("ssm_grad", (ssm_grad_kernel<T, N>), grid, dim3(4 * L), st, a);
+        // whole 32s of workgroups a die, for both parts
+        const long long a_die = (p.chunks + 7) / 8 * s.G * p.splits;
+        const dim3 grid((unsigned)((a_die + 31) / 32 * 32 * 8 * 2));
+        GDN_LAUNCH("ssm_grad", (ssm_grad_kernel<T, N>), grid, dim3(2 * L), st, a);
     }
     if (p.splits > 1) {
         const int width = s.G * N;

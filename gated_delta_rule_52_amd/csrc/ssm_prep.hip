@@ -130,12 +130,12 @@ __global__ __launch_bounds__(256) void ssm_finish_kernel(FinishArgs a)
     const float* more = v + TOK_ROWS * L;
     double rest = 0;
 #pragma unroll
-    for (int b = 0; b < 2 * NB; ++b) rest += (double)more[b];  // <S, dS>, by wave
+    for (int b = 0; b < NB; ++b) rest += (double)more[b];  // <S, dS>
     rest *= (double)dec[DEC_ROWS * L + DEC_KEEP];
     if constexpr (NB == 4) {  // across blocks 1 and 2
         const int b = l / LB;
-        if (b == 1) rest += (double)more[8] + (double)more[9];
-        if (b == 2) rest += (double)more[10];
+        if (b == 1) rest += (double)more[4] + (double)more[5];
+        if (b == 2) rest += (double)more[6];
     }
     const float A = a.A[head], bias = a.bias ? a.bias[head] : 0.f;
     double sa = 0, sd = 0, sb = 0;

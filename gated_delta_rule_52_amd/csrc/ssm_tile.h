@@ -91,10 +91,10 @@ enum { DEC_KEEP, DEC_TOTAL };
 // What ssm_grad.hip leaves of a chunk and head for the steps' gradients, a row of L
 // values each: sums of r from the state before and from earlier blocks, of q / delta
 // into the state behind and into later blocks, the pairs of the token's own block
-// that pass over it, x . du and x . dy.  Behind them <S, dS> by wave, and, in chunks of
+// that pass over it, x . du and x . dy.  Behind them <S, dS> by block, and, in chunks of
 // four blocks, the sums of the pairs between blocks (2, 0), (3, 0), and (3, 0) + (3, 1).
 enum { TOK_R_STATE, TOK_R_BLOCKS, TOK_Q_STATE, TOK_Q_BLOCKS, TOK_OWN, TOK_XDU, TOK_XDY, TOK_ROWS };
-template <int L> constexpr int kTokens = TOK_ROWS * L + 12;  // floats a chunk and head
+template <int L> constexpr int kTokens = TOK_ROWS * L + 8;  // floats a chunk and head
 
 // v as three bf16 each: the upper 8 bits of its 24, the next, the rest.  Cut off and
 // not rounded, which leaves all bits and takes fewer instructions.
