@@ -40,6 +40,7 @@ struct SsmArgs {
 struct SsmPlan {
     int L;              // tokens of a chunk
     int slices;         // H P / 64
+    int pairs;          // of slices in a group, the last of which may lack its second
     long long chunks;   // at most, over all sequences
     long long between;  // states between chunks, at most
     int seg;            // chunks of a segment; 0: a sequence is one segment

@@ -39,7 +39,7 @@ struct GradArgs {
     const void *x, *B, *C, *dy;
     const float *dec, *D, *h0, *dhT;
     const int* cu;
-    const float *fwd, *back;  // [states][slices][N][64]
+    const float *fwd, *back;  // [states][slices] states
     void *dx, *dB, *dC;
     float *token, *part;  // token: [chunks][H][kTokens]; part: [2][splits][T][G][N]
     long long xs, bs, cs;
@@ -126,7 +126,7 @@ template <typename T, int N> struct Grad {
     using VTab = Rows<T, kSlice>;
     using NRead = Reads<T, N>;
     using VRead = Reads<T, kSlice>;
-    using State = f32x4[SW][2];
+    using State = float[SW][8];
 
     template <typename R> static __device__ __forceinline__ void fetch(char* tab, const T* base, long long stride, int live, int l)
     {
@@ -135,35 +135,38 @@ template <typename T, int N> struct Grad {
             R::template fetch<16>(tab, r, base + (size_t)rr * stride, (uint32_t)(stride * sizeof(T)), live - 1 - rr, l);
         }
     }
-    // half hh of a state: between chunks [N][64], at a sequence's edge [N][P]
+    // Rows 64 hh .. + 63 of a state, as a table of its 64 values along them: run i of a
+    // thread is 8 rows of value p.  At a sequence's edge a state is [N][P].
     static __device__ __forceinline__ void load_state(const GradArgs& a, const Chunk& k, const float* between, long long which,
                                                       const float* edge, int slice, int hh, int tid, State& v)
     {
         const int per_head = a.P / kSlice, head = slice / per_head;
         const float* s = edge ? edge + (((size_t)k.u.b * a.H + head) * N + 64 * hh) * a.P + (slice - head * per_head) * kSlice
                               : between + (((size_t)which * a.slices + slice) * N + 64 * hh) * kSlice;
-        const int stride = edge ? a.P : kSlice;
 #pragma unroll
         for (int i = 0; i < SW; ++i) {
-            const int x = i * NTH + tid, n = x >> 3, q = x & 7;
-            v[i][0] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q);
-            v[i][1] = *reinterpret_cast<const f32x4*>(s + (size_t)n * stride + 8 * q + 4);
+            const int x = i * NTH + tid, p = x & 63, n = x >> 6 << 3;
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = s[(size_t)(n + j) * a.P + p];
+            } else {
+                load_state8(s, n, p, v[i]);
+            }
         }
     }
     static __device__ __forceinline__ void put_state(GradLds<T, N>& m, int tid, const State& v)
     {
 #pragma unroll
         for (int i = 0; i < SW; ++i) {
-            const int x = i * NTH + tid, n = x >> 3, q = x & 7;
+            const int x = i * NTH + tid, p = x & 63, q = x >> 6;
             if constexpr (sizeof(T) == 2) {
                 u32x4 parts[3];
-                const float f[8] = {v[i][0][0], v[i][0][1], v[i][0][2], v[i][0][3], v[i][1][0], v[i][1][1], v[i][1][2], v[i][1][3]};
-                split(f, parts);
+                split(v[i], parts);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(m.st[p] + VTab::word(n, q) * 16) = parts[p];
+                for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x4*>(m.st[j] + VTab::word(p, q) * 16) = parts[j];
             } else {
-                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(n, 2 * q) * 16) = v[i][0];
-                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(n, 2 * q + 1) * 16) = v[i][1];
+                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(p, 2 * q) * 16) = f32x4{v[i][0], v[i][1], v[i][2], v[i][3]};
+                *reinterpret_cast<f32x4*>(m.st[0] + VTab::word(p, 2 * q + 1) * 16) = f32x4{v[i][4], v[i][5], v[i][6], v[i][7]};
             }
         }
     }
@@ -198,7 +201,7 @@ template <typename T, int N> struct Grad {
         const int w = uniform(wave_id()), rb = w, live = k.live, per_head = a.P / kSlice;
         const bool has_s = k.c > 0 || a.h0, has_d = k.c < k.u.chunks - 1 || a.dhT;
         fetch<NTab>(m.rows, (const T*)a.B + k.row0 * a.bs + (size_t)k.g * N, a.bs, live, lane_id());
-        const uint32_t na = NTab::along_at(), va = VTab::along_at(), nd = NRead::down_at();
+        const uint32_t na = NTab::along_at(), va = VTab::along_at(), nd = NRead::down_at(), vp = VRead::plain_at();
         const int mine = 32 * rb + (lane_id() & 31), row = mine < live ? mine : live - 1;
         Frag<T> own[KN], val[4];  // the lane's rows of C and dy
 #pragma unroll
@@ -238,7 +241,7 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                         for (int i = 0; i < SW; ++i)
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(sv[i][j >> 2][j & 3], dv[i][j >> 2][j & 3], dot);
+                            for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(sv[i][j], dv[i][j], dot);
                     }
                 }
                 if (hh == 0) wait_vm<0>();
@@ -248,12 +251,12 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                 for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
                     f32x16 z = zero16();
-                    const uint32_t al = opaque(va);
+                    const uint32_t pl = opaque(vp);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.st[p], al, 32 * (i - 2 * hh), kk), val[kk], z);
-                    ordered<T, 4 * PARTS, 1>();
+                        for (int kk = 0; kk < 4; ++kk) z = mma32(VRead::plain(m.st[p], pl, 16 * kk, 32 * (i - 2 * hh)), val[kk], z);
+                    ordered<T, 4 * PARTS, 2>();
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const Frag<T> cv = permuted<T>(own[2 * i + b]);
@@ -414,13 +417,12 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                 for (int pt = 0; pt < 2; ++pt) {
                     f32x16 z = zero16();
-                    const uint32_t pl = opaque(vp);
+                    const uint32_t al = opaque(va);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            z = mma32(VRead::plain(m.st[p], pl, 16 * kk, 32 * pt), own[4 * hh + kk], z);
-                    ordered<T, 4 * PARTS, 2>();
+                        for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.st[p], al, 32 * pt, kk), own[4 * hh + kk], z);
+                    ordered<T, 4 * PARTS, 1>();
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const Frag<T> xv = permuted<T>(val[2 * pt + b]);
@@ -436,10 +438,10 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                 for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
                     f32x16 z = zero16();
-                    const uint32_t al = opaque(va);
+                    const uint32_t pl = opaque(vp);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) z = mma32(VTab::along(m.st[0], al, 32 * (i - 2 * hh), kk), val[kk], z);
-                    ordered<T, 4, 1>();
+                    for (int kk = 0; kk < 4; ++kk) z = mma32(VRead::plain(m.st[0], pl, 16 * kk, 32 * (i - 2 * hh)), val[kk], z);
+                    ordered<T, 4, 2>();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[i][j] = __builtin_fmaf(z[j], f_s * d_s, acc[i][j]);
                 }
@@ -548,7 +550,7 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), sizeof(T) == 2 ? 2 : 1) 
     int job;
     Chunk k;
     deal((((j >> 6) << 5 | (j & 31)) << 3) | (blockIdx.x & 7), jobs, unit, job);
-    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, unit, k.u)) return;
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, 0, unit, k.u)) return;
     const int per_group = a.H / a.G;
     k.id = unit;
     k.c = k.u.at;
@@ -584,7 +586,7 @@ template <typename T, int N> gdn_status grad(const gdn_ssm_shape& s, const SsmPl
     constexpr int L = SsmTile<T>::L;
     if (p.chunks) {
         // whole 32s of workgroups a die, for both parts
-        const long long a_die = (p.chunks + 7) / 8 * s.G * p.splits;
+        const long long a_die = dealt(p.chunks, s.G * p.splits) / 8;
         const dim3 grid((unsigned)((a_die + 31) / 32 * 32 * 8 * 2));
         GDN_LAUNCH("ssm_grad", (ssm_grad_kernel<T, N>), grid, dim3(2 * L), st, a);
     }

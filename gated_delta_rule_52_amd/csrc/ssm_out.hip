@@ -20,7 +20,7 @@ struct OutArgs {
     const void *x, *B, *C;
     const float *dec, *D;
     const int* cu;
-    const void* between;  // [states][slices][64][N], then each sequence's first
+    const void* between;  // [states][slices] states, then each sequence's first
     void* y;
     long long xs, bs, cs, firsts;
     int nb, T, H, P, per_group, slices, parts, first;
@@ -42,13 +42,13 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
     int part;
     deal(blockIdx.x, a.parts, id, part);
     Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, id, u)) return;
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, 0, id, u)) return;
     const int c = u.at, live = u.n - c * L < L ? u.n - c * L : L;
     const size_t row0 = (size_t)u.start + (size_t)c * L;
     const int l = lane_id(), h = l >> 5, w = uniform(wave_id());
     // later rows have more to do: the order is turned round from block to block,
     // for the waves of two workgroups on one SIMD
-    const int rb = (blockIdx.x >> 3) & 1 ? NW - 1 - w : w;
+    const int rb = (blockIdx.x >> 8) & 1 ? NW - 1 - w : w;
     const int per_head = a.P / kSlice, s_first = (int)((long long)part * a.slices / a.parts),
               s_last = (int)((long long)(part + 1) * a.slices / a.parts);
 
@@ -79,8 +79,20 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), 2) void ssm_out_kernel(O
         }
         if (state) {
             const T* s = (const T*)a.between + ((size_t)(c > 0 ? u.between + c - 1 : a.firsts + u.b) * a.slices + slice) * kSlice * N;
-            for (int r = 16 * w; r < kSlice; r += 16 * NW)
-                NTab::template fetch<16>(s_s, r, s + (size_t)r * N, (uint32_t)(N * sizeof(T)), 15);
+            constexpr int VE = 16 / (int)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < N / VE * kSlice / (64 * NW); ++i) {
+                const int x = i * 64 * NW + threadIdx.x, p = x % kSlice, q = x / kSlice;  // word q of row p
+                u32x4 word;
+                if constexpr (sizeof(T) == 2) {
+                    const uint2 lo = *reinterpret_cast<const uint2*>(s + (8 * q) * kSlice + 4 * p),
+                                hi = *reinterpret_cast<const uint2*>(s + (8 * q + 4) * kSlice + 4 * p);
+                    word = u32x4{lo.x, lo.y, hi.x, hi.y};
+                } else {
+                    word = *reinterpret_cast<const u32x4*>(s + (4 * q) * kSlice + 4 * p);
+                }
+                *reinterpret_cast<u32x4*>(s_s + NTab::word(p, q) * 16) = word;
+            }
         }
         const float* dec = a.dec + ((size_t)id * a.H + head) * kDecays<L>;
         if (threadIdx.x < L) {
@@ -175,7 +187,7 @@ template <typename T, int N> gdn_status out(const SsmPlan& p, OutArgs a, hipStre
     int parts = a.slices;
     while (parts > 1 && p.chunks * (parts / 2) >= 1024) parts /= 2;
     a.parts = parts;
-    const dim3 grid((unsigned)((p.chunks + 7) / 8 * 8 * parts));
+    const dim3 grid(dealt(p.chunks, parts));
     GDN_LAUNCH("ssm_out", (ssm_out_kernel<T, N>), grid, dim3(64 * (SsmTile<T>::L / 32)), st, a);
     return GDN_OK;
 }

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void ssm_prep_kernel(PrepArgs a)
 {
     constexpr int K = L / 64, LB = 32 / K;  // tokens a lane; lanes a block of 32 tokens
     Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, blockIdx.x, u)) return;
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, 0, blockIdx.x, u)) return;
     const int head = blockIdx.y * 4 + wave_id(), l = lane_id();
     if (head >= a.H) return;
     const int live = u.n - u.at * L < L ? u.n - u.at * L : L;
@@ -72,8 +72,10 @@ __global__ __launch_bounds__(256) void ssm_prep_kernel(PrepArgs a)
         o[DEC_HI * L + t] = hi;
         o[DEC_LO * L + t] = (float)(x - (double)hi);
         o[DEC_DELTA * L + t] = d[k];
-        o[DEC_E * L + t] = exp2_hw((float)x);
-        o[DEC_F * L + t] = exp2_hw((float)(total - x));
+        const float f = exp2_hw((float)(total - x));
+        o[DEC_E * L + t] = t < live ? exp2_hw((float)x) : 0.f;
+        o[DEC_F * L + t] = f;
+        o[DEC_FD * L + t] = f * d[k];
         o[DEC_AHEAD * L + t] = exp2_hw((float)(x - start));
         o[DEC_BEHIND * L + t] = exp2_hw((float)(end - x));
     }
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(256) void ssm_finish_kernel(FinishArgs a)
 {
     constexpr int K = L / 64, LB = 32 / K, NB = L / 32;
     Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, blockIdx.x, u)) return;
+    if (!find_unit<L>(a.cu, a.nb, a.T, L, 0, 0, blockIdx.x, u)) return;
     const int head = blockIdx.y * 4 + wave_id(), l = lane_id();
     if (head >= a.H) return;
     const int live = u.n - u.at * L < L ? u.n - u.at * L : L;

@@ -21,57 +21,63 @@ template <> struct SsmTile<float> {
 };
 
 // Units of `len` tokens (chunks, segments) of packed sequences, in the order of
-// the sequences.  Unit `id`: the at-th of `count` of sequence b, whose rows are
-// start .. start + n - 1; chunks: of the sequence; before, between: the chunks, and
-// the states between chunks, of all sequences before it.  Every sequence has `least`
-// units or more.
+// the sequences.  A sequence has `count` of them, of which count - drop are dealt out,
+// `least` at least.  Unit `id` of those: the at-th of sequence b, whose rows are
+// start .. start + n - 1; chunks: of the sequence; first: the units, before, between:
+// the chunks and the states between chunks, of all sequences before it.
 struct Unit {
     int b, at, count, start, n, chunks;
-    long long before, between;
+    long long first, before, between;
 };
 template <int L>
-__device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int T, int len, int least, long long id, Unit& u)
+__device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int T, int len, int drop, int least, long long id,
+                                          Unit& u)
 {
     const int l = lane_id();
-    long long before = 0, between = 0, chunks = 0;
+    long long dealt = 0, first = 0, between = 0, chunks = 0;
     for (int b0 = 0; b0 < B; b0 += 64) {
         const int b = b0 + l < B ? b0 + l : B - 1;
         int st = cu[b], en = cu[b + 1];
         st = st < 0 ? 0 : st > T ? T : st;
         en = en < st ? st : en > T ? T : en;
-        const int n = en - st, ch = (n + L - 1) / L;
-        int nu = (n + len - 1) / len;
-        nu = b0 + l < B ? (nu < least ? least : nu) : 0;
-        const int nbt = b0 + l < B && ch > 1 ? ch - 1 : 0;
-        const int nch = b0 + l < B ? ch : 0, inc = wave_scan(nu), incb = wave_scan(nbt), incc = wave_scan(nch);
-        const uint64_t hit = __ballot(before + inc > id);
+        const bool real = b0 + l < B;
+        const int n = en - st, ch = real ? (n + L - 1) / L : 0, count = real ? (n + len - 1) / len : 0;
+        const int nu = real ? (count - drop < least ? least : count - drop) : 0, nbt = ch > 1 ? ch - 1 : 0;
+        const int inc = wave_scan(nu), incf = wave_scan(count), incb = wave_scan(nbt), incc = wave_scan(ch);
+        const uint64_t hit = __ballot(dealt + inc > id);
         if (hit) {
-            const int first = __builtin_ctzll(hit);
-            u.b = b0 + first;
-            u.count = __builtin_amdgcn_readlane(nu, first);
-            u.at = (int)(id - before) - (__builtin_amdgcn_readlane(inc, first) - u.count);
-            u.start = __builtin_amdgcn_readlane(st, first);
-            u.n = __builtin_amdgcn_readlane(n, first);
-            u.chunks = __builtin_amdgcn_readlane(ch, first);
-            u.before = chunks + __builtin_amdgcn_readlane(incc, first) - u.chunks;
-            u.between = between + __builtin_amdgcn_readlane(incb, first) - __builtin_amdgcn_readlane(nbt, first);
+            const int k = __builtin_ctzll(hit);
+            auto here = [&](int x) { return __builtin_amdgcn_readlane(x, k); };
+            u.b = b0 + k;
+            u.count = here(count);
+            u.at = (int)(id - dealt) - (here(inc) - here(nu));
+            u.start = here(st);
+            u.n = here(n);
+            u.chunks = here(ch);
+            u.first = first + here(incf) - u.count;
+            u.before = chunks + here(incc) - u.chunks;
+            u.between = between + here(incb) - here(nbt);
             return true;
         }
-        before += __builtin_amdgcn_readlane(inc, 63);
+        dealt += __builtin_amdgcn_readlane(inc, 63);
+        first += __builtin_amdgcn_readlane(incf, 63);
         between += __builtin_amdgcn_readlane(incb, 63);
         chunks += __builtin_amdgcn_readlane(incc, 63);
     }
     return false;
 }
 
-// Workgroup -> (unit, slice), the slices of a unit on one die: they read the same
-// B and C, and workgroups go to the 8 dies in turn.  The grid is a multiple of 8 units.
+// Workgroup -> (unit, slice).  Workgroups go to the 8 dies in turn; four slices of a
+// unit, which read the same B and C, are one die's, and the dies have equal numbers (a
+// unit's slices all on one: up to 72 of 480 workgroups on a die with room for 64 at a
+// time, and nearly twice the time).  The grid is a multiple of 32.
 __device__ __forceinline__ void deal(long long id, int slices, long long& unit, int& slice)
 {
-    const long long j = id >> 3;
-    unit = (j / slices) * 8 + (id & 7);
-    slice = (int)(j % slices);
+    const long long k = id >> 3, flat = ((k >> 2) * 8 + (id & 7)) * 4 + (k & 3);
+    unit = flat / slices;
+    slice = (int)(flat - unit * slices);
 }
+inline unsigned dealt(long long units, int slices) { return (unsigned)((units * slices + 31) / 32 * 32); }
 
 // log(1 + exp(v)), v itself from where they agree in fp32
 __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
@@ -82,11 +88,11 @@ __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1p
 // 48 bits.  Blocks are of 32 tokens; E_ts of t in a later block than s is
 // AHEAD_t exp(c at the start of t's block - c at the end of s's) BEHIND_s, factors
 // that decay throughout, so that a pair costs a product and no exponential.
-enum { DEC_HI, DEC_LO, DEC_DELTA, DEC_E, DEC_F, DEC_AHEAD, DEC_BEHIND, DEC_ROWS };
+enum { DEC_HI, DEC_LO, DEC_DELTA, DEC_E, DEC_F, DEC_FD, DEC_AHEAD, DEC_BEHIND, DEC_ROWS };
 template <int L> constexpr int kDecays = DEC_ROWS * L + 4;  // floats a chunk and head
 enum { DEC_KEEP, DEC_TOTAL };
-//   E: exp(c), F: exp(c_L - c), AHEAD: exp(c - c before the block), BEHIND: exp(c at
-//   the block's end - c); behind the last token delta is 0 and c stays as it is
+//   E: exp(c), F: exp(c_L - c), FD: that times delta, AHEAD: exp(c - c before the block), BEHIND: exp(c at
+//   the block's end - c); behind the last token delta and E are 0 and c stays as it is
 
 // What ssm_grad.hip leaves of a chunk and head for the steps' gradients, a row of L
 // values each: sums of r from the state before and from earlier blocks, of q / delta
@@ -114,6 +120,16 @@ __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&w)[3])
         a -= upper(a), b -= upper(b);
         w[2][i] = upper_halves(a, b);
     }
+}
+
+// A state of N rows of 64 values in memory, as the walk's lanes hold it: value p of
+// row n at (n / 4) 256 + 4 p + n % 4.  Eight rows of one value, from the two runs of
+// four, are a word of bf16 (or two of fp32) of a table of 64 rows p along n.
+__device__ __forceinline__ void load_state8(const float* s, int n, int p, float (&v)[8])
+{
+    const f32x4 a = *reinterpret_cast<const f32x4*>(s + n * kSlice + 4 * p), b = *reinterpret_cast<const f32x4*>(s + (n + 4) * kSlice + 4 * p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
 }
 
 // Reads of a row table (Rows) from a lane's byte offset, all others of a kind being

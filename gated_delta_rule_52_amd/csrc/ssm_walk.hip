@@ -4,12 +4,12 @@
 //   S_out  = exp(c_L) S_in  + B^T (exp(c_L - c) delta x)     over a sequence's chunks
 //   dS_in  = exp(c_L) dS_out + C^T (exp(c) dy)               over them in reverse
 //
-// A workgroup walks a segment of a sequence with a slice of 64 of a head's values,
-// its N x 64 state in fp32 accumulators: four waves, each 32 of the 64 values and
-// half of N.  The scaled operand (f x) is split into three bf16 that hold all its
-// bits, so the state is as exact as in fp32.  Rows of both operands are read down
-// the tokens by transposing loads; the next chunk's are on their way in registers
-// meanwhile, and two workgroups share a compute unit.
+// A workgroup walks a segment of a sequence with two slices of 64 of its heads'
+// values: a wave has 32 of them, whose N x 32 state it keeps in fp32 accumulators.
+// It reads both operands down the tokens by transposing loads, scales its own (f x)
+// and splits it into three bf16 that hold all its bits, so that the state is as
+// exact as in fp32: three products for one, which leave time for that and for the
+// next chunk's direct loads into the other buffer.
 //
 // Where sequences are cut into segments, a first launch walks the first of them as
 // it is and forms what the others but the last contribute from a zero state; the
@@ -28,8 +28,8 @@ struct WalkArgs {
     const void *rows, *vals;  // B and x, or C and dy
     const float* init;        // h0 or dhT
     float* last;              // hT or dh0
-    float *seg, *tot;         // [segs][slices][N][64], [segs][slices]
-    void* between;            // [states][slices][..]; for the outputs, then each sequence's first
+    float *seg, *tot;         // [segs][slices] states and logarithms of decays
+    void* between;            // [states][slices] states; for the outputs, then each sequence's first
     long long rs, vs;
 };
 struct WalkCall {
@@ -37,172 +37,220 @@ struct WalkCall {
     const float* dec;
     const int* cu;
     long long firsts;
-    int nb, T, H, P, per_group, slices, seg_len;
+    int nb, T, H, P, per_group, slices, pairs, seg_len;  // pairs: of slices, in a group
 };
 
 template <typename T, int N> struct WalkLds {
     static constexpr int L = SsmTile<T>::L;
-    char rows[L * Rows<T, N>::BYTES], vals[SsmTile<T>::PARTS][L * Rows<T, kSlice>::BYTES];
+    char rows[2][L * Rows<T, N>::BYTES], vals[2][2][L * Rows<T, kSlice>::BYTES];
+    float f[2][2][L];
 };
 
 // PHASE 0: all segments of a sequence but the last; 1: all but the first, or the only
-// one.  OUT: states as T [64][N] (operands of the outputs), otherwise fp32 [N][64].
+// one.  OUT: states between chunks as T (operands of the outputs), otherwise fp32.
 template <typename T, int N, bool BACK, int PHASE, bool OUT>
 __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& g, WalkLds<T, N>& m)
 {
-    constexpr int L = SsmTile<T>::L, PARTS = SsmTile<T>::PARTS, NT = N / 64;
+    constexpr int L = SsmTile<T>::L, PARTS = SsmTile<T>::PARTS, NT = N / 32, KK = L / 16;
     using RT = Rows<T, N>;
     using VT = Rows<T, kSlice>;
-    constexpr int RW = L * RT::U / 256, VW = L * VT::U / 256;  // words a thread stages
 
     long long id;
-    int slice;
-    deal(blockIdx.x, a.slices, id, slice);
+    int pair;
+    deal(blockIdx.x, a.H / a.per_group * a.pairs, id, pair);
     Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, a.seg_len * L, 1, id, u)) return;
-    const int order = BACK ? u.count - 1 - u.at : u.at;
-    if (PHASE == 0 ? order == u.count - 1 : order == 0 && u.count > 1) return;
-    const int per_head = a.P / kSlice, head = slice / per_head, p0 = (slice - head * per_head) * kSlice;
-    const int l = lane_id(), w = uniform(wave_id()), pt = w & 1, n0 = (w >> 1) * (N / 2), tid = threadIdx.x;
-    const int col = 32 * pt + (l & 31);
+    if (!find_unit<L>(a.cu, a.nb, a.T, a.seg_len * L, 1, PHASE, id, u)) return;
+    if (u.count > 1 && (PHASE == 1) != BACK) ++u.at;  // the first of the walk is left out, or the last
+    const int order = BACK && u.count ? u.count - 1 - u.at : u.at;
+    const int w = uniform(wave_id()), l = lane_id(), which = w >> 1, pt = w & 1;
+    const int group = pair / a.pairs, per_head = a.P / kSlice, in_group = a.per_group * per_head;
+    const int at_group = 2 * (pair - group * a.pairs) + which;
+    const bool live_slice = at_group < in_group;  // an odd slice has no neighbour: its waves take the other's place and write nothing
+    const int slice = group * in_group + (live_slice ? at_group : at_group - 1);
+    const int head = slice / per_head, p0 = (slice - head * per_head) * kSlice, col = 32 * pt + (l & 31);
 
-    const int c0 = u.at * a.seg_len, c1 = u.chunks - c0 < a.seg_len ? u.chunks : c0 + a.seg_len;
-    const T* rows = (const T*)g.rows + (size_t)(head / a.per_group) * N;
+    const int c0 = u.at * a.seg_len, c1 = u.chunks - c0 < a.seg_len ? u.chunks : c0 + a.seg_len, count = c1 - c0;
+    const T* rows = (const T*)g.rows + (size_t)group * N;
     const T* vals = (const T*)g.vals + (size_t)head * a.P + p0;
-    u32x4 rw[RW], vw[VW];
-    float fw[VW], keep, total;
-    auto live_of = [&](int c) { return u.n - c * L < L ? u.n - c * L : L; };
-    auto load = [&](int c) {
-        const int live = live_of(c);
-        const size_t row0 = (size_t)u.start + (size_t)c * L;
-        const float* dec = a.dec + ((size_t)(u.before + c) * a.H + head) * kDecays<L>;
-        keep = dec[DEC_ROWS * L + DEC_KEEP];
-        total = dec[DEC_ROWS * L + DEC_TOTAL];
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            const int x = i * 256 + tid, r = x / VT::U, v = x % VT::U;
-            vw[i] = *reinterpret_cast<const u32x4*>(vals + (row0 + (r < live ? r : live - 1)) * g.vs + v * (16 / sizeof(T)));
-            fw[i] = BACK ? (r < live ? dec[DEC_E * L + r] : 0.f) : dec[DEC_F * L + r] * dec[DEC_DELTA * L + r];
-        }
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-            const int x = i * 256 + tid, r = x / RT::U, v = x % RT::U;
-            rw[i] = *reinterpret_cast<const u32x4*>(rows + (row0 + (r < live ? r : live - 1)) * g.rs + v * (16 / sizeof(T)));
-        }
+    auto chunk_of = [&](int k) { return BACK ? c1 - 1 - k : c0 + k; };
+    float keep_next = 1.f, total_next = 0.f;
+    // Chunk k into a buffer by direct loads, in KK shares: a wave loads a quarter of the
+    // rows, and half of its slice's values and factors (0 behind the last token, whose
+    // rows are copies).  FULL: a chunk of L tokens, lane offsets from the row before.
+    constexpr int RI = L / 4 / RT::PER, VI = L / 2 / VT::PER;  // direct loads of a wave
+    const uint32_t r_row = (uint32_t)(g.rs * sizeof(T)), v_row = (uint32_t)(g.vs * sizeof(T));
+    struct Source {
+        const char *rows, *vals;
+        const float* dec;
+        int live;
     };
-    const int count = c1 - c0;
-    if (count > 0) load(BACK ? c1 - 1 : c0);
+    auto source_of = [&](int k) {
+        const int c = chunk_of(k);
+        const size_t row0 = (size_t)u.start + (size_t)c * L;
+        return Source{(const char*)(rows + row0 * g.rs), (const char*)(vals + row0 * g.vs),
+                      a.dec + ((size_t)(u.before + c) * a.H + head) * kDecays<L>, u.n - c * L < L ? u.n - c * L : L};
+    };
+    const uint32_t r_off = (l / RT::U) * r_row, v_off = (l / VT::U) * v_row;
+    auto load = [&](const Source& s, int buf, int part, auto FULL) {
+#pragma unroll
+        for (int i = VI * part / KK; i < VI * (part + 1) / KK; ++i) {
+            const int r = L / 2 * pt + i * VT::PER, rr = r + l / VT::U;
+            const uint32_t word = ((l % VT::U) ^ VT::f(rr)) * 16;
+            char* to = m.vals[buf][which] + r * VT::BYTES;
+            if constexpr (FULL())
+                dma16_at(s.vals + (size_t)r * v_row, v_off + word, to);
+            else
+                dma16_at(s.vals, (uint32_t)(rr < s.live ? rr : s.live - 1) * v_row + word, to);
+        }
+#pragma unroll
+        for (int i = RI * part / KK; i < RI * (part + 1) / KK; ++i) {
+            const int r = L / 4 * w + i * RT::PER, rr = r + l / RT::U;
+            const uint32_t word = ((l % RT::U) ^ RT::f(rr)) * 16;
+            char* to = m.rows[buf] + r * RT::BYTES;
+            if constexpr (FULL())
+                dma16_at(s.rows + (size_t)r * r_row, r_off + word, to);
+            else
+                dma16_at(s.rows, (uint32_t)(rr < s.live ? rr : s.live - 1) * r_row + word, to);
+        }
+        if (part == 0 && (L == 128 || pt == 0))
+            dma4(s.dec + (BACK ? DEC_E : DEC_FD) * L + 64 * pt + l, m.f[buf][which] + 64 * pt);
+    };
+    if (count > 0) {
+        const Source s = source_of(0);
+        keep_next = s.dec[DEC_ROWS * L + DEC_KEEP];
+        total_next = s.dec[DEC_ROWS * L + DEC_TOTAL];
+#pragma unroll
+        for (int part = 0; part < KK; ++part) load(s, 0, part, std::false_type{});
+    }
 
     f32x16 acc[NT];
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = zero16();
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] = f(acc[i][r], 32 * i + acc_rows(r >> 2) + (r & 3), i, r);
+    };
+    each([&](float, int, int, int) { return 0.f; });
     if (order == 0) {
         if (g.init) {
-            const float* s = g.init + (((size_t)u.b * a.H + head) * N + n0) * a.P + p0 + col;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][r] = s[(size_t)(32 * i + acc_rows(r >> 2) + (r & 3)) * a.P];
+            const float* s = g.init + ((size_t)u.b * a.H + head) * N * a.P + p0 + col;
+            each([&](float, int n, int, int) { return s[(size_t)n * a.P]; });
         }
     } else if (PHASE == 1) {
-        const long long first = BACK ? id - u.at + u.count - 1 : id - u.at;
-        for (int k = 0; k < order; ++k) {
-            const size_t at = (size_t)(BACK ? first - k : first + k) * a.slices + slice;
-            const float e = exp2_hw(g.tot[at]);
-            const float* s = g.seg + (at * N + n0) * kSlice + col;
+        const long long first = BACK ? u.first + u.count - 1 : u.first;
+        auto at_of = [&](int k) { return (size_t)(BACK ? first - k : first + k) * a.slices + slice; };
+        f32x16 next[NT];
+        auto load_next = [&](int k) {
+            const float* s = g.seg + at_of(k) * N * kSlice + col * 4;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float v = s[(32 * i + acc_rows(r >> 2) + (r & 3)) * kSlice];
-                    acc[i][r] = k ? __builtin_fmaf(acc[i][r], e, v) : v;
+                for (int r = 0; r < 16; r += 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(s + (32 * i + acc_rows(r >> 2)) * kSlice);
+                    next[i][r] = v[0], next[i][r + 1] = v[1], next[i][r + 2] = v[2], next[i][r + 3] = v[3];
                 }
+        };
+        load_next(0);
+        each([&](float, int, int i, int r) { return next[i][r]; });
+        if (order > 1) load_next(1);
+        for (int k = 1; k < order; ++k) {
+            const float e = exp2_hw(g.tot[at_of(k)]);
+            each([&](float v, int, int i, int r) { return __builtin_fmaf(v, e, next[i][r]); });
+            if (k + 1 < order) load_next(k + 1);
         }
     }
 
+    // a state as four rows of N after the other, their values side by side: what a lane
+    // holds is stored as it stands (StateAt)
+    auto store_state = [&](auto* s) {
+        typedef std::remove_reference_t<decltype(*s)> S;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                store4<S>(s + (32 * i + acc_rows(r >> 2)) * kSlice + col * 4, acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+    };
+    auto store_between = [&](long long state) {
+        typedef std::conditional_t<OUT, T, float> S;
+        if (live_slice) store_state((S*)g.between + ((size_t)state * a.slices + slice) * N * kSlice);
+    };
     float tot = 0.f;
-    for (int k = 0; k < count; ++k) {
-        const int c = BACK ? c1 - 1 - k : c0 + k;
-        __syncthreads();  // the tables of the chunk before are read
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            const int x = i * 256 + tid, at = VT::word(x / VT::U, x % VT::U) * 16;
-            if constexpr (sizeof(T) == 2) {
-                float v[8];
-                u32x4 parts[3];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = __uint_as_float(vw[i][j] << 16) * fw[i];
-                    v[2 * j + 1] = upper(__uint_as_float(vw[i][j])) * fw[i];
-                }
-                split(v, parts);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(m.vals[p] + at) = parts[p];
-            } else {
-                u32x4 v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(__uint_as_float(vw[i][j]) * fw[i]);
-                *reinterpret_cast<u32x4*>(m.vals[0] + at) = v;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-            const int x = i * 256 + tid;
-            *reinterpret_cast<u32x4*>(m.rows + RT::word(x / RT::U, x % RT::U) * 16) = rw[i];
-        }
+    // chunk k, from buffer k % 2
+    auto step = [&](int k, auto BUF) {
+        constexpr int buf = BUF();
+        wait_vm<0>();
         __syncthreads();
-        const float e = keep;
-        tot += total;
-        if (k + 1 < count) load(BACK ? c - 1 : c + 1);
-        const bool edge = c == (BACK ? u.chunks - 1 : 0);
-        if ((PHASE == 1 || order == 0) && (!edge || (OUT && g.init))) {
-            const size_t at = (size_t)(edge ? a.firsts + u.b : u.between + (BACK ? c : c - 1)) * a.slices + slice;
-            if constexpr (OUT) {
-                T* s = (T*)g.between + (at * kSlice + col) * N + n0;
+        const float keep = keep_next;
+        tot += total_next;
+        const Source next = source_of(k + 1 < count ? k + 1 : k);  // behind the last chunk it is loaded again
+        keep_next = next.dec[DEC_ROWS * L + DEC_KEEP];
+        total_next = next.dec[DEC_ROWS * L + DEC_TOTAL];
+        if (PHASE == 1 || order == 0) {
+            const int c = chunk_of(k);
+            if (c != (BACK ? u.chunks - 1 : 0))
+                store_between(u.between + (BACK ? c : c - 1));
+            else if (OUT && g.init)
+                store_between(a.firsts + u.b);
+        }
+        each([&](float v, int, int, int) { return v * keep; });
+        __builtin_amdgcn_sched_barrier(0);
+        Frag<T> f[2][NT], raw;
+        f32x4 f0, f1;
+        auto read = [&](int kk, Frag<T> (&o)[NT]) {
+            const float* fs = m.f[buf][which] + 16 * kk + acc_rows(0);  // permuted order
+            raw = VT::down(m.vals[buf][which], 16 * kk, 32 * pt);
+            f0 = *reinterpret_cast<const f32x4*>(fs);
+            f1 = *reinterpret_cast<const f32x4*>(fs + 8);
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) o[i] = RT::down(m.rows[buf], 16 * kk, 32 * i);
+        };
+        Frag<T> v[2][PARTS];
+        auto scale = [&](Frag<T> (&o)[PARTS]) {
+            float x[8];
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4)
-                        store4<T>(s + 32 * i + acc_rows(r >> 2), acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+            for (int j = 0; j < 8; ++j) x[j] = (float)raw[j] * (j < 4 ? f0[j & 3] : f1[j & 3]);
+            if constexpr (sizeof(T) == 2) {
+                u32x4 p[3];
+                split(x, p);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) o[i] = __builtin_bit_cast(bf16x8, p[i]);
             } else {
-                float* s = (float*)g.between + (at * N + n0) * kSlice + col;
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[(32 * i + acc_rows(r >> 2) + (r & 3)) * kSlice] = acc[i][r];
+                for (int j = 0; j < 8; ++j) o[0][j] = x[j];
             }
-        }
+        };
+        auto products = [&](auto FULL) {
+            read(0, f[0]);
+            scale(v[0]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int kk = 0; kk < KK; ++kk) {
+                if (kk + 1 < KK) read(kk + 1, f[(kk + 1) & 1]);
+                load(next, buf ^ 1, kk, FULL);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][r] *= e;
+                for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-        for (int kk = 0; kk < L / 16; ++kk) {
-            Frag<T> f[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) f[i] = RT::down(m.rows, 16 * kk, n0 + 32 * i);
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                const Frag<T> v = VT::down(m.vals[p], 16 * kk, 32 * pt);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) acc[i] = mma32(f[i], v, acc[i]);
+                    for (int i = 0; i < NT; ++i) acc[i] = mma32(f[kk & 1][i], v[kk & 1][p], acc[i]);
+                if (kk + 1 < KK) scale(v[(kk + 1) & 1]);
             }
-        }
+        };
+        if (next.live == L)
+            products(std::true_type{});
+        else
+            products(std::false_type{});
+    };
+    for (int k = 0; k < count; k += 2) {
+        step(k, std::integral_constant<int, 0>{});
+        if (k + 1 < count) step(k + 1, std::integral_constant<int, 1>{});
     }
+    wait_vm<0>();  // the last chunk's second load
+    if (!live_slice) return;
     if (PHASE == 0) {
-        const size_t at = (size_t)id * a.slices + slice;
-        if (tid == 0) g.tot[at] = tot;
-        float* s = g.seg + (at * N + n0) * kSlice + col;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[(32 * i + acc_rows(r >> 2) + (r & 3)) * kSlice] = acc[i][r];
-    } else if (g.last && order == u.count - 1) {
-        float* s = g.last + (((size_t)u.b * a.H + head) * N + n0) * a.P + p0 + col;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[(size_t)(32 * i + acc_rows(r >> 2) + (r & 3)) * a.P] = acc[i][r];
+        const size_t at = (size_t)(u.first + u.at) * a.slices + slice;
+        if (pt == 0 && l == 0) g.tot[at] = tot;
+        store_state(g.seg + at * N * kSlice);
+    } else if (g.last && order >= u.count - 1) {
+        float* s = g.last + ((size_t)u.b * a.H + head) * N * a.P + p0 + col;
+        each([&](float v, int n, int, int) { return s[(size_t)n * a.P] = v; });
     }
 }
 
@@ -218,7 +266,8 @@ __global__ __launch_bounds__(256, 2) void ssm_walk_kernel(WalkCall a)
 
 template <typename T, int N, bool OUT> gdn_status walk(const SsmPlan& p, const WalkCall& a, hipStream_t st)
 {
-    const dim3 grid((unsigned)((p.segs + 7) / 8 * 8 * p.slices), OUT ? 1 : 2);
+    // a sequence has one segment fewer in the first launch, and in the second one at least
+    const dim3 grid(dealt(p.segs, a.H / a.per_group * a.pairs), OUT ? 1 : 2);
     if (p.seg) GDN_LAUNCH("ssm_walk_segments", (ssm_walk_kernel<T, N, 0, OUT>), grid, dim3(256), st, a);
     GDN_LAUNCH("ssm_walk", (ssm_walk_kernel<T, N, 1, OUT>), grid, dim3(256), st, a);
     return GDN_OK;
@@ -251,7 +300,7 @@ gdn_status ssm_walk(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& x, 
     a.dec = (const float*)(ws + p.dec_at);
     a.cu = x.cu;
     a.firsts = p.between;
-    a.nb = s.B; a.T = s.T; a.H = s.H; a.P = s.P; a.per_group = s.H / s.G; a.slices = p.slices;
+    a.nb = s.B; a.T = s.T; a.H = s.H; a.P = s.P; a.per_group = s.H / s.G; a.slices = p.slices; a.pairs = p.pairs;
     a.seg_len = p.seg ? p.seg : s.T / p.L + 1;  // longer than any sequence
     return s.dtype == GDN_BF16 ? walk<bf16>(s.N, backward, p, a, st) : walk<float>(s.N, backward, p, a, st);
 }
