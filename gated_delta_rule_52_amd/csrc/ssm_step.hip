@@ -111,19 +111,16 @@ SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward)
     p.pairs = (p.slices / s.G + 1) / 2;
     p.chunks = s.T ? s.T / p.L + (s.B < s.T ? s.B : s.T) : 0;
     p.between = s.T / p.L;  // n tokens have ceil(n / L) - 1 <= n / L states between their chunks
-    // Segments: where whole sequences are fewer than 512 workgroups (two a compute
-    // unit), about as many segments as make them, of 4 chunks or more.
-    // Segments: the first launch walks all but the last of a sequence's, the second
-    // all but the first, and a workgroup begins with a sum over those before its own.
-    // As many as keep either launch within a workgroup for each compute unit (they take
-    // all of its LDS), so that none waits for another; three at least (two are as long as
-    // one, in two launches), none below 4 chunks.
+    // Segments: the first launch walks all but the last of a sequence's, the last one
+    // all but the first.  As many as keep either launch within two workgroups a compute
+    // unit, which is what fits; three at least (two are as long as one, in two
+    // launches), none below 2 chunks.
     const long long whole = (long long)s.B * s.G * p.pairs * (backward ? 2 : 1), each = (p.between + s.B - 1) / s.B;
-    long long want = 1 + 256 / whole, seg = 0;
+    long long want = 1 + 512 / whole, seg = 0;
     if (want > 32) want = 32;
-    if (want > 2 && each > 8) {
+    if (want > 2 && each > 6) {
         seg = (each + want - 1) / want;
-        if (seg < 4) seg = 4;
+        if (seg < 2) seg = 2;
     }
     p.seg = (int)seg;
     p.segs = seg ? s.T / (seg * p.L) + s.B : s.B;

@@ -122,6 +122,16 @@ __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&w)[3])
     }
 }
 
+// a wave-uniform address in LDS as its offset there, and dma16_at (attn.h) to one
+__device__ __forceinline__ uint32_t lds_offset(const void* p)
+{
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p);
+}
+__device__ __forceinline__ void dma16_to(const void* base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+
 // A state of N rows of 64 values in memory, as the walk's lanes hold it: value p of
 // row n at (n / 4) 256 + 4 p + n % 4.  Eight rows of one value, from the two runs of
 // four, are a word of bf16 (or two of fp32) of a table of 64 rows p along n.

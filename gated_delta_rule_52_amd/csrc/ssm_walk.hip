@@ -8,14 +8,19 @@
 // values: a wave has 32 of them, whose N x 32 state it keeps in fp32 accumulators.
 // It reads both operands down the tokens by transposing loads, scales its own (f x)
 // and splits it into three bf16 that hold all its bits, so that the state is as
-// exact as in fp32: three products for one, which leave time for that and for the
-// next chunk's direct loads into the other buffer.
+// exact as in fp32: three products for one.  Half a chunk is in LDS at a time, the
+// other half on its way there by direct loads, so that two workgroups share a compute
+// unit: a wave alone on its SIMD issues its products, its splitting and its reads one
+// after the other (6.2 thousand cycles for 96 products that take 3.2).
 //
 // Where sequences are cut into segments, a first launch walks the first of them as
-// it is and forms what the others but the last contribute from a zero state; the
-// second launch walks those with the sum of all before them: most products are
-// formed twice, fewer in a row.  The given state is read by the first segment's
-// workgroup alone and the last state written behind it, so they may be one.
+// it is and forms what the others but the last contribute from a zero state, a second
+// adds these up along the sequence, and a third walks the segments but the first from
+// there: most products are formed twice, fewer in a row.  The given state is read by
+// the first segment's workgroup alone and the last state written behind it, so they
+// may be one.
+#include <stddef.h>
+
 #include "ssm_tile.h"
 
 #include "common.h"
@@ -42,8 +47,9 @@ struct WalkCall {
 
 template <typename T, int N> struct WalkLds {
     static constexpr int L = SsmTile<T>::L;
-    char rows[2][L * Rows<T, N>::BYTES], vals[2][2][L * Rows<T, kSlice>::BYTES];
-    float f[2][2][L];
+    static constexpr int H = L / 2;
+    char rows[2][H * Rows<T, N>::BYTES], vals[2][2][H * Rows<T, kSlice>::BYTES];
+    float f[2][2][64];
 };
 
 // PHASE 0: all segments of a sequence but the last; 1: all but the first, or the only
@@ -51,9 +57,10 @@ template <typename T, int N> struct WalkLds {
 template <typename T, int N, bool BACK, int PHASE, bool OUT>
 __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& g, WalkLds<T, N>& m)
 {
-    constexpr int L = SsmTile<T>::L, PARTS = SsmTile<T>::PARTS, NT = N / 32, KK = L / 16;
+    constexpr int L = SsmTile<T>::L, HALF = L / 2, PARTS = SsmTile<T>::PARTS, NT = N / 32, KK = HALF / 16;
     using RT = Rows<T, N>;
     using VT = Rows<T, kSlice>;
+    using Lds = WalkLds<T, N>;
 
     long long id;
     int pair;
@@ -74,53 +81,56 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
     const T* vals = (const T*)g.vals + (size_t)head * a.P + p0;
     auto chunk_of = [&](int k) { return BACK ? c1 - 1 - k : c0 + k; };
     float keep_next = 1.f, total_next = 0.f;
-    // Chunk k into a buffer by direct loads, in KK shares: a wave loads a quarter of the
-    // rows, and half of its slice's values and factors (0 behind the last token, whose
-    // rows are copies).  FULL: a chunk of L tokens, lane offsets from the row before.
-    constexpr int RI = L / 4 / RT::PER, VI = L / 2 / VT::PER;  // direct loads of a wave
+    // Half a chunk into its buffer by direct loads, in KK shares: a wave loads a quarter
+    // of the rows, and half of its slice's values and factors (0 behind the last token,
+    // whose rows are copies).
+    constexpr int RI = HALF / 4 / RT::PER, VI = HALF / 2 / VT::PER;  // direct loads of a wave
     const uint32_t r_row = (uint32_t)(g.rs * sizeof(T)), v_row = (uint32_t)(g.vs * sizeof(T));
     struct Source {
         const char *rows, *vals;
         const float* dec;
-        int live;
+        int live;  // of the half's tokens
     };
-    auto source_of = [&](int k) {
-        const int c = chunk_of(k);
-        const size_t row0 = (size_t)u.start + (size_t)c * L;
+    auto source_of = [&](int k, int half) {
+        const int c = chunk_of(k), from = c * L + half * HALF, live = u.n - from;
+        const size_t row0 = (size_t)u.start + (live < 1 ? u.n - 1 : from);
         return Source{(const char*)(rows + row0 * g.rs), (const char*)(vals + row0 * g.vs),
-                      a.dec + ((size_t)(u.before + c) * a.H + head) * kDecays<L>, u.n - c * L < L ? u.n - c * L : L};
+                      a.dec + ((size_t)(u.before + c) * a.H + head) * kDecays<L>, live < 1 ? 1 : live < HALF ? live : HALF};
     };
+    const uint32_t lds = lds_offset(&m);
     const uint32_t r_off = (l / RT::U) * r_row, v_off = (l / VT::U) * v_row;
-    auto load = [&](const Source& s, int buf, int part, auto FULL) {
+    auto load = [&](const Source& s, int buf, int part, bool full) {
 #pragma unroll
         for (int i = VI * part / KK; i < VI * (part + 1) / KK; ++i) {
-            const int r = L / 2 * pt + i * VT::PER, rr = r + l / VT::U;
-            const uint32_t word = ((l % VT::U) ^ VT::f(rr)) * 16;
-            char* to = m.vals[buf][which] + r * VT::BYTES;
-            if constexpr (FULL())
-                dma16_at(s.vals + (size_t)r * v_row, v_off + word, to);
+            const int r = HALF / 2 * pt + i * VT::PER, rr = r + l / VT::U;
+            const uint32_t word = ((l % VT::U) ^ VT::f(rr)) * 16, to = lds + (uint32_t)offsetof(Lds, vals) + (2 * buf + which) * HALF * VT::BYTES + r * VT::BYTES;
+            if (full)
+                dma16_to(s.vals + (size_t)r * v_row, v_off + word, to);
             else
-                dma16_at(s.vals, (uint32_t)(rr < s.live ? rr : s.live - 1) * v_row + word, to);
+                dma16_to(s.vals, (uint32_t)(rr < s.live ? rr : s.live - 1) * v_row + word, to);
         }
 #pragma unroll
         for (int i = RI * part / KK; i < RI * (part + 1) / KK; ++i) {
-            const int r = L / 4 * w + i * RT::PER, rr = r + l / RT::U;
-            const uint32_t word = ((l % RT::U) ^ RT::f(rr)) * 16;
-            char* to = m.rows[buf] + r * RT::BYTES;
-            if constexpr (FULL())
-                dma16_at(s.rows + (size_t)r * r_row, r_off + word, to);
+            const int r = HALF / 4 * w + i * RT::PER, rr = r + l / RT::U;
+            const uint32_t word = ((l % RT::U) ^ RT::f(rr)) * 16, to = lds + (uint32_t)offsetof(Lds, rows) + buf * HALF * RT::BYTES + r * RT::BYTES;
+            if (full)
+                dma16_to(s.rows + (size_t)r * r_row, r_off + word, to);
             else
-                dma16_at(s.rows, (uint32_t)(rr < s.live ? rr : s.live - 1) * r_row + word, to);
+                dma16_to(s.rows, (uint32_t)(rr < s.live ? rr : s.live - 1) * r_row + word, to);
         }
-        if (part == 0 && (L == 128 || pt == 0))
-            dma4(s.dec + (BACK ? DEC_E : DEC_FD) * L + 64 * pt + l, m.f[buf][which] + 64 * pt);
+        // 64 words for HALF factors: the rest is not read
+        if (part == 0 && pt == 0)
+            dma4(s.dec + (BACK ? DEC_E : DEC_FD) * L + HALF * buf + (HALF == 64 ? l : l & 31), m.f[buf][which]);
+    };
+    auto load_all = [&](const Source& s, int buf) {
+#pragma unroll
+        for (int part = 0; part < KK; ++part) load(s, buf, part, false);
     };
     if (count > 0) {
-        const Source s = source_of(0);
+        const Source s = source_of(0, 0);
         keep_next = s.dec[DEC_ROWS * L + DEC_KEEP];
         total_next = s.dec[DEC_ROWS * L + DEC_TOTAL];
-#pragma unroll
-        for (int part = 0; part < KK; ++part) load(s, 0, part, std::false_type{});
+        load_all(s, 0);
     }
 
     f32x16 acc[NT];
@@ -137,27 +147,15 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
             each([&](float, int n, int, int) { return s[(size_t)n * a.P]; });
         }
     } else if (PHASE == 1) {
-        const long long first = BACK ? u.first + u.count - 1 : u.first;
-        auto at_of = [&](int k) { return (size_t)(BACK ? first - k : first + k) * a.slices + slice; };
-        f32x16 next[NT];
-        auto load_next = [&](int k) {
-            const float* s = g.seg + at_of(k) * N * kSlice + col * 4;
+        const size_t at = (size_t)(u.first + u.at + (BACK ? 1 : -1)) * a.slices + slice;
+        const float* s = g.seg + at * N * kSlice + col * 4;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(s + (32 * i + acc_rows(r >> 2)) * kSlice);
-                    next[i][r] = v[0], next[i][r + 1] = v[1], next[i][r + 2] = v[2], next[i][r + 3] = v[3];
-                }
-        };
-        load_next(0);
-        each([&](float, int, int i, int r) { return next[i][r]; });
-        if (order > 1) load_next(1);
-        for (int k = 1; k < order; ++k) {
-            const float e = exp2_hw(g.tot[at_of(k)]);
-            each([&](float v, int, int i, int r) { return __builtin_fmaf(v, e, next[i][r]); });
-            if (k + 1 < order) load_next(k + 1);
-        }
+            for (int r = 0; r < 16; r += 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(s + (32 * i + acc_rows(r >> 2)) * kSlice);
+                acc[i][r] = v[0], acc[i][r + 1] = v[1], acc[i][r + 2] = v[2], acc[i][r + 3] = v[3];
+            }
     }
 
     // a state as four rows of N after the other, their values side by side: what a lane
@@ -175,24 +173,30 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
         if (live_slice) store_state((S*)g.between + ((size_t)state * a.slices + slice) * N * kSlice);
     };
     float tot = 0.f;
-    // chunk k, from buffer k % 2
-    auto step = [&](int k, auto BUF) {
-        constexpr int buf = BUF();
+    // half a chunk, from its buffer; the next one's loads on the way
+    auto step = [&](int k, auto HALF_OF) {
+        constexpr int buf = HALF_OF();
         wait_vm<0>();
         __syncthreads();
-        const float keep = keep_next;
-        tot += total_next;
-        const Source next = source_of(k + 1 < count ? k + 1 : k);  // behind the last chunk it is loaded again
-        keep_next = next.dec[DEC_ROWS * L + DEC_KEEP];
-        total_next = next.dec[DEC_ROWS * L + DEC_TOTAL];
-        if (PHASE == 1 || order == 0) {
-            const int c = chunk_of(k);
-            if (c != (BACK ? u.chunks - 1 : 0))
-                store_between(u.between + (BACK ? c : c - 1));
-            else if (OUT && g.init)
-                store_between(a.firsts + u.b);
+        // behind the last half it is loaded again
+        const Source next = buf == 0 ? source_of(k, 1) : k + 1 < count ? source_of(k + 1, 0) : source_of(k, 1);
+        if constexpr (buf == 0) {
+            const float keep = keep_next;
+            tot += total_next;
+            if (PHASE == 1 || order == 0) {
+                const int c = chunk_of(k);
+                if (c != (BACK ? u.chunks - 1 : 0))
+                    store_between(u.between + (BACK ? c : c - 1));
+                else if (OUT && g.init)
+                    store_between(a.firsts + u.b);
+            }
+            each([&](float v, int, int, int) { return v * keep; });
+        } else {
+            keep_next = next.dec[DEC_ROWS * L + DEC_KEEP];
+            total_next = next.dec[DEC_ROWS * L + DEC_TOTAL];
         }
-        each([&](float v, int, int, int) { return v * keep; });
+        const bool full = next.live == HALF;
+        if (!full) load_all(next, buf ^ 1);
         __builtin_amdgcn_sched_barrier(0);
         Frag<T> f[2][NT], raw;
         f32x4 f0, f1;
@@ -219,30 +223,24 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
                 for (int j = 0; j < 8; ++j) o[0][j] = x[j];
             }
         };
-        auto products = [&](auto FULL) {
-            read(0, f[0]);
-            scale(v[0]);
+        read(0, f[0]);
+        scale(v[0]);
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                if (kk + 1 < KK) read(kk + 1, f[(kk + 1) & 1]);
-                load(next, buf ^ 1, kk, FULL);
+        for (int kk = 0; kk < KK; ++kk) {
+            if (kk + 1 < KK) read(kk + 1, f[(kk + 1) & 1]);
+            if (full) load(next, buf ^ 1, kk, true);
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
+            for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) acc[i] = mma32(f[kk & 1][i], v[kk & 1][p], acc[i]);
-                if (kk + 1 < KK) scale(v[(kk + 1) & 1]);
-            }
-        };
-        if (next.live == L)
-            products(std::true_type{});
-        else
-            products(std::false_type{});
+                for (int i = 0; i < NT; ++i) acc[i] = mma32(f[kk & 1][i], v[kk & 1][p], acc[i]);
+            if (kk + 1 < KK) scale(v[(kk + 1) & 1]);
+        }
     };
-    for (int k = 0; k < count; k += 2) {
+    for (int k = 0; k < count; ++k) {
         step(k, std::integral_constant<int, 0>{});
-        if (k + 1 < count) step(k + 1, std::integral_constant<int, 1>{});
+        step(k, std::integral_constant<int, 1>{});
     }
-    wait_vm<0>();  // the last chunk's second load
+    wait_vm<0>();  // the last half's second load
     if (!live_slice) return;
     if (PHASE == 0) {
         const size_t at = (size_t)(u.first + u.at) * a.slices + slice;
@@ -264,11 +262,55 @@ __global__ __launch_bounds__(256, 2) void ssm_walk_kernel(WalkCall a)
         walk_segment<T, N, true, PHASE, OUT>(a, a.way[1], m);
 }
 
+// The states at the segments' ends, in place, from what each contributes: four values
+// a thread along a sequence's segments (blockIdx.y), those to come on their way.
+// blockIdx.x: slice and 1024 values of it; blockIdx.z: way.
+template <int L, int N> __global__ __launch_bounds__(256) void ssm_segments_kernel(WalkCall a)
+{
+    constexpr int BLOCKS = N * kSlice / 1024, AHEAD = 4;
+    const WalkArgs& g = a.way[blockIdx.z];
+    const bool back = blockIdx.z != 0;
+    Unit u;
+    if (!find_unit<L>(a.cu, a.nb, a.T, a.seg_len * L, 0x7fffffff, 1, blockIdx.y, u)) return;
+    const int slice = blockIdx.x / BLOCKS, many = u.count - 1;  // those of the first launch
+    const size_t at0 = (size_t)(u.first + (back ? u.count - 1 : 0)) * a.slices + slice;
+    const long long step = (back ? -1LL : 1LL) * a.slices;
+    float* s = g.seg + (blockIdx.x % BLOCKS * 256 + threadIdx.x) * 4;
+    auto at = [&](int k) { return s + (at0 + k * step) * N * kSlice; };
+    f32x4 v[AHEAD], acc{0.f, 0.f, 0.f, 0.f};
+    float decay[AHEAD];
+    auto fetch = [&](int k, int i) {
+        v[i] = *reinterpret_cast<const f32x4*>(at(k));
+        decay[i] = g.tot[at0 + k * step];
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (k < many) fetch(k, k);
+    for (int k0 = 0; k0 < many; k0 += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = k0 + i;
+            if (k < many) {
+                const float e = exp2_hw(decay[i]);
+                // the first is whole as it stands
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = k ? __builtin_fmaf(acc[j], e, v[i][j]) : v[i][j];
+                if (k + AHEAD < many) fetch(k + AHEAD, i);
+                if (k) *reinterpret_cast<f32x4*>(at(k)) = acc;
+            }
+        }
+    }
+}
+
 template <typename T, int N, bool OUT> gdn_status walk(const SsmPlan& p, const WalkCall& a, hipStream_t st)
 {
     // a sequence has one segment fewer in the first launch, and in the second one at least
     const dim3 grid(dealt(p.segs, a.H / a.per_group * a.pairs), OUT ? 1 : 2);
-    if (p.seg) GDN_LAUNCH("ssm_walk_segments", (ssm_walk_kernel<T, N, 0, OUT>), grid, dim3(256), st, a);
+    if (p.seg) {
+        GDN_LAUNCH("ssm_walk_segments", (ssm_walk_kernel<T, N, 0, OUT>), grid, dim3(256), st, a);
+        GDN_LAUNCH("ssm_segments", (ssm_segments_kernel<SsmTile<T>::L, N>), dim3(a.slices * (N / 16), a.nb, OUT ? 1 : 2),
+                   dim3(256), st, a);
+    }
     GDN_LAUNCH("ssm_walk", (ssm_walk_kernel<T, N, 1, OUT>), grid, dim3(256), st, a);
     return GDN_OK;
 }
