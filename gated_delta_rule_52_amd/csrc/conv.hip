@@ -10,12 +10,25 @@
 // fp32, rounded once when stored.  Bound by HBM: a thread holds one 16-byte word of
 // channels and walks down a strip of tokens with its window in registers, so that
 // every row is read once (but for the W - 1 rows between strips).
+//
+// A workgroup is CW words of channels by 256 / CW strips.  Of 64 words a wave is one
+// strip: its rows come as whole kilobytes, and where a sequence ends is a question for
+// scalar registers; of 16 words where 64 would leave more than a fifth of the lanes
+// without a channel.  32768 rows of 1024 bf16: forward 34 us (16 words: 41), 3.9 TB/s;
+// backward 50 us (without the rows to come on their way: 58), 4.0 TB/s.
 #include "conv.h"
 #include "common.h"
 
 namespace gdn {
 
 namespace {
+
+// a thread's word of channels in its workgroup, and its strip (or sequence)
+template <int CW> __device__ __forceinline__ int lane_word() { return threadIdx.x & (CW - 1); }
+template <int CW> __device__ __forceinline__ int lane_strip()
+{
+    return CW == 64 ? __builtin_amdgcn_readfirstlane(wave_id()) : (int)threadIdx.x / CW;
+}
 
 // one 16-byte word of channels
 template <typename T> struct Word;
@@ -218,20 +231,20 @@ __device__ __forceinline__ void head_rows(const ConvArgs& a, int b, int c)
     }
 }
 
-// blocks of 16 channel words x 16 strips; blockIdx.y: channels.  The first
-// a.head_blocks of blockIdx.x are 16 sequences each, the others 16 strips.
-template <typename T, int W, bool PAST>
+// blockIdx.y: channels.  The first a.head_blocks of blockIdx.x are sequences, the others strips.
+template <typename T, int W, int CW, bool PAST>
 __global__ __launch_bounds__(256) void conv_forward_kernel(ConvArgs a)
 {
     constexpr int VE = Word<T>::VE, K = W - 1, AHEAD = 8;
-    const int c = (blockIdx.y * 16 + (threadIdx.x & 15)) * VE, sub = threadIdx.x >> 4;
+    constexpr int NS = 256 / CW;
+    const int c = (blockIdx.y * CW + lane_word<CW>()) * VE, sub = lane_strip<CW>();
     if (c >= a.C) return;
     if ((int)blockIdx.x < a.head_blocks) {
-        const int b = blockIdx.x * 16 + sub;
+        const int b = blockIdx.x * NS + sub;
         if (b < a.B) head_rows<T, W>(a, b, c);
         return;
     }
-    const long long first = ((long long)(blockIdx.x - a.head_blocks) * 16 + sub) * a.strip;
+    const long long first = ((long long)(blockIdx.x - a.head_blocks) * NS + sub) * a.strip;
     if (first >= a.T) return;
     const int t0 = (int)first, t1 = a.T - t0 < a.strip ? a.T : t0 + a.strip;
     Seq s;
@@ -247,10 +260,18 @@ __global__ __launch_bounds__(256) void conv_forward_kernel(ConvArgs a)
         clear(win[j]);
         if (t >= 0) Word<T>::open(load_word(x + (size_t)t * a.x_stride), win[j]);
     }
+    u32x4 next[AHEAD];  // the rows to come are on their way while these are worked on
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) next[i] = load_word(x + (size_t)(t + i < t1 ? t + i : t1 - 1) * a.x_stride);
+    };
+    fetch(t0);
     for (int t = t0; t < t1; t += AHEAD) {
         u32x4 r[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) r[i] = load_word(x + (size_t)(t + i < t1 ? t + i : t1 - 1) * a.x_stride);
+        for (int i = 0; i < AHEAD; ++i) r[i] = next[i];
+        if (t + AHEAD < t1) fetch(t + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             if (t + i < t1) {
@@ -272,15 +293,15 @@ __global__ __launch_bounds__(256) void conv_forward_kernel(ConvArgs a)
 
 // Gradients.  A thread walks its strip and the W - 1 rows behind it, forms dz of
 // every row and with it dx of the row W - 1 before.  Its sums for the taps and the
-// bias go to `part` [strip blocks][W + 1][C], a block's 16 strips added in LDS, and
+// bias go to `part` [strip blocks][W + 1][C], a block's strips added in LDS, and
 // are added up by conv_finish_kernel: the same order in every run.
-template <typename T, int W, bool PAST>
+template <typename T, int W, int CW, bool PAST>
 __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a)
 {
-    constexpr int VE = Word<T>::VE, K = W - 1, AHEAD = 4;
-    __shared__ float tot[16][16 * VE + 1];
-    const int cw = threadIdx.x & 15, c = (blockIdx.y * 16 + cw) * VE, sub = threadIdx.x >> 4;
-    const long long first = ((long long)blockIdx.x * 16 + sub) * a.strip;
+    constexpr int VE = Word<T>::VE, K = W - 1, AHEAD = 4, NS = 256 / CW;
+    __shared__ float tot[NS][CW * VE + 1];
+    const int cw = lane_word<CW>(), c = (blockIdx.y * CW + cw) * VE, sub = lane_strip<CW>();
+    const long long first = ((long long)blockIdx.x * NS + sub) * a.strip;
     float dw[W][VE], db[VE];
     clear(db);
 #pragma unroll
@@ -309,14 +330,22 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a)
             }
         }
         // up to row last - 1, then K - (last - t1) rows that do not exist: the end of the buffer
-        for (int t = t0; t < t1 + K; t += AHEAD) {
-            u32x4 rx[AHEAD], ry[AHEAD];
+        u32x4 next_x[AHEAD], next_y[AHEAD];
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const int row = t + i < last ? t + i : last - 1;
-                rx[i] = load_word(x + (size_t)row * a.x_stride);
-                ry[i] = load_word(dy + (size_t)row * a.C);
+                next_x[i] = load_word(x + (size_t)row * a.x_stride);
+                next_y[i] = load_word(dy + (size_t)row * a.C);
             }
+        };
+        fetch(t0);
+        for (int t = t0; t < t1 + K; t += AHEAD) {
+            u32x4 rx[AHEAD], ry[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) rx[i] = next_x[i], ry[i] = next_y[i];
+            if (t + AHEAD < last) fetch(t + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const int row = t + i;
@@ -362,11 +391,10 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a)
                         }
 #pragma unroll
                         for (int k = 0; k < W; ++k) {  // dz of row to + k with tap K - k
-                            const bool in = to + k < ends[0];
+                            if (to + k < ends[0]) {
 #pragma unroll
-                            for (int e = 0; e < VE; ++e) {
-                                const float d = k < K ? dzs[k < K ? k : 0][e] : dz[e];
-                                g[e] = __builtin_fmaf(taps.w[K - k][e], in ? d : 0.f, g[e]);
+                                for (int e = 0; e < VE; ++e)
+                                    g[e] = __builtin_fmaf(taps.w[K - k][e], k < K ? dzs[k < K ? k : 0][e] : dz[e], g[e]);
                             }
                         }
                         store_word<PAST>((T*)a.dx + (size_t)to * a.C + c, Word<T>::close(g));
@@ -388,11 +416,12 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a)
 #pragma unroll
         for (int e = 0; e < VE; ++e) tot[sub][cw * VE + e] = q < W ? dw[q < W ? q : 0][e] : db[e];
         __syncthreads();
-        const int i = threadIdx.x, ch = blockIdx.y * 16 * VE + i;
-        if (i < 16 * VE && ch < a.C) {
+        for (int i = threadIdx.x; i < CW * VE; i += 256) {
+            const int ch = blockIdx.y * CW * VE + i;
+            if (ch >= a.C) break;
             float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += tot[k][i];
+            for (int k = 0; k < NS; ++k) sum += tot[k][i];
             a.part[((size_t)blockIdx.x * (W + 1) + q) * a.C + ch] = sum;
         }
     }
@@ -468,10 +497,16 @@ __global__ __launch_bounds__(256) void conv_dstate_kernel(ConvArgs a)
     }
 }
 
-int channel_blocks(const gdn_conv_shape& s)
+// words of channels a workgroup has
+int channel_words(const gdn_conv_shape& s)
+{
+    const int words = s.C / (s.dtype == GDN_BF16 ? 8 : 4), idle = (words + 63) / 64 * 64 - words;
+    return idle * 5 <= words ? 64 : 16;
+}
+int channel_blocks(const gdn_conv_shape& s, int cw)
 {
     const int words = s.C / (s.dtype == GDN_BF16 ? 8 : 4);
-    return (words + 15) / 16;
+    return (words + cw - 1) / cw;
 }
 
 // Tokens a thread walks: 32 where that leaves 512 threads a compute unit, fewer
@@ -496,17 +531,25 @@ template <typename F> gdn_status with_taps(int W, F&& f)
 // outputs larger than the L2 (4 MB on each of 8 dies) are not kept there
 bool past_l2(const gdn_conv_shape& s) { return (long long)s.T * s.C * (s.dtype == GDN_BF16 ? 2 : 4) > (32LL << 20); }
 
+template <typename F> gdn_status with_words(const gdn_conv_shape& s, F&& f)
+{
+    return channel_words(s) == 64 ? f(std::integral_constant<int, 64>{}) : f(std::integral_constant<int, 16>{});
+}
+
 template <typename T> gdn_status forward(const gdn_conv_shape& s, ConvArgs a, hipStream_t st)
 {
     a.strip = conv_strip(s);
-    a.head_blocks = (s.B + 15) / 16;
     const int strips = a.cu ? (s.T + a.strip - 1) / a.strip : 0;
-    const dim3 grid(a.head_blocks + (strips + 15) / 16, channel_blocks(s));
     return with_taps(s.W, [&](auto w) -> gdn_status {
         constexpr int W = decltype(w)::value;
-        return with_bool(past_l2(s), [&](auto past) -> gdn_status {
-            GDN_LAUNCH("conv_forward", (conv_forward_kernel<T, W, decltype(past)::value>), grid, dim3(256), st, a);
-            return GDN_OK;
+        return with_words(s, [&](auto cw) -> gdn_status {
+            constexpr int CW = decltype(cw)::value, NS = 256 / CW;
+            a.head_blocks = (s.B + NS - 1) / NS;
+            const dim3 grid(a.head_blocks + (strips + NS - 1) / NS, channel_blocks(s, CW));
+            return with_bool(past_l2(s), [&](auto past) -> gdn_status {
+                GDN_LAUNCH("conv_forward", (conv_forward_kernel<T, W, CW, decltype(past)::value>), grid, dim3(256), st, a);
+                return GDN_OK;
+            });
         });
     });
 }
@@ -518,16 +561,19 @@ template <typename T> gdn_status backward(const gdn_conv_shape& s, ConvArgs a, f
     return with_taps(s.W, [&](auto w) -> gdn_status {
         constexpr int W = decltype(w)::value;
         if (blocks) {
-            const gdn_status r = with_bool(past_l2(s), [&](auto past) -> gdn_status {
-                GDN_LAUNCH("conv_backward", (conv_backward_kernel<T, W, decltype(past)::value>),
-                           dim3(blocks, channel_blocks(s)), dim3(256), st, a);
-                return GDN_OK;
+            const gdn_status r = with_words(s, [&](auto cw) -> gdn_status {
+                constexpr int CW = decltype(cw)::value;
+                return with_bool(past_l2(s), [&](auto past) -> gdn_status {
+                    GDN_LAUNCH("conv_backward", (conv_backward_kernel<T, W, CW, decltype(past)::value>),
+                               dim3(blocks, channel_blocks(s, CW)), dim3(256), st, a);
+                    return GDN_OK;
+                });
             });
             if (r != GDN_OK) return r;
         }
         GDN_LAUNCH("conv_finish", (conv_finish_kernel<W>), dim3(cols), dim3(256), st, a.part, dw, db, blocks, s.C);
         if (a.dstate)
-            GDN_LAUNCH("conv_dstate", (conv_dstate_kernel<T, W>), dim3((s.B + 15) / 16, channel_blocks(s)), dim3(256), st, a);
+            GDN_LAUNCH("conv_dstate", (conv_dstate_kernel<T, W>), dim3((s.B + 15) / 16, channel_blocks(s, 16)), dim3(256), st, a);
         return GDN_OK;
     });
 }
@@ -536,8 +582,8 @@ template <typename T> gdn_status backward(const gdn_conv_shape& s, ConvArgs a, f
 
 int conv_partials(const gdn_conv_shape& s)
 {
-    const long long strip = conv_strip(s);
-    return (int)((s.T + 16 * strip - 1) / (16 * strip));
+    const long long rows = (long long)conv_strip(s) * (256 / channel_words(s));
+    return (int)((s.T + rows - 1) / rows);
 }
 
 gdn_status conv_forward_dispatch(const gdn_conv_shape& s, const ConvArgs& a, hipStream_t st)
