@@ -25,6 +25,7 @@ outputs that are allocated here.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -49,6 +50,13 @@ class GdnSsmShape(ctypes.Structure):
 class GdnPagesShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("rows", ctypes.c_int)]
+
+
+# The shapes of sizes, to be read only: a decoding step's calls are short enough for
+# the host to count, and a structure's fields take it longer than to find it.
+_conv_sizes = lru_cache(maxsize=256)(GdnConvShape)
+_ssm_sizes = lru_cache(maxsize=256)(GdnSsmShape)
+_pages_sizes = lru_cache(maxsize=256)(GdnPagesShape)
 
 
 def declare(L):
@@ -80,20 +88,24 @@ def _room(n, ws, device, name):
 # short causal convolution
 # ---------------------------------------------------------------------------
 def _conv_shape(x, weight, bias, state, B, silu, dev):
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, C], got {tuple(x.shape)}")
-    if weight.dim() != 2 or weight.shape[0] != x.shape[1]:
-        raise ValueError(f"weight must be [{x.shape[1]}, W], got {tuple(weight.shape)}")
-    (T, C), W = x.shape, weight.shape[1]
+    shape, taps, dtype = x.shape, weight.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, C], got {tuple(shape)}")
+    T, C = shape
+    if len(taps) != 2 or taps[0] != C:
+        raise ValueError(f"weight must be [{C}, W], got {tuple(taps)}")
+    W = taps[1]
     if (B | T | C | W) >> 31:
         raise _too_large(B, T, C, W)
     stride = 0
     if not x.is_contiguous() or x.get_device() != dev.index:
-        stride = _take(x.unsqueeze(1), "x", (T, 1, C), x.dtype, dev, stride=True)
-    _alike(dev, weight.shape, _F32, ("weight",), weight)
-    _alike(dev, weight.shape[:1], _F32, ("bias",), bias)
-    _alike(dev, (B, W - 1, C), x.dtype, ("state",), state)
-    return GdnConvShape(B, T, C, W, _dtype(x, "x"), int(bool(silu)), stride)
+        stride = _take(x.unsqueeze(1), "x", (T, 1, C), dtype, dev, stride=True)
+    _alike(dev, taps, _F32, ("weight",), weight)
+    if bias is not None:
+        _alike(dev, (C,), _F32, ("bias",), bias)
+    if state is not None:
+        _alike(dev, (B, W - 1, C), dtype, ("state",), state)
+    return _conv_sizes(B, T, C, W, _dtype(x, "x"), int(bool(silu)), stride)
 
 
 def gdn_conv_forward(x, weight, cu_seqlens, bias=None, state=None, *, silu=True, y=None, state_out=None,
@@ -147,7 +159,8 @@ def gdn_conv_step(x, weight, state, bias=None, *, silu=True, y=None):
     sh = _conv_shape(x, weight, bias, state, x.shape[0], silu, dev)
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _alike(dev, x.shape, x.dtype, ("y",), y)
+    else:
+        _alike(dev, x.shape, x.dtype, ("y",), y)
     if sh.T == 0:
         return y
     _run(lib().gdn_conv_step, "gdn_conv_step", dev, ctypes.byref(sh), _p(x), _p(weight), _p(bias), _p(state), _p(y))
@@ -158,18 +171,19 @@ def gdn_conv_step(x, weight, state, bias=None, *, silu=True, y=None):
 # selective state space scan
 # ---------------------------------------------------------------------------
 def _ssm_shape(x, dt, A, Bm, Cm, D, dt_bias, B, softplus, dev):
-    if x.dim() != 3 or Bm.dim() != 3:
-        raise ValueError(f"x must be [T, H, P] and B [T, G, N], got {tuple(x.shape)} and {tuple(Bm.shape)}")
-    (T, H, P), (G, N) = x.shape, Bm.shape[1:]
+    shape, pairs, dtype = x.shape, Bm.shape, x.dtype
+    if len(shape) != 3 or len(pairs) != 3:
+        raise ValueError(f"x must be [T, H, P] and B [T, G, N], got {tuple(shape)} and {tuple(pairs)}")
+    T, H, P = shape
+    _, G, N = pairs
     if (B | T | H | P | G | N) >> 31:
         raise _too_large(B, T, H, P, G, N)
-    dtype = x.dtype
-    xs = _take(x, "x", x.shape, dtype, dev, stride=True)
+    xs = _take(x, "x", shape, dtype, dev, stride=True)
     bs = _take(Bm, "B", (T, G, N), dtype, dev, stride=True)
     cs = _take(Cm, "C", (T, G, N), dtype, dev, stride=True)
     _alike(dev, (T, H), _F32, ("dt",), dt)
     _alike(dev, (H,), _F32, ("A", "D", "dt_bias"), A, D, dt_bias)
-    return GdnSsmShape(B, T, H, G, N, P, _dtype(x, "x"), int(bool(softplus)), xs, bs, cs)
+    return _ssm_sizes(B, T, H, G, N, P, _dtype(x, "x"), int(bool(softplus)), xs, bs, cs)
 
 
 def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens, *, D=None, dt_bias=None, softplus=True, h0=None, y=None, hT=None,
@@ -229,7 +243,8 @@ def gdn_ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, 
         raise ValueError("state is required")
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _alike(dev, x.shape, x.dtype, ("y",), y)
+    else:
+        _alike(dev, x.shape, x.dtype, ("y",), y)
     _alike(dev, (sh.B, sh.H, sh.N, sh.P), _F32, ("state",), state)
     if sh.T == 0:
         return y
@@ -243,19 +258,20 @@ def gdn_ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, 
 # ---------------------------------------------------------------------------
 def _pages_shape(flags, kv_len, page_table, free_pages, free_count, page_size, rows, kv_out, count_out, names):
     dev = _gpu(kv_len, "kv_len")
-    if kv_len.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != kv_len.shape[0]:
-        raise ValueError(f"kv_len must be [B] and page_table [B, max_pages], got {tuple(kv_len.shape)} and "
-                         f"{tuple(page_table.shape)}")
-    if free_pages.dim() != 1:
-        raise ValueError(f"free_pages must be [num_pages], got {tuple(free_pages.shape)}")
-    (B, width), pool = page_table.shape, free_pages.shape[0]
+    lens, table, stack = kv_len.shape, page_table.shape, free_pages.shape
+    if len(lens) != 1 or len(table) != 2 or table[0] != lens[0]:
+        raise ValueError(f"kv_len must be [B] and page_table [B, max_pages], got {tuple(lens)} and {tuple(table)}")
+    if len(stack) != 1:
+        raise ValueError(f"free_pages must be [num_pages], got {tuple(stack)}")
+    (B, width), pool = table, stack[0]
     if (B | width | pool | page_size | rows) >> 31:
         raise _too_large(B, width, pool, page_size, rows)
-    _alike(dev, (B,), _I32, names, flags, kv_len, kv_out)
-    _alike(dev, page_table.shape, _I32, ("page_table",), page_table)
-    _alike(dev, free_pages.shape, _I32, ("free_pages",), free_pages)
-    _alike(dev, (1,), _I32, ("free_count", "count_out"), free_count, count_out)
-    return GdnPagesShape(B, pool, page_size, width, rows), dev
+    # kv_out and count_out are kv_len and free_count where they are updated in place
+    _alike(dev, lens, _I32, names, flags, kv_len, None if kv_out is kv_len else kv_out)
+    _alike(dev, table, _I32, ("page_table",), page_table)
+    _alike(dev, stack, _I32, ("free_pages",), free_pages)
+    _alike(dev, (1,), _I32, ("free_count", "count_out"), free_count, None if count_out is free_count else count_out)
+    return _pages_sizes(B, pool, page_size, width, rows), dev
 
 
 def gdn_pages_release(done, kv_len, page_table, free_pages, free_count, page_size, *, kv_out=None, count_out=None):
