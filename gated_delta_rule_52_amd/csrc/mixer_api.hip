@@ -30,9 +30,9 @@ gdn_status check_conv(const gdn_conv_shape* sh, bool step, gdn_conv_shape& s)
     if (step && s.T != s.B) return GDN_ERR_INVALID_ARG;
     if (s.W < 2 || s.W > 4) return GDN_ERR_UNSUPPORTED;
     const int ve = s.dtype == GDN_BF16 ? 8 : 4;
-    // launches below 2^32 work-items, 16 sequences or 16 strips of 8 tokens or more a
-    // workgroup of 256, and rows of all channels in y
-    if (s.C % ve || s.C > (1 << 20) || s.T > (1 << 28) || s.B > (1 << 26)) return GDN_ERR_UNSUPPORTED;
+    // launches below 2^32 work-items, 4 sequences or 4 strips of 8 tokens or more (32
+    // where there are many) a workgroup of 256, and rows of all channels in y
+    if (s.C % ve || s.C > (1 << 20) || s.T > (1 << 28) || s.B > (1 << 25)) return GDN_ERR_UNSUPPORTED;
     if (!s.x_stride) s.x_stride = s.C;
     if (s.x_stride < s.C) return GDN_ERR_INVALID_ARG;
     if (s.x_stride % ve) return GDN_ERR_ALIGNMENT;
@@ -168,6 +168,7 @@ gdn_status gdn_ssm_forward(const gdn_ssm_shape* sh, const void* x, const float* 
     if (any_off16(x, B, C, h0, y, hT, ws) || any_off4(dt, A, D, dt_bias) || off4(cu_seqlens)) return GDN_ERR_ALIGNMENT;
     const SsmPlan p = ssm_plan(s, false);
     if (!ws || ws_bytes < p.bytes) return GDN_ERR_WORKSPACE;
+    if (s.T && y == x) return GDN_ERR_INVALID_ARG;
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.y = y; a.hT = hT;
@@ -195,8 +196,10 @@ gdn_status gdn_ssm_backward(const gdn_ssm_shape* sh, const void* x, const float*
         return GDN_ERR_ALIGNMENT;
     const SsmPlan p = ssm_plan(s, true);
     if (!ws || ws_bytes < p.bytes) return GDN_ERR_WORKSPACE;
-    // the gradients read dhT after the walk has written dh0
-    if (dhT && dhT == dh0) return GDN_ERR_INVALID_ARG;
+    // the gradients read h0 and dhT after the walk has written dh0, and one workgroup's
+    // operands after another has written its results
+    if (dh0 && (dhT == dh0 || h0 == dh0)) return GDN_ERR_INVALID_ARG;
+    if (s.T && (dx == x || dx == dy || dB == B || dB == C || dC == B || dC == C || dB == dC)) return GDN_ERR_INVALID_ARG;
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dy = dy; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.dhT = dhT; a.dx = dx; a.dB = dB; a.dC = dC; a.ddt = ddt; a.dA = dA; a.dD = dD; a.dbias = ddt_bias; a.dh0 = dh0;
@@ -218,6 +221,7 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape* sh, const void* x, const float* dt,
     if (r != GDN_OK) return r;
     if (any_null(x, B, C, (const void*)y) || !dt || !A || !state) return GDN_ERR_INVALID_ARG;
     if (any_off16(x, B, C, state, y) || any_off4(dt, A, D, dt_bias)) return GDN_ERR_ALIGNMENT;
+    if (y == x) return GDN_ERR_INVALID_ARG;
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.y = y;
     a.xs = s.x_stride; a.bs = s.b_stride; a.cs = s.c_stride;

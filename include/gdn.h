@@ -413,7 +413,8 @@ gdn_status gdn_attn_paged(const gdn_attn_shape *shape, const void *q, const void
  * conventions of the part above hold: sequences are packed, cu_seqlens and every
  * other int array are device data, clamped or checked where they are used, and
  * rows of no sequence are neither used nor written.  Weights, steps and states of
- * the scan are float32 (4-byte aligned where they are per head).
+ * the scan are float32 (4-byte aligned where they are per head).  Outputs may not
+ * overlap inputs or one another, but where a call says that one may be the other.
  * ---------------------------------------------------------------------------
  *
  * Short causal convolution along the tokens, every channel by itself: with e the
@@ -424,7 +425,7 @@ gdn_status gdn_attn_paged(const gdn_attn_shape *shape, const void *q, const void
  *   [T, C] dense; weight, dweight [C, W], bias, dbias [C] float32 (bias may be
  *   NULL); states [B, W - 1, C] (dtype), oldest row first.
  * W is 2, 3 or 4; C a multiple of 8 (bf16) or 4 (float32), at most 2^20; T at most
- * 2^28, B at most 2^26.  y may not be x, nor dx x or dy.
+ * 2^28, B at most 2^25.  y may not be x, nor dx x or dy.
  *
  * gdn_conv_forward: state_out (NULL: not written) may be state.  A sequence
  * without rows keeps its state.
@@ -471,7 +472,7 @@ gdn_status gdn_conv_step(const gdn_conv_shape *shape, const void *x, const float
  * gdn_ssm_forward: y, and hT the state behind each sequence (NULL: not written; may
  * be h0; a sequence without rows keeps its state).
  * gdn_ssm_backward: gradients of sum(y dy) + sum(hT dhT) (dhT NULL = zero); dD,
- * ddt_bias and dh0 may be NULL, and dh0 may not be dhT.  The states are formed
+ * ddt_bias and dh0 may be NULL.  The states are formed
  * again; nothing is kept between the calls.  Float32 results, and hT, are as exact
  * for bf16 inputs as for the same values in float32.
  * Both: ws holds gdn_ssm_workspace_bytes(shape, GDN_SSM_...) bytes; calls that

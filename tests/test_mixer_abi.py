@@ -49,7 +49,7 @@ def conv_backward(sh, x=P, w=P, cu=P, dy=P, dx=Q, dw=P, ws=P, n=BIG):
 @pytest.mark.parametrize("bad,code", [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(C=0), 1), (dict(dtype=2), 1), (dict(silu=2), 1), (dict(x_stride=-8), 1),
     (dict(x_stride=56), 1), (dict(W=1), 2), (dict(W=5), 2), (dict(C=60), 2), (dict(C=6, dtype=0), 2), (dict(x_stride=68), 3),
-    (dict(C=(1 << 20) + 8), 2), (dict(T=(1 << 28) + 1), 2), (dict(B=(1 << 26) + 1), 2),
+    (dict(C=(1 << 20) + 8), 2), (dict(T=(1 << 28) + 1), 2), (dict(B=(1 << 25) + 1), 2),
 ])
 def test_conv_refusals(bad, code):
     assert conv_forward(conv(**bad)) == code
@@ -125,6 +125,25 @@ def test_scan_pointers():
     few, many = ssm(T=1000), ssm(T=100000)
     size = L.gdn_ssm_workspace_bytes
     assert 0 < size(few, 0) < size(many, 0) < size(many, 1)
+
+
+def test_scan_refuses_outputs_that_are_inputs():
+    """A workgroup's results would be another's operands."""
+    L, sh = gdn.lib(), ssm()
+    at = [ctypes.c_void_p(4096 * (i + 1)) for i in range(20)]
+    names = ("x", "dt", "A", "B", "C", "cu", "h0", "dy", "dhT", "dx", "ddt", "dA", "dB", "dC", "dh0", "ws")
+    p = dict(zip(names, at))
+
+    def back(**kw):
+        q = dict(p, **kw)
+        return L.gdn_ssm_backward(sh, q["x"], q["dt"], q["A"], q["B"], q["C"], None, None, q["cu"], q["h0"], q["dy"], q["dhT"], q["dx"],
+                                  q["ddt"], q["dA"], q["dB"], q["dC"], None, None, q["dh0"], q["ws"], BIG, None)
+
+    for out, of in (("dx", "x"), ("dx", "dy"), ("dB", "B"), ("dB", "C"), ("dC", "B"), ("dC", "C"), ("dC", "dB"), ("dh0", "h0"),
+                    ("dh0", "dhT")):
+        assert back(**{out: p[of]}) == 1, (out, of)
+    assert ssm_forward(sh, x=at[0], y=at[0]) == 1
+    assert L.gdn_ssm_step(ssm(T=2), at[0], at[1], at[2], at[3], at[4], None, None, at[5], at[0], None) == 1
 
 
 @pytest.mark.parametrize("bad,code", [
