@@ -172,11 +172,9 @@ __global__ __launch_bounds__(256) void ssm_sums_kernel(const float* __restrict__
     __shared__ double red[4][3];
     const int l = lane_id(), head = blockIdx.x;
     long long chunks = 0;
+    int top = 0, st, en;
     for (int b0 = 0; b0 < nb; b0 += 64) {
-        const int b = b0 + l < nb ? b0 + l : nb - 1;
-        int st = cu[b], en = cu[b + 1];
-        st = st < 0 ? 0 : st > T ? T : st;
-        en = en < st ? st : en > T ? T : en;
+        ordered_bounds(cu, nb, T, b0, top, st, en);
         chunks += gdn::wave_sum(b0 + l < nb ? (en - st + L - 1) / L : 0);
     }
     double s[3] = {0, 0, 0};

@@ -20,6 +20,27 @@ template <> struct SsmTile<float> {
     static constexpr int PARTS = 1;
 };
 
+// Bounds of the lanes' sequences b0, b0 + 1 .., clamped to 0 <= start <= end <= T; a
+// bound below an earlier one counts as that one, so that no row is two sequences':
+// the workspace has the chunks of T rows.  top: the greatest bound so far, 0 at first.
+// The search for it runs only where there is such a bound.
+__device__ __forceinline__ void ordered_bounds(const int* __restrict__ cu, int B, int T, int b0, int& top, int& st, int& en)
+{
+    const int l = lane_id(), b = b0 + l < B ? b0 + l : B - 1;
+    st = cu[b], en = cu[b + 1];
+    st = st < 0 ? 0 : st > T ? T : st;
+    en = en < 0 ? 0 : en > T ? T : en;
+    if (__any(en < st || st < top)) {
+        st = st < top ? top : st;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int up = __shfl_up(st, o);
+            if (l >= o && up > st) st = up;
+        }
+        en = en < st ? st : en;
+    }
+    top = __builtin_amdgcn_readlane(en, 63);
+}
+
 // Units of `len` tokens (chunks, segments) of packed sequences, in the order of
 // the sequences.  A sequence has `count` of them, of which count - drop are dealt out,
 // `least` at least.  Unit `id` of those: the at-th of sequence b, whose rows are
@@ -35,11 +56,9 @@ __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int
 {
     const int l = lane_id();
     long long dealt = 0, first = 0, between = 0, chunks = 0;
+    int top = 0, st, en;
     for (int b0 = 0; b0 < B; b0 += 64) {
-        const int b = b0 + l < B ? b0 + l : B - 1;
-        int st = cu[b], en = cu[b + 1];
-        st = st < 0 ? 0 : st > T ? T : st;
-        en = en < st ? st : en > T ? T : en;
+        ordered_bounds(cu, B, T, b0, top, st, en);
         const bool real = b0 + l < B;
         const int n = en - st, ch = real ? (n + L - 1) / L : 0, count = real ? (n + len - 1) / len : 0;
         const int nu = real ? (count - drop < least ? least : count - drop) : 0, nbt = ch > 1 ? ch - 1 : 0;

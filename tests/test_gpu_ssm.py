@@ -230,6 +230,21 @@ def test_bounds_of_cu_are_clamped():
         assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bounds_of_cu_that_decrease(dtype):
+    """A bound below an earlier one counts as that one: no row is two sequences', and
+    the workspace's chunks suffice however often the bounds go up and down."""
+    from itertools import accumulate
+    T, B = 300, 140
+    for given in ([0, 150, 40, T], [T, 0] * 2 + [T], [0] + [T, 0] * 69 + [T], [(i * 7) % 50 for i in range(140)] + [T]):
+        nb = len(given) - 1
+        s = make(T, nb, 2, 1, 64, 64, DT[dtype])
+        inside = list(accumulate(given, max))
+        assert nb <= B and inside[-1] == given[-1]
+        for a, c in zip(forward(s, given) + backward(s, given), forward(s, inside) + backward(s, inside)):
+            assert torch.equal(a, c)
+
+
 def test_nonfinite_values_stay_in_their_sequence_and_head():
     s = make(400, 3, 2, 1, 64, 64, torch.bfloat16)
     cu = [0, 130, 290, 400]
