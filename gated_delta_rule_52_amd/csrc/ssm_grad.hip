@@ -70,8 +70,9 @@ template <typename T> __device__ __forceinline__ void acc_parts(const f32x16& s,
     }
 }
 
-// row m = l % 32 of the strictly lower triangle of ones, columns 16 b .. + 15, permuted order
-template <typename T> __device__ __forceinline__ Frag<T> ones_below(int b, int l)
+// row m = l % 32 of the strictly lower triangle of ones (minus: of -1), columns
+// 16 b .. + 15, permuted order
+template <typename T> __device__ __forceinline__ Frag<T> ones_below(int b, int l, bool minus)
 {
     const int m = l & 31, h = l >> 5;
     if constexpr (sizeof(T) == 2) {
@@ -79,13 +80,13 @@ template <typename T> __device__ __forceinline__ Frag<T> ones_below(int b, int l
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int s = 16 * b + 8 * (i >> 1) + 4 * h + 2 * (i & 1);
-            w[i] = (s < m ? 0x3f80u : 0u) | (s + 1 < m ? 0x3f800000u : 0u);
+            w[i] = ((s < m ? 0x3f80u : 0u) | (s + 1 < m ? 0x3f800000u : 0u)) ^ (minus ? 0x80008000u : 0u);
         }
         return __builtin_bit_cast(bf16x8, w);
     } else {
         f32x8 v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 16 * b + 8 * (j >> 2) + 4 * h + (j & 3) < m ? 1.f : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = 16 * b + 8 * (j >> 2) + 4 * h + (j & 3) < m ? (minus ? -1.f : 1.f) : 0.f;
         return v;
     }
 }
@@ -161,7 +162,7 @@ template <typename T, int N> struct Grad {
             const int x = i * NTH + tid, p = x & 63, q = x >> 6;
             if constexpr (sizeof(T) == 2) {
                 u32x4 parts[3];
-                split(v[i], parts);
+                split<true>(v[i], parts);  // dB takes the first part alone
 #pragma unroll
                 for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x4*>(m.st[j] + VTab::word(p, q) * 16) = parts[j];
             } else {
@@ -315,23 +316,27 @@ template <typename T, int N> struct Grad {
                                 gm[4 * i + j] *= s + j < at && at < live ? z[4 * i + j] : 0.f;
                             }
                         }
-                        // over[t][t'] = sum_{s < t} M_t's, then for every t the sum over t' >= t
+                        // over[t][t'] = sum_{s < t} M_t's, then for every t the sum over t' >= t.
+                        // The bf16 products round their sums down a little on average, which
+                        // sums over all tokens (dA, ddt_bias) would show: every other block of
+                        // tokens sums -M, and the smallest parts come first.
+                        const bool minus = w & 1;
                         f32x16 over = zero16();
+                        Frag<T> parts[2][PARTS];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            Frag<T> parts[PARTS];
-                            acc_parts<T>(gm, b, parts);
-                            const Frag<T> ones = ones_below<T>(b, l);
+                        for (int b = 0; b < 2; ++b) acc_parts<T>(gm, b, parts[b]);
 #pragma unroll
-                            for (int p = 0; p < PARTS; ++p) over = mma32(ones, parts[p], over);
-                        }
+                        for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) over = mma32(ones_below<T>(b, l, minus), parts[b][p], over);
                         float mine = 0.f;
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             const float v = lane16_sum((l & 31) >= acc_rows(q >> 2, l) + (q & 3) ? over[q] : 0.f);
                             mine = (l & 15) == q ? v : mine;
                         }
-                        over_own += mine + __shfl_xor(mine, 16);
+                        mine += __shfl_xor(mine, 16);
+                        over_own += minus ? -mine : mine;
                     }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -122,19 +122,25 @@ enum { TOK_R_STATE, TOK_R_BLOCKS, TOK_Q_STATE, TOK_Q_BLOCKS, TOK_OWN, TOK_XDU, T
 template <int L> constexpr int kTokens = TOK_ROWS * L + 8;  // floats a chunk and head
 
 // v as three bf16 each: the upper 8 bits of its 24, the next, the rest.  Cut off and
-// not rounded, which leaves all bits and takes fewer instructions.
+// not rounded, which leaves all bits and takes fewer instructions; the first one
+// rounded (NEAREST) where it also stands for v by itself.
 __device__ __forceinline__ uint32_t upper_halves(float a, float b)  // of a in the low half
 {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 __device__ __forceinline__ float upper(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
-__device__ __forceinline__ void split(const float (&v)[8], u32x4 (&w)[3])
+template <bool NEAREST = false> __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&w)[3])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a = v[2 * i], b = v[2 * i + 1];
-        w[0][i] = upper_halves(a, b);
-        a -= upper(a), b -= upper(b);
+        if constexpr (NEAREST) {
+            w[0][i] = cvt2_bf16(a, b);
+            a -= __uint_as_float(w[0][i] << 16), b -= upper(__uint_as_float(w[0][i]));
+        } else {
+            w[0][i] = upper_halves(a, b);
+            a -= upper(a), b -= upper(b);
+        }
         w[1][i] = upper_halves(a, b);
         a -= upper(a), b -= upper(b);
         w[2][i] = upper_halves(a, b);
