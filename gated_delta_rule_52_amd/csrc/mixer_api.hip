@@ -69,6 +69,8 @@ gdn_status check_ssm(const gdn_ssm_shape* sh, SsmCall call, gdn_ssm_shape& s)
         if (*st[i] > (1LL << 24)) return GDN_ERR_UNSUPPORTED;
     }
     if (call != CALL_STEP) {
+        // every workgroup looks for its chunk along the bounds, 64 sequences at a time
+        if (s.B > 65536) return GDN_ERR_UNSUPPORTED;
         // below 2^32 work-items: 512 a chunk (or segment) and slice or part, in whole
         // eights of chunks and 32s of workgroups a die
         const SsmPlan p = ssm_plan(s, call == CALL_BACKWARD);

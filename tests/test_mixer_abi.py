@@ -240,3 +240,11 @@ def test_plain_pages():
     assert kv == [21, 18, 40] and count == 2 and cu == [0, 1, 3, 43]
     assert table == [[0, 1, -1], [2, 4, -1], [3, 8, 7]]
     assert pos[:4] == [20, 16, 17, 0] and slots[:4] == [20, 64, 65, 48] and slots[-1] == 7 * 16 + 7
+
+
+def test_scan_sequences_at_the_limit():
+    """Every workgroup of the packed calls looks for its chunk along the bounds."""
+    size = gdn.lib().gdn_ssm_workspace_bytes
+    assert size(ssm(B=65537, H=1, G=1), 0) == size(ssm(B=65537, H=1, G=1), 1) == 0
+    assert size(ssm(B=65536, H=1, G=1), 0) > 0 and size(ssm(B=65536, H=1, G=1), 1) > 0
+    assert ssm_forward(ssm(B=65537, H=1, G=1)) == ssm_backward(ssm(B=65537, H=1, G=1)) == 2
