@@ -45,6 +45,7 @@ struct SsmPlan {
     long long between;  // states between chunks, at most
     int seg;            // chunks of a segment; 0: a sequence is one segment
     long long segs;     // at most, over all sequences
+    long long several;  // at most, of sequences that have several
     int splits;         // parts into which the heads of a group are dealt in the gradients
     size_t dec_at, seg_at, tot_at, fwd_at, back_at, token_at, sum_at, part_at, bytes;  // offsets in the workspace
 };

@@ -123,8 +123,19 @@ SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward)
         seg = (each + want - 1) / want;
         if (seg < 2) seg = 2;
     }
+    // Where there are workgroups enough, or the mean sequence is short, one may still be
+    // long (a prompt among single tokens): none walks more than 4 times the mean length,
+    // or 32 chunks, in a row.  16 heads of 64, N = 128: 65536 tokens among 255 single ones
+    // 512 us (in a row 2100); 256 sequences of 256, for which nothing is cut, 316 (299).
+    if (!seg) {
+        const long long most = 4 * each < 32 ? 32 : 4 * each;
+        if (p.between > 2 * most) seg = most;
+    }
     p.seg = (int)seg;
     p.segs = seg ? s.T / (seg * p.L) + s.B : s.B;
+    // n tokens that are more than one segment's are less than 2 n / (seg L) of them
+    p.several = seg ? 2LL * s.T / (seg * p.L) : 0;
+    if (p.several > p.segs) p.several = p.segs;
     // Parts of a group's heads in the gradients: until there is a workgroup for every
     // compute unit (it takes nearly all of its LDS).
     p.splits = 1;
@@ -139,8 +150,8 @@ SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward)
     const long long state = (long long)p.slices * s.N * kSlice;
     const int ways = backward ? 2 : 1;
     p.dec_at = take(p.chunks * s.H * (p.L == 128 ? kDecays<128> : kDecays<64>) * 4);
-    p.seg_at = take(p.seg ? ways * p.segs * state * 4 : 0);
-    p.tot_at = take(p.seg ? ways * p.segs * p.slices * 4 : 0);
+    p.seg_at = take(ways * p.several * state * 4);
+    p.tot_at = take(ways * p.several * p.slices * 4);
     p.fwd_at = take(backward ? p.between * state * 4 : (p.between + s.B) * state * e);
     if (backward) {
         p.back_at = take(p.between * state * 4);

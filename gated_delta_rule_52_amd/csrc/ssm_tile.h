@@ -43,9 +43,10 @@ __device__ __forceinline__ void ordered_bounds(const int* __restrict__ cu, int B
 
 // Units of `len` tokens (chunks, segments) of packed sequences, in the order of
 // the sequences.  A sequence has `count` of them, of which count - drop are dealt out,
-// `least` at least.  Unit `id` of those: the at-th of sequence b, whose rows are
-// start .. start + n - 1; chunks: of the sequence; first: the units, before, between:
-// the chunks and the states between chunks, of all sequences before it.
+// `least` at least (drop < 0: one, if there are several).  Unit `id` of those: the at-th
+// of sequence b, whose rows are start .. start + n - 1; chunks: of the sequence; first:
+// the units of those with several, before, between: the chunks and the states between
+// chunks, of all sequences before it.
 struct Unit {
     int b, at, count, start, n, chunks;
     long long first, before, between;
@@ -61,8 +62,9 @@ __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int
         ordered_bounds(cu, B, T, b0, top, st, en);
         const bool real = b0 + l < B;
         const int n = en - st, ch = real ? (n + L - 1) / L : 0, count = real ? (n + len - 1) / len : 0;
-        const int nu = real ? (count - drop < least ? least : count - drop) : 0, nbt = ch > 1 ? ch - 1 : 0;
-        const int inc = wave_scan(nu), incf = wave_scan(count), incb = wave_scan(nbt), incc = wave_scan(ch);
+        const int several = count > 1 ? count : 0, nbt = ch > 1 ? ch - 1 : 0;
+        const int nu = !real ? 0 : drop < 0 ? several > 0 : count - drop < least ? least : count - drop;
+        const int inc = wave_scan(nu), incf = wave_scan(several), incb = wave_scan(nbt), incc = wave_scan(ch);
         const uint64_t hit = __ballot(dealt + inc > id);
         if (hit) {
             const int k = __builtin_ctzll(hit);
@@ -73,7 +75,7 @@ __device__ __forceinline__ bool find_unit(const int* __restrict__ cu, int B, int
             u.start = here(st);
             u.n = here(n);
             u.chunks = here(ch);
-            u.first = first + here(incf) - u.count;
+            u.first = first + here(incf) - here(several);
             u.before = chunks + here(incc) - u.chunks;
             u.between = between + here(incb) - here(nbt);
             return true;

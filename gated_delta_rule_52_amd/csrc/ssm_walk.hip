@@ -264,7 +264,8 @@ __global__ __launch_bounds__(256, 2) void ssm_walk_kernel(WalkCall a)
 }
 
 // The states at the segments' ends, in place, from what each contributes: four values
-// a thread along a sequence's segments (blockIdx.y), those to come on their way.
+// a thread along a sequence's segments (blockIdx.y: of the sequences that have several),
+// those to come on their way.
 // blockIdx.x: slice and 1024 values of it; blockIdx.z: way.
 template <int L, int N> __global__ __launch_bounds__(256) void ssm_segments_kernel(WalkCall a)
 {
@@ -272,7 +273,7 @@ template <int L, int N> __global__ __launch_bounds__(256) void ssm_segments_kern
     const WalkArgs& g = a.way[blockIdx.z];
     const bool back = blockIdx.z != 0;
     Unit u;
-    if (!find_unit<L>(a.cu, a.nb, a.T, a.seg_len * L, 0x7fffffff, 1, blockIdx.y, u)) return;
+    if (!find_unit<L>(a.cu, a.nb, a.T, a.seg_len * L, -1, 0, blockIdx.y, u)) return;
     const int slice = blockIdx.x / BLOCKS, many = u.count - 1;  // those of the first launch
     const size_t at0 = (size_t)(u.first + (back ? u.count - 1 : 0)) * a.slices + slice;
     const long long step = (back ? -1LL : 1LL) * a.slices;
@@ -305,12 +306,15 @@ template <int L, int N> __global__ __launch_bounds__(256) void ssm_segments_kern
 
 template <typename T, int N, bool OUT> gdn_status walk(const SsmPlan& p, const WalkCall& a, hipStream_t st)
 {
-    // a sequence has one segment fewer in the first launch, and in the second one at least
-    const dim3 grid(dealt(p.segs, a.H / a.per_group * a.pairs), OUT ? 1 : 2);
+    // a sequence has one segment fewer in the first launch, and in the last one at least;
+    // those that have several are at most as many as whole segments fit into the tokens
+    const int jobs = a.H / a.per_group * a.pairs;
+    const dim3 grid(dealt(p.segs, jobs), OUT ? 1 : 2);
     if (p.seg) {
-        GDN_LAUNCH("ssm_walk_segments", (ssm_walk_kernel<T, N, 0, OUT>), grid, dim3(256), st, a);
-        GDN_LAUNCH("ssm_segments", (ssm_segments_kernel<SsmTile<T>::L, N>), dim3(a.slices * (N / 16), a.nb, OUT ? 1 : 2),
-                   dim3(256), st, a);
+        const long long whole = p.segs - a.nb;
+        GDN_LAUNCH("ssm_walk_segments", (ssm_walk_kernel<T, N, 0, OUT>), dim3(dealt(whole, jobs), OUT ? 1 : 2), dim3(256), st, a);
+        GDN_LAUNCH("ssm_segments", (ssm_segments_kernel<SsmTile<T>::L, N>),
+                   dim3(a.slices * (N / 16), (unsigned)(whole < a.nb ? whole : a.nb), OUT ? 1 : 2), dim3(256), st, a);
     }
     GDN_LAUNCH("ssm_walk", (ssm_walk_kernel<T, N, 1, OUT>), grid, dim3(256), st, a);
     return GDN_OK;
@@ -336,8 +340,8 @@ gdn_status ssm_walk(const gdn_ssm_shape& s, const SsmPlan& p, const SsmArgs& x, 
         g.vs = back ? (long long)s.H * s.P : x.xs;
         g.init = back ? x.dhT : x.h0;
         g.last = back ? x.dh0 : backward ? nullptr : x.hT;
-        g.seg = (float*)(ws + p.seg_at) + back * p.segs * state;
-        g.tot = (float*)(ws + p.tot_at) + back * p.segs * p.slices;
+        g.seg = (float*)(ws + p.seg_at) + back * p.several * state;
+        g.tot = (float*)(ws + p.tot_at) + back * p.several * p.slices;
         g.between = ws + (back ? p.back_at : p.fwd_at);
     }
     a.dec = (const float*)(ws + p.dec_at);

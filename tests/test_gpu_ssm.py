@@ -230,6 +230,25 @@ def test_bounds_of_cu_are_clamped():
         assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_long_sequence_among_short_ones(dtype):
+    """Cut into segments although the mean sequence is short."""
+    lens = [1, 0, 2] * 20 + [8700 if dtype == "bf16" else 4400] + [1] * 30 + [130, 0, 3]
+    cu, B = cumulate(lens), len(lens)
+    s = make(cu[-1], B, 2, 1, 64, 64, DT[dtype], decay=0.1)
+    got = dict(zip(GRADS, backward(s, cu)))
+    got["y"], got["hT"] = forward(s, cu)
+    torch.cuda.synchronize()
+    want = ref.ssm(s["x"], s["dt"], s["A"], s["B"], s["C"], cu, s["D"], s["dt_bias"], True, s["h0"], s["dy"], s["dhT"])
+    errs = {k: worst(v, *want[k]) for k, v in got.items()}
+    log(f"one long {dtype}: " + " ".join(f"{k}={v:.3f}" for k, v in errs.items()))
+    assert max(errs.values()) <= 1, errs
+    st = s["h0"].clone()
+    y2, _ = forward(dict(s, h0=st), cu, hT=st)
+    torch.cuda.synchronize()
+    assert torch.equal(got["y"], y2) and torch.equal(got["hT"], st)
+
+
 def test_step_gradients_are_not_biased():
     """The steps' gradients of bf16 inputs against those of the same values in float32.
     Their differences are roundings of either, as often up as down and of each token's
