@@ -571,15 +571,29 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), sizeof(T) == 2 ? 2 : 1) 
         Grad<T, N>::of_t(a, k, m);
 }
 
-// dB and dC from the parts of a group's heads, in order: a word of 4 values a thread
+// dB and dC from the parts of a group's heads, in order: a word of 4 values a thread.
+// The sequences' rows end at the greatest bound, which is the last one only where no
+// bound decreases (ordered_bounds).
 template <typename T>
 __global__ __launch_bounds__(256) void ssm_join_kernel(const float* __restrict__ part, const int* __restrict__ cu, T* dB,
                                                        T* dC, int nb, int tokens, int splits, int width)
 {
+    __shared__ int red[4];
+    int end = 0;
+    for (int b = threadIdx.x; b <= nb; b += 256) end = cu[b] > end ? cu[b] : end;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        const int other = __shfl_xor(end, o);
+        end = other > end ? other : end;
+    }
+    if (lane_id() == 0) red[wave_id()] = end;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) end = red[w] > end ? red[w] : end;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x, total = (long long)tokens * width / 4;
     if (i >= total) return;
     const int row = (int)(i * 4 / width);
-    if (row < cu[0] || row >= cu[nb]) return;  // a row of no sequence
+    if (row < cu[0] || row >= end) return;  // a row of no sequence
     const f32x4* p = reinterpret_cast<const f32x4*>(part) + (size_t)blockIdx.y * splits * total + i;
     f32x4 s = p[0];
     for (int k = 1; k < splits; ++k) s += p[(size_t)k * total];

@@ -465,8 +465,7 @@ gdn_status gdn_conv_step(const gdn_conv_shape *shape, const void *x, const float
  * D, dt_bias and h0 (zero state) may be NULL; A is meant to be negative, but is
  * not tested.  N and P in {64, 128}; H a multiple of G, at most 1024; T * H < 2^27,
  * B * H < 2^23, B at most 65536 but for single tokens; strides at most 2^24.  Of bounds
- * that decrease, one below an earlier one counts as that one in y, hT and the states'
- * gradients.
+ * that decrease, one below an earlier one counts as that one.
  * A value that is not finite reaches no other sequence and no other head's output;
  * within a sequence and head it may reach the other results of its chunk of 128
  * tokens (float32: 64), the earlier ones among them.
