@@ -129,6 +129,9 @@ gdn_status gdn_conv_backward(const gdn_conv_shape* sh, const void* x, const floa
     if (any_off16(x, weight, bias, state, dy, dstate_out, dx, dweight, dbias, dstate, ws) || off4(cu_seqlens))
         return GDN_ERR_ALIGNMENT;
     if (!ws || ws_bytes < conv_ws(s)) return GDN_ERR_WORKSPACE;
+    // the launch of dstate reads these behind the outputs that they would be, or behind
+    // its own earlier rows
+    if (dweight == weight || (dbias && dbias == bias) || (dstate && dstate == dstate_out)) return GDN_ERR_INVALID_ARG;
     ConvArgs a{};
     a.x = x; a.w = weight; a.bias = bias; a.cu = cu_seqlens; a.state = state;
     a.dy = dy; a.dstate_out = dstate_out; a.dx = dx; a.dstate = dstate; a.part = (float*)ws;

@@ -1,0 +1,25 @@
+"""Host side: outputs that are inputs which a later launch, or another workgroup, still
+reads are refused before any launch (no pointer below is ever followed)."""
+import ctypes
+
+import pytest
+
+import gated_delta_rule_52_amd as gdn
+from test_block_abi import BIG
+from test_mixer_abi import conv
+
+CONV = ("x", "weight", "bias", "cu", "state", "dy", "dstate_out", "dx", "dweight", "dbias", "dstate", "ws")
+
+
+def at(names):
+    return {n: ctypes.c_void_p(4096 * (i + 1)) for i, n in enumerate(names)}
+
+
+@pytest.mark.parametrize("out,of", [("dx", "x"), ("dx", "dy"), ("dstate", "dstate_out"), ("dweight", "weight"), ("dbias", "bias")])
+def test_conv_backward_refuses_outputs_that_are_inputs(out, of):
+    """dstate's rows are sums with rows of dstate_out that an earlier one would have
+    replaced, and its launch reads weight and bias behind the one that writes their
+    gradients."""
+    p = at(CONV)
+    p[out] = p[of]
+    assert gdn.lib().gdn_conv_backward(conv(), *p.values(), BIG, None) == 1
