@@ -17,6 +17,7 @@ bool off16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 bool off4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
 
 template <typename... P> bool any_null(P... p) { return (... || (p == nullptr)); }
+template <typename... P> bool any_of(const void* x, P... p) { return (... || (x == (const void*)p)); }
 template <typename... P> bool any_off16(P... p) { return (... || off16((const void*)p)); }
 template <typename... P> bool any_off4(P... p) { return (... || off4((const void*)p)); }
 
@@ -173,7 +174,7 @@ gdn_status gdn_ssm_forward(const gdn_ssm_shape* sh, const void* x, const float* 
     if (any_off16(x, B, C, h0, y, hT, ws) || any_off4(dt, A, D, dt_bias) || off4(cu_seqlens)) return GDN_ERR_ALIGNMENT;
     const SsmPlan p = ssm_plan(s, false);
     if (!ws || ws_bytes < p.bytes) return GDN_ERR_WORKSPACE;
-    if (s.T && y == x) return GDN_ERR_INVALID_ARG;
+    if (s.T && any_of(y, x, B, C)) return GDN_ERR_INVALID_ARG;  // another workgroup's operands
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.y = y; a.hT = hT;
@@ -204,7 +205,8 @@ gdn_status gdn_ssm_backward(const gdn_ssm_shape* sh, const void* x, const float*
     // the gradients read h0 and dhT after the walk has written dh0, and one workgroup's
     // operands after another has written its results
     if (dh0 && (dhT == dh0 || h0 == dh0)) return GDN_ERR_INVALID_ARG;
-    if (s.T && (dx == x || dx == dy || dB == B || dB == C || dC == B || dC == C || dB == dC)) return GDN_ERR_INVALID_ARG;
+    if (s.T && (any_of(dx, x, B, C, dy) || any_of(dB, x, B, C, dy, dx) || any_of(dC, x, B, C, dy, dx, dB)))
+        return GDN_ERR_INVALID_ARG;
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dy = dy; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.cu = cu_seqlens;
     a.h0 = h0; a.dhT = dhT; a.dx = dx; a.dB = dB; a.dC = dC; a.ddt = ddt; a.dA = dA; a.dD = dD; a.dbias = ddt_bias; a.dh0 = dh0;
@@ -226,7 +228,7 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape* sh, const void* x, const float* dt,
     if (r != GDN_OK) return r;
     if (any_null(x, B, C, (const void*)y) || !dt || !A || !state) return GDN_ERR_INVALID_ARG;
     if (any_off16(x, B, C, state, y) || any_off4(dt, A, D, dt_bias)) return GDN_ERR_ALIGNMENT;
-    if (y == x) return GDN_ERR_INVALID_ARG;
+    if (any_of(y, x, B, C)) return GDN_ERR_INVALID_ARG;
     SsmArgs a{};
     a.x = x; a.B = B; a.C = C; a.dt = dt; a.A = A; a.D = D; a.bias = dt_bias; a.y = y;
     a.xs = s.x_stride; a.bs = s.b_stride; a.cs = s.c_stride;
