@@ -18,6 +18,7 @@
 // backward 46 us, 4.4 TB/s (traced; among others 34, with 16 words 41, and 50, without the
 // rows to come on their way 58).
 #include "conv.h"
+#include "bounds.h"
 #include "common.h"
 
 namespace gdn {
@@ -142,46 +143,129 @@ template <int VE> __device__ __forceinline__ void clear(float (&v)[VE])
     for (int e = 0; e < VE; ++e) v[e] = 0.f;
 }
 
-// bounds of sequence b, clamped to 0 <= start <= end <= T
-__device__ __forceinline__ void bounds(const ConvArgs& a, int b, int& st, int& en)
+__device__ __forceinline__ int clamped(const ConvArgs& a, int i)
+{
+    const int v = a.cu[i];
+    return v < 0 ? 0 : v > a.T ? a.T : v;
+}
+
+__device__ __forceinline__ int wave_most(int x)
+{
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        const int other = __shfl_xor(x, o);
+        x = other > x ? other : x;
+    }
+    return __builtin_amdgcn_readfirstlane(x);
+}
+
+// The greatest of x and of 256 WORDS bounds from i on, a lane's share of them
+template <int WORDS> __device__ __forceinline__ int most_of(const int* __restrict__ cu, int i, int x)
+{
+    typedef int i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+    i32x4 v[WORDS];
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) v[k] = *reinterpret_cast<const i32x4*>(cu + i + 256 * k + 4 * lane_id());
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x = v[k][j] > x ? v[k][j] : x;
+    return x;
+}
+
+// Rows st .. en - 1 of sequence b, as ordered_bounds has them: it begins at the greatest
+// of the bounds up to its own.  Called by whole workgroups, whose sequences follow one
+// another from `base` on; they read whole 8192s of the bounds before it together.
+__device__ __forceinline__ void rows_of(const ConvArgs& a, int base, int b, int& st, int& en)
 {
     if (!a.cu) {  // single tokens: row b is all of sequence b
         st = b, en = b + 1;
         return;
     }
-    st = a.cu[b], en = a.cu[b + 1];
-    st = st < 0 ? 0 : st > a.T ? a.T : st;
-    en = en < st ? st : en > a.T ? a.T : en;
+    __shared__ int red[4];
+    const int first = __builtin_amdgcn_readfirstlane(b);
+    int i0 = 0;
+    st = en = 0;
+    if (base >= 8192) {
+        const int w = __builtin_amdgcn_readfirstlane(wave_id());
+        for (; i0 + 8192 <= base + 1; i0 += 8192) st = most_of<8>(a.cu, i0 + 2048 * w, st);
+        red[w] = wave_most(st);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st = red[k] > st ? red[k] : st;
+    }
+    if (first >= a.B) return;
+    for (; i0 + 2048 <= first + 1; i0 += 2048) st = most_of<8>(a.cu, i0, st);
+    for (; i0 + 256 <= first + 1; i0 += 256) st = most_of<1>(a.cu, i0, st);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = i0 + 64 * k + lane_id(), v = a.cu[i <= first ? i : first];
+        st = v > st ? v : st;
+    }
+    st = wave_most(st);
+    st = st > a.T ? a.T : st;
+    if (b >= a.B) return;
+    for (int i = first + 1; i <= b; ++i) {
+        const int v = clamped(a, i);
+        st = v > st ? v : st;
+    }
+    en = clamped(a, b + 1);
+    en = en < st ? st : en;
 }
 
 // the sequence of a row, moved forward as the rows go on; end past every row where there is none
 struct Seq {
     int b, st, en;
-    __device__ __forceinline__ void find(const ConvArgs& a, int t)
+    // Called by whole waves, with one row t a CW lanes, ascending: 64 sequences at a time
+    // along the ordered bounds, behind whole 2048s and 256s of them that end at or before
+    // the first row.  (A bisection would find some rise past t, not the first.)
+    template <int CW> __device__ __forceinline__ void find(const ConvArgs& a, int t)
     {
-        int lo = 0, hi = a.B;  // the number of ends at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu[mid + 1] <= t)
-                lo = mid + 1;
-            else
-                hi = mid;
+        constexpr int GROUPS = 64 / CW;
+        const int l = lane_id(), t0 = __builtin_amdgcn_readfirstlane(t);
+        b = a.B, st = en = 0x7fffffff;
+        if (t0 >= a.T) return;
+        int b0 = 0, top = 0, most = a.cu[0];
+        auto skip = [&](auto words) {
+            constexpr int WORDS = decltype(words)::value;
+            for (; b0 + 256 * WORDS <= a.B; b0 += 256 * WORDS) {
+                const int m = most_of<WORDS>(a.cu, b0 + 1, most);
+                if (__any(m > t0)) break;
+                most = m;
+            }
+        };
+        if (most <= t0) {
+            skip(std::integral_constant<int, 8>{});
+            skip(std::integral_constant<int, 1>{});
+            if (b0) top = wave_most(most < 0 ? 0 : most);
         }
-        b = lo;
-        read(a);
-    }
-    __device__ __forceinline__ void read(const ConvArgs& a)
-    {
-        if (b < a.B)
-            bounds(a, b, st, en);
-        else
-            st = en = 0x7fffffff;
+        unsigned open = 0;  // groups of lanes whose row is yet to be found
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) open |= __builtin_amdgcn_readlane(t, g * CW) < a.T ? 1u << g : 0u;
+        for (; b0 < a.B && open; b0 += 64) {
+            int s, e;
+            ordered_bounds(a.cu, a.B, a.T, b0, top, s, e);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const uint64_t hit = __ballot(e > __builtin_amdgcn_readlane(t, g * CW));
+                if (hit && (open >> g & 1)) {
+                    const int k = __builtin_ctzll(hit), sk = __builtin_amdgcn_readlane(s, k), ek = __builtin_amdgcn_readlane(e, k);
+                    if (GROUPS == 1 || l / CW == g) b = b0 + k, st = sk, en = ek;
+                    open &= ~(1u << g);
+                }
+            }
+        }
     }
     __device__ __forceinline__ void move(const ConvArgs& a, int t)
     {
         while (t >= en && b < a.B) {
-            ++b;
-            read(a);
+            if (++b < a.B) {
+                st = en;
+                const int e = clamped(a, b + 1);
+                en = e < st ? st : e;
+            } else {
+                st = en = 0x7fffffff;
+            }
         }
     }
 };
@@ -189,14 +273,11 @@ struct Seq {
 // A sequence's first W - 1 rows (those whose window holds its state) and its new
 // state, by the threads that have read the old one: state and state_out may be one.
 template <typename T, int W>
-__device__ __forceinline__ void head_rows(const ConvArgs& a, int b, int c)
+__device__ __forceinline__ void head_rows(const ConvArgs& a, int b, int st, int n, int c)
 {
     constexpr int VE = Word<T>::VE, K = W - 1;
     Taps<T, W> taps;
     taps.load(a, c);
-    int st, en;
-    bounds(a, b, st, en);
-    const int n = en - st;
     const T* x = (const T*)a.x + (size_t)st * a.x_stride + c;
     u32x4 old[K], rows[K], tail[K];
 #pragma unroll
@@ -239,18 +320,18 @@ __global__ __launch_bounds__(256) void conv_forward_kernel(ConvArgs a)
     constexpr int VE = Word<T>::VE, K = W - 1, AHEAD = 8;
     constexpr int NS = 256 / CW;
     const int c = (blockIdx.y * CW + lane_word<CW>()) * VE, sub = lane_strip<CW>();
-    if (c >= a.C) return;
     if ((int)blockIdx.x < a.head_blocks) {
         const int b = blockIdx.x * NS + sub;
-        if (b < a.B) head_rows<T, W>(a, b, c);
+        int st, en;
+        rows_of(a, blockIdx.x * NS, b, st, en);
+        if (b < a.B && c < a.C) head_rows<T, W>(a, b, st, en - st, c);
         return;
     }
     const long long first = ((long long)(blockIdx.x - a.head_blocks) * NS + sub) * a.strip;
-    if (first >= a.T) return;
-    const int t0 = (int)first, t1 = a.T - t0 < a.strip ? a.T : t0 + a.strip;
+    const int t0 = first < a.T ? (int)first : a.T, t1 = a.T - t0 < a.strip ? a.T : t0 + a.strip;
     Seq s;
-    s.find(a, t0);
-    if (s.b >= a.B) return;  // behind the last sequence
+    s.find<CW>(a, t0);
+    if (s.b >= a.B || c >= a.C) return;  // behind the last sequence
     Taps<T, W> taps;
     taps.load(a, c);
     const T* x = (const T*)a.x + c;
@@ -303,15 +384,16 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a)
     __shared__ float tot[NS][CW * VE + 1];
     const int cw = lane_word<CW>(), c = (blockIdx.y * CW + cw) * VE, sub = lane_strip<CW>();
     const long long first = ((long long)blockIdx.x * NS + sub) * a.strip;
+    const int t0 = first < a.T ? (int)first : a.T;
+    Seq s;
+    s.find<CW>(a, t0);
     float dw[W][VE], db[VE];
     clear(db);
 #pragma unroll
     for (int j = 0; j < W; ++j) clear(dw[j]);
-    if (c < a.C && first < a.T) {
-        const int t0 = (int)first, t1 = a.T - t0 < a.strip ? a.T : t0 + a.strip;
+    if (c < a.C && t0 < a.T) {
+        const int t1 = a.T - t0 < a.strip ? a.T : t0 + a.strip;
         const int last = a.T - t1 < K ? a.T : t1 + K;  // rows whose dz this strip needs
-        Seq s;
-        s.find(a, t0);
         Taps<T, W> taps;
         taps.load(a, c);
         const T *x = (const T*)a.x + c, *dy = (const T*)a.dy + c;
@@ -462,11 +544,11 @@ __global__ __launch_bounds__(256) void conv_dstate_kernel(ConvArgs a)
 {
     constexpr int VE = Word<T>::VE, K = W - 1;
     const int c = (blockIdx.y * 16 + (threadIdx.x & 15)) * VE, b = blockIdx.x * 16 + (threadIdx.x >> 4);
+    int st, en;
+    rows_of(a, blockIdx.x * 16, b, st, en);
     if (c >= a.C || b >= a.B) return;
     Taps<T, W> taps;
     taps.load(a, c);
-    int st, en;
-    bounds(a, b, st, en);
     const int n = en - st;
     float win[K][VE], dzs[K][VE], z[VE], v[VE];
 #pragma unroll

@@ -34,6 +34,7 @@ gdn_status check_conv(const gdn_conv_shape* sh, bool step, gdn_conv_shape& s)
     // launches below 2^32 work-items, 4 sequences or 4 strips of 8 tokens or more (32
     // where there are many) a workgroup of 256, and rows of all channels in y
     if (s.C % ve || s.C > (1 << 20) || s.T > (1 << 28) || s.B > (1 << 25)) return GDN_ERR_UNSUPPORTED;
+    if (!step && s.B > 65536) return GDN_ERR_UNSUPPORTED;  // every strip looks for its sequence along the bounds
     if (!s.x_stride) s.x_stride = s.C;
     if (s.x_stride < s.C) return GDN_ERR_INVALID_ARG;
     if (s.x_stride % ve) return GDN_ERR_ALIGNMENT;

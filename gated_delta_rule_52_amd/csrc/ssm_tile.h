@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn.h"
+#include "bounds.h"
 #include "ssm.h"
 
 namespace gdn {
@@ -19,27 +20,6 @@ template <> struct SsmTile<float> {
     static constexpr int L = 64;
     static constexpr int PARTS = 1;
 };
-
-// Bounds of the lanes' sequences b0, b0 + 1 .., clamped to 0 <= start <= end <= T; a
-// bound below an earlier one counts as that one, so that no row is two sequences':
-// the workspace has the chunks of T rows.  top: the greatest bound so far, 0 at first.
-// The search for it runs only where there is such a bound.
-__device__ __forceinline__ void ordered_bounds(const int* __restrict__ cu, int B, int T, int b0, int& top, int& st, int& en)
-{
-    const int l = lane_id(), b = b0 + l < B ? b0 + l : B - 1;
-    st = cu[b], en = cu[b + 1];
-    st = st < 0 ? 0 : st > T ? T : st;
-    en = en < 0 ? 0 : en > T ? T : en;
-    if (__any(en < st || st < top)) {
-        st = st < top ? top : st;
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(st, o);
-            if (l >= o && up > st) st = up;
-        }
-        en = en < st ? st : en;
-    }
-    top = __builtin_amdgcn_readlane(en, 63);
-}
 
 // Units of `len` tokens (chunks, segments) of packed sequences, in the order of
 // the sequences.  A sequence has `count` of them, of which count - drop are dealt out,

@@ -425,7 +425,8 @@ gdn_status gdn_attn_paged(const gdn_attn_shape *shape, const void *q, const void
  *   [T, C] dense; weight, dweight [C, W], bias, dbias [C] float32 (bias may be
  *   NULL); states [B, W - 1, C] (dtype), oldest row first.
  * W is 2, 3 or 4; C a multiple of 8 (bf16) or 4 (float32), at most 2^20; T at most
- * 2^28, B at most 2^25.  y may not be x, nor dx x or dy, dstate dstate_out, dweight
+ * 2^28, B at most 65536, or 2^25 for single tokens.  Of bounds that decrease, one
+ * below an earlier one counts as that one.  y may not be x, nor dx x or dy, dstate dstate_out, dweight
  * weight or dbias bias.
  *
  * gdn_conv_forward: state_out (NULL: not written) may be state.  A sequence
