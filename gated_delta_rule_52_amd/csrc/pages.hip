@@ -93,7 +93,7 @@ __global__ __launch_bounds__(1024) void pages_release_kernel(PagesArgs a)
             const int len = a.kv_len[b], done = a.flag[b];
             if (done && len > 0) back = pages_of(len, a.shift);
             if (back > a.width) back = a.width;
-            if (a.counts && blockIdx.x == 0) a.kv_out[b] = done ? 0 : len;
+            if (a.counts && blockIdx.x == 0) a.kv_out[b] = done || len < 0 ? 0 : len;
         }
         i64 all;
         const i64 inc = carry + scan_1024(back, red, all);
