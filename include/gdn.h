@@ -513,6 +513,12 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape *shape, const void *x, const float *
  * whose top is its end.  kv_len [B] counts the positions that each sequence has;
  * its pages are the first ceil(kv_len / page_size) entries of its row of page_table
  * [B, max_pages].  All arrays int32 device memory, but for slots (int64).
+ * Entries of the table and of the stack are the caller's names of pages and are
+ * trusted: num_pages is the room of the stack, not a limit on the names, which
+ * gdn_attn_append and gdn_attn_paged test against their cache.  Only a name below 0
+ * is known as no page (slot -1).  So a length that claims pages which its row does
+ * not have (-1) puts -1 on the stack when they are released, and the tokens of a
+ * sequence that takes it get slots of -1.
  *
  * gdn_pages_release: the pages of every sequence with done[b] != 0 go on the stack,
  * in the order of the sequences and of their tables, and its length becomes 0 (the
