@@ -115,9 +115,10 @@ def ssm_serial(x, dt, A, Bm, Cm, cu, D=None, bias=None, softplus=True, h0=None):
     return torch.cat(ys), torch.stack(hs)
 
 
-def ssm(x, dt, A, Bm, Cm, cu, D=None, bias=None, softplus=True, h0=None, dy=None, dhT=None):
+def ssm(x, dt, A, Bm, Cm, cu, D=None, bias=None, softplus=True, h0=None, dy=None, dhT=None, keep=None):
     """{name: (value, bound)}: y and hT, and the gradients where dy is given; a sequence
-    and a head at a time, every pair of tokens by itself.  Rows of no sequence: 0."""
+    and a head at a time, every pair of tokens by itself.  Rows of no sequence: 0.
+    keep(b, h, ...) is called with what the steps' gradients are made of."""
     dtype = x.dtype
     half = HALF[dtype] if dtype == torch.bfloat16 else 0.0  # a rounded operand; fp32 has none
     T, H, P = x.shape
@@ -192,6 +193,8 @@ def ssm(x, dt, A, Bm, Cm, cu, D=None, bias=None, softplus=True, h0=None, dy=None
             dd = (A[h] * dg + (X * du).sum(1)) * s
             bd = (u * (A[h].abs() * dga + (X.abs() * dua).sum(1)) + U32 * 8 * dd.abs()) * s + U32 * 4 * dd.abs()
             out["ddt"][0][a:e, h], out["ddt"][1][a:e, h] = dd, bd
+            if keep is not None:
+                keep(b, h, d=d, A=A[h], slope=s, dg=dg, dd=dd, M=M, yx=Z.diagonal(), through=thr)
             out["dA"][0][h] += (d * dg).sum()
             out["dA"][1][h] += u * (d.abs() * dga).sum() * 2
             out["dD"][0][h] += Z.diagonal().sum()
