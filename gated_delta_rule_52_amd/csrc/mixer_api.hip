@@ -67,8 +67,7 @@ gdn_status check_ssm(const gdn_ssm_shape* sh, SsmCall call, gdn_ssm_shape& s)
         if (!*st[i]) *st[i] = row[i];
         if (*st[i] < row[i]) return GDN_ERR_INVALID_ARG;
         if ((*st[i] * e) % 16) return GDN_ERR_ALIGNMENT;
-        // a run of 16 token rows is addressed with 32-bit offsets from its first
-        if (*st[i] > (1LL << 24)) return GDN_ERR_UNSUPPORTED;
+        if (*st[i] > kMostStride) return GDN_ERR_UNSUPPORTED;
     }
     if (call != CALL_STEP) {
         // every workgroup looks for its chunk along the bounds, 64 sequences at a time

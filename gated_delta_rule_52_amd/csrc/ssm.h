@@ -33,7 +33,6 @@ struct SsmArgs {
     void *dx, *dB, *dC;
     float *ddt, *dA, *dD, *dbias;
     long long xs, bs, cs;  // elements between tokens of x, B, C
-    int nb, T, H, G, P, softplus;
 };
 
 // How a call is laid out, from its sizes alone (the lengths are device data).
@@ -49,7 +48,11 @@ struct SsmPlan {
     int splits;         // parts into which the heads of a group are dealt in the gradients
     size_t dec_at, seg_at, tot_at, fwd_at, back_at, token_at, sum_at, part_at, bytes;  // offsets in the workspace
 };
-SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward);
+SsmPlan ssm_plan(const gdn_ssm_shape& s, bool backward);  // ssm_plan.hip
+
+// The most elements between two tokens of x, B or C.  The walk addresses the rows of half
+// a chunk, and the other kernels runs of 16, with 32-bit byte offsets from their first.
+constexpr long long kMostStride = 1LL << 24;
 
 // The decays of every chunk and head; the walk over the chunks (states between them,
 // and the last one into hT; for the gradients forward and backward, and dh0).

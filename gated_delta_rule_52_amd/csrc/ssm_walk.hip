@@ -86,6 +86,8 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
     // of the rows, and half of its slice's values and factors (0 behind the last token,
     // whose rows are copies).
     constexpr int RI = HALF / 4 / RT::PER, VI = HALF / 2 / VT::PER;  // direct loads of a wave
+    // offsets of rows from the half's first fit 31 bits, also where they are not whole loads
+    static_assert((HALF - 1) * kMostStride * (long long)sizeof(T) + RT::BYTES < (1LL << 31), "row offsets");
     const uint32_t r_row = (uint32_t)(g.rs * sizeof(T)), v_row = (uint32_t)(g.vs * sizeof(T));
     struct Source {
         const char *rows, *vals;
@@ -160,7 +162,7 @@ __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& 
     }
 
     // a state as four rows of N after the other, their values side by side: what a lane
-    // holds is stored as it stands (StateAt)
+    // holds is stored as it stands (load_state8 reads it)
     auto store_state = [&](auto* s) {
         typedef std::remove_reference_t<decltype(*s)> S;
 #pragma unroll
