@@ -14,7 +14,7 @@
 // A workgroup is CW words of channels by 256 / CW strips.  Of 64 words a wave is one
 // strip: its rows come as whole kilobytes, and where a sequence ends is a question for
 // scalar registers; of 16 words where 64 would leave more than a fifth of the lanes
-// without a channel.  32768 rows of 1024 bf16: forward 26 us, 5.1 TB/s;
+// without a channel.  32768 rows of 1024 bf16: forward 26 to 27 us, 5.0 TB/s;
 // backward 46 us, 4.4 TB/s (traced; among others 34, with 16 words 41, and 50, without the
 // rows to come on their way 58).
 #include "conv.h"

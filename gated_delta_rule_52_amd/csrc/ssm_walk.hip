@@ -54,7 +54,10 @@ template <typename T, int N> struct WalkLds {
 };
 
 // PHASE 0: all segments of a sequence but the last; 1: all but the first, or the only
-// one.  OUT: states between chunks as T (operands of the outputs), otherwise fp32.
+// one.  OUT: states between chunks as T, rounded to nearest: they are operands of the
+// outputs alone (ssm_out.hip), the walk goes on from its own in fp32, and they are half
+// the bytes.  Otherwise fp32, for the gradients: those of the steps are sums of products
+// with them that have to be as exact as in fp32.
 template <typename T, int N, bool BACK, int PHASE, bool OUT>
 __device__ __forceinline__ void walk_segment(const WalkCall& a, const WalkArgs& g, WalkLds<T, N>& m)
 {
