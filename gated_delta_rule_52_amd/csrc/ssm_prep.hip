@@ -60,7 +60,9 @@ __global__ __launch_bounds__(256) void ssm_prep_kernel(PrepArgs a)
         run += in ? (double)d[k] * a2 : 0.0;
         c[k] = run;
     }
-    const double s = wave_scan(run), total = __shfl(s, 63);
+    // of the lanes before: not a difference, in which a step that is not finite would
+    // reach the lane's earlier tokens
+    const double s = wave_scan(run), total = __shfl(s, 63), up = __shfl_up(s, 1), ahead = l ? up : 0.0;
     const double end = __shfl(s, (l / LB) * LB + LB - 1);
     const double before = __shfl(s, (l / LB) * LB - 1 < 0 ? 0 : (l / LB) * LB - 1);
     const double start = l < LB ? 0.0 : before;
@@ -68,7 +70,7 @@ __global__ __launch_bounds__(256) void ssm_prep_kernel(PrepArgs a)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int t = K * l + k;
-        const double x = c[k] + (s - run);
+        const double x = c[k] + ahead;
         const float hi = (float)x;
         o[DEC_HI * L + t] = hi;
         o[DEC_LO * L + t] = (float)(x - (double)hi);

@@ -220,6 +220,38 @@ private:
     }
 };
 
+// Pairs within a block of 32 tokens are masked: a token may depend on the block's later
+// (or earlier) ones through products with 0, and an infinity or a NaN times that would
+// reach it.  Where a block has such rows, the products take finite ones (finite_only),
+// and what those leave out is added here, times the lane's weight: w holds the weights
+// of the block's rows (row0 .. + 31 of the table), `later`: the lane's token takes the
+// rows from its own on, otherwise those up to its own.
+template <typename T, int D>
+__device__ __forceinline__ void add_masked_rest(f32x16 (&acc)[D / 32], const f32x16& w, const void* tab, int row0, bool later)
+{
+    const int l = lane_id(), t = l & 31;
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {  // rare: with few registers, not fast
+        float mine = 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mine = r == 4 * (j >> 3) + (j & 3) ? w[r] : mine;
+        mine = __shfl(mine, t | (j & 4) << 3);
+        const uint32_t at = Reads<T, D>::row_at(row0 + j);
+        const bool takes = later ? j >= t : j <= t;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 x = Reads<T, D>::row4(tab, at, i, q);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (takes && !(fabsf(x[k]) < INFINITY)) acc[i][4 * q + k] += mine * x[k];
+            }
+        }
+    }
+}
+
 // rows of a tile's accumulator registers 4 i .. 4 i + 3: 8 i + 4 h + 0 .. 3
 __device__ __forceinline__ int acc_rows(int i, int l = lane_id()) { return 8 * i + 4 * (l >> 5); }
 
