@@ -29,6 +29,11 @@
 // the s before it and an s the t behind it, so the parts' waves complement one
 // another on a SIMD.  Each sum is formed within a lane and its other half, in one
 // order.  32768 tokens of 6 heads of 128, N = 128: 206 us.
+//
+// Masked pairs (s behind t within a block of 32) must not let an infinity or a NaN
+// through: their factors are selected away, and where G or Z of a block has such a value
+// the chunk's part is done again with care (CAREFUL).  The sums that find it take
+// 1 % of a call of small heads (in line, the care took the registers of the hot loop).
 #include "ssm_tile.h"
 
 #include "common.h"
@@ -91,6 +96,40 @@ template <typename T> __device__ __forceinline__ Frag<T> ones_below(int b, int l
         for (int j = 0; j < 8; ++j) v[j] = 16 * b + 8 * (j >> 2) + 4 * h + (j & 3) < m ? (minus ? -1.f : 1.f) : 0.f;
         return v;
     }
+}
+
+// Whether a block's products G and Z of all pairs, masked ones among them, are finite: a
+// row of either side that is not leaves none of its own finite.
+__device__ __forceinline__ bool finite_pairs(const f32x16& g, const f32x16& z)
+{
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s += g[r] + z[r];
+    return !__any(!(fabsf(s) < INFINITY));
+}
+
+// The pairs that are not finite, taken out of g (M of the lane's t' and the registers'
+// s), as the products with ones_below would sum them: lane q of 16 gets the sum over
+// t' >= t > s of register q's t.  Rare.
+__device__ __forceinline__ float own_pairs(f32x16& g, int l)
+{
+    f32x16 out;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const bool finite = fabsf(g[r]) < INFINITY;
+        out[r] = finite ? 0.f : g[r];
+        g[r] = finite ? g[r] : 0.f;
+    }
+    float mine = 0.f;
+#pragma unroll 1
+    for (int t = 0; t < 32; ++t) {
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v += acc_rows(r >> 2, l) + (r & 3) < t ? out[r] : 0.f;
+        v = wave_sum((l & 31) >= t ? v : 0.f);
+        if ((l & 15) == 4 * (t >> 3) + (t & 3) && l >> 5 == (t >> 2 & 1)) mine = v;
+    }
+    return mine;
 }
 
 // an operand in plain order as in permuted order (attn.h): 4 of each half's values change places
@@ -198,8 +237,13 @@ template <typename T, int N> struct Grad {
             }
     }
 
+    // Both parts return whether a block's own pairs, the masked ones among them, had a value
+    // that is not finite.  It would reach results that do not depend on it through products
+    // with 0: the chunk's part is then done again with CAREFUL, which keeps such values
+    // from the masked products and adds them where they belong.
+    //
     // the part of the t: dC and r
-    static __device__ __forceinline__ void of_t(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
+    template <bool CAREFUL> static __device__ __forceinline__ bool of_t(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
     {
         const int w = uniform(wave_id()), rb = w, live = k.live, per_head = a.P / kSlice;
         const bool has_s = k.c > 0 || a.h0, has_d = k.c < k.u.chunks - 1 || a.dhT;
@@ -213,6 +257,7 @@ template <typename T, int N> struct Grad {
         f32x16 acc[TN];
 #pragma unroll
         for (int i = 0; i < TN; ++i) acc[i] = zero16();
+        bool seen = false;
         float r_state = 0.f, r_blocks = 0.f, over_own = 0.f, dot = 0.f, cross0 = 0.f, cross1 = 0.f;
 
         for (int slice = k.h_first * per_head; slice < k.h_last * per_head; ++slice) {
@@ -305,6 +350,7 @@ template <typename T, int N> struct Grad {
                             cross1 += sb ? all : 0.f;
                         }
                     } else {
+                        if constexpr (!CAREFUL) seen |= !finite_pairs(gm, z);
                         const float hc = hi_s[at], lc = lo_s[at];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -313,15 +359,17 @@ template <typename T, int N> struct Grad {
                                         ds = *reinterpret_cast<const f32x4*>(d_s + s);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                // pairs that are none: exp2(-inf)
-                                z[4 * i + j] *= exp2_hw(s + j <= at ? (hc - hs[j]) + (lc - ls[j]) : -INFINITY) * ds[j];
-                                gm[4 * i + j] *= s + j < at && at < live ? z[4 * i + j] : 0.f;
+                                // selected: pairs that are none may be anything
+                                const float e = exp2_hw((hc - hs[j]) + (lc - ls[j])) * ds[j];
+                                z[4 * i + j] = s + j <= at ? z[4 * i + j] * e : 0.f;
+                                gm[4 * i + j] = s + j < at && at < live ? gm[4 * i + j] * z[4 * i + j] : 0.f;
                             }
                         }
                         // over[t][t'] = sum_{s < t} M_t's, then for every t the sum over t' >= t.
                         // The bf16 products round their sums down a little on average, which
                         // sums over all tokens (dA, ddt_bias) would show: every other block of
                         // tokens sums -M, and the smallest parts come first.
+                        if constexpr (CAREFUL) over_own += own_pairs(gm, l);
                         const bool minus = w & 1;
                         f32x16 over = zero16();
                         Frag<T> parts[2][PARTS];
@@ -344,10 +392,17 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const Frag<T> zv = acc_frag<T>(z, b);
+                        if (CAREFUL && sb == rb) {
 #pragma unroll
-                        for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * sb + 16 * b, 32 * i), zv, acc[i]);
-                        ordered<T, TN, 2>();
+                            for (int i = 0; i < TN; ++i)
+                                acc[i] = mma32(finite_only(NRead::down(m.rows, ndn, 32 * sb + 16 * b, 32 * i)), zv, acc[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * sb + 16 * b, 32 * i), zv, acc[i]);
+                            ordered<T, TN, 2>();
+                        }
                     }
+                    if (CAREFUL && sb == rb) add_masked_rest<T, N>(acc, z, m.rows, 32 * sb, false);
                 }
                 r_blocks += r;
             }
@@ -372,10 +427,11 @@ template <typename T, int N> struct Grad {
             __syncthreads();
         }
         store(a, k, acc, false, 32 * rb + (lane_id() & 31));
+        return seen;
     }
 
     // the part of the s: dx, dB and q
-    static __device__ __forceinline__ void of_s(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
+    template <bool CAREFUL> static __device__ __forceinline__ bool of_s(const GradArgs& a, const Chunk& k, GradLds<T, N>& m)
     {
         const int w = uniform(wave_id()), rb = w, live = k.live, per_head = a.P / kSlice;
         const bool has_d = k.c < k.u.chunks - 1 || a.dhT;
@@ -390,6 +446,7 @@ template <typename T, int N> struct Grad {
         f32x16 acc[TN];
 #pragma unroll
         for (int i = 0; i < TN; ++i) acc[i] = zero16();
+        bool seen = false;
         float q_blocks = 0.f, q_state = 0.f, xdu = 0.f, xdy = 0.f;
 
         for (int slice = k.h_first * per_head; slice < k.h_last * per_head; ++slice) {
@@ -480,6 +537,7 @@ template <typename T, int N> struct Grad {
                             }
                         }
                     } else {
+                        if constexpr (!CAREFUL) seen |= !finite_pairs(gm, z);
                         const float hc = hi_s[at], lc = lo_s[at];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -487,13 +545,14 @@ template <typename T, int N> struct Grad {
                             const f32x4 ht = *reinterpret_cast<const f32x4*>(hi_s + t), lt = *reinterpret_cast<const f32x4*>(lo_s + t);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                // pairs that are none: exp2(-inf)
-                                const float e = exp2_hw(at <= t + j && t + j < live ? (ht[j] - hc) + (lt[j] - lc) : -INFINITY);
-                                const float eg = e * gm[4 * i + j], zv = z[4 * i + j];
-                                xdu = __builtin_fmaf(eg, zv, xdu);
+                                // selected: pairs that are none may be anything
+                                const bool pair = at <= t + j && t + j < live;
+                                const float e = exp2_hw((ht[j] - hc) + (lt[j] - lc));
+                                const float eg = pair ? e * gm[4 * i + j] : 0.f, zv = z[4 * i + j];
+                                xdu = pair ? __builtin_fmaf(eg, zv, xdu) : xdu;
                                 xdy += t + j == at ? zv : 0.f;
                                 gm[4 * i + j] = eg;
-                                z[4 * i + j] = e * zv * d_s;
+                                z[4 * i + j] = pair ? e * zv * d_s : 0.f;
                             }
                         }
                     }
@@ -501,11 +560,24 @@ template <typename T, int N> struct Grad {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const Frag<T> mv = acc_frag<T>(gm, b), zv = acc_frag<T>(z, b);
+                        if (CAREFUL && tb == rb) {
 #pragma unroll
-                        for (int pt = 0; pt < 2; ++pt) du[pt] = mma32(VRead::down(m.vals, vdn, 32 * tb + 16 * b, 32 * pt), mv, du[pt]);
+                            for (int pt = 0; pt < 2; ++pt)
+                                du[pt] = mma32(finite_only(VRead::down(m.vals, vdn, 32 * tb + 16 * b, 32 * pt)), mv, du[pt]);
 #pragma unroll
-                        for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * tb + 16 * b, 32 * i), zv, acc[i]);
-                        ordered<T, 2 + TN, 2>();
+                            for (int i = 0; i < TN; ++i)
+                                acc[i] = mma32(finite_only(NRead::down(m.rows, ndn, 32 * tb + 16 * b, 32 * i)), zv, acc[i]);
+                        } else {
+#pragma unroll
+                            for (int pt = 0; pt < 2; ++pt) du[pt] = mma32(VRead::down(m.vals, vdn, 32 * tb + 16 * b, 32 * pt), mv, du[pt]);
+#pragma unroll
+                            for (int i = 0; i < TN; ++i) acc[i] = mma32(NRead::down(m.rows, ndn, 32 * tb + 16 * b, 32 * i), zv, acc[i]);
+                            ordered<T, 2 + TN, 2>();
+                        }
+                    }
+                    if (CAREFUL && tb == rb) {
+                        add_masked_rest<T, kSlice>(du, gm, m.vals, 32 * tb, true);
+                        add_masked_rest<T, N>(acc, z, m.rows, 32 * tb, true);
                     }
                 }
             }
@@ -540,6 +612,7 @@ template <typename T, int N> struct Grad {
             __syncthreads();
         }
         store(a, k, acc, true, 32 * rb + (lane_id() & 31));
+        return seen;
     }
 };
 
@@ -567,10 +640,13 @@ __global__ __launch_bounds__(64 * (SsmTile<T>::L / 32), sizeof(T) == 2 ? 2 : 1) 
     k.sp = job - k.g * a.splits;
     k.h_first = k.g * per_group + (int)((long long)per_group * k.sp / a.splits);
     k.h_last = k.g * per_group + (int)((long long)per_group * (k.sp + 1) / a.splits);
-    if (is_s)
-        Grad<T, N>::of_s(a, k, m);
-    else
-        Grad<T, N>::of_t(a, k, m);
+    const bool seen = is_s ? Grad<T, N>::template of_s<false>(a, k, m) : Grad<T, N>::template of_t<false>(a, k, m);
+    if (__builtin_expect(__syncthreads_or(seen), 0)) {
+        if (is_s)
+            Grad<T, N>::template of_s<true>(a, k, m);
+        else
+            Grad<T, N>::template of_t<true>(a, k, m);
+    }
 }
 
 // dB and dC from the parts of a group's heads, in order: a word of 4 values a thread.

@@ -22,6 +22,29 @@ __device__ __forceinline__ double wave_scan(double x)
     }
     return x;
 }
+// sums over the other lanes of a run of W, before the lane and behind it
+template <int W> __device__ __forceinline__ double lanes_before(double x)
+{
+    const int at = lane_id() % W;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const double up = __shfl_up(x, o, W);
+        if (at >= o) x += up;
+    }
+    x = __shfl_up(x, 1, W);
+    return at ? x : 0.0;
+}
+template <int W> __device__ __forceinline__ double lanes_behind(double x)
+{
+    const int at = lane_id() % W;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const double down = __shfl_down(x, o, W);
+        if (at + o < W) x += down;
+    }
+    x = __shfl_down(x, 1, W);
+    return at < W - 1 ? x : 0.0;
+}
 __device__ __forceinline__ double wave_sum(double x)
 {
 #pragma unroll
@@ -111,7 +134,7 @@ __global__ __launch_bounds__(256) void ssm_finish_kernel(FinishArgs a)
     const size_t row0 = (size_t)u.start + (size_t)u.at * L, at = (size_t)blockIdx.x * a.H + head;
     const float *v = a.token + at * kTokens<L>, *dec = a.dec + at * kDecays<L>;
     float d[K], xdu[K], zd[K], dgd[K];
-    double ri[K], ro[K], qo[K], qi[K], sri = 0, sro = 0, sqo = 0, sqi = 0;
+    double ri[K], ro[K], qo[K], qi[K], sri = 0, sro = 0, sqo = 0, sqi = 0;  // of the lane
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int t = K * l + k;
@@ -126,12 +149,10 @@ __global__ __launch_bounds__(256) void ssm_finish_kernel(FinishArgs a)
         dgd[k] = v[TOK_OWN * L + t];
         sri += ri[k], sro += ro[k], sqo += qo[k], sqi += qi[k];
     }
-    const int last = (l / LB) * LB + LB - 1;
-    const double ci = wave_scan(sri), co = wave_scan(sro), po = wave_scan(sqo), pi = wave_scan(sqi);
-    // from the lane's first token on, to the chunk's and to the block's end; before it, from their starts
-    double all_r = __shfl(ci, 63) - (ci - sri), own_r = __shfl(co, last) - (co - sro);
-    const double first = __shfl(po, last - LB < 0 ? 0 : last - LB);
-    double own_q = po - sqo - (l < LB ? 0.0 : first), all_q = pi - sqi;
+    // of the lanes behind, to the chunk's and to the block's end, and of those before, from
+    // their starts: no differences, in which a token that is not finite would reach others
+    const double all_r = lanes_behind<64>(sri), own_r = lanes_behind<LB>(sro), own_q = lanes_before<LB>(sqo),
+                 all_q = lanes_before<64>(sqi);
     const float* more = v + TOK_ROWS * L;
     double rest = 0;
 #pragma unroll
@@ -147,9 +168,9 @@ __global__ __launch_bounds__(256) void ssm_finish_kernel(FinishArgs a)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int t = K * l + k;
-        const double dg = all_r + own_r + own_q + all_q + rest + (double)dgd[k];
-        all_r -= ri[k], own_r -= ro[k];
-        all_q += qi[k], own_q += qo[k];
+        double dg = all_r + own_r + own_q + all_q + rest + (double)dgd[k];
+#pragma unroll
+        for (int j = 0; j < K; ++j) dg += j < k ? qi[j] + qo[j] : ri[j] + ro[j];
         if (t < live) {
             const size_t o = (row0 + t) * a.H + head;
             double dd = (double)A * dg + (double)xdu[k];

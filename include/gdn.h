@@ -468,10 +468,9 @@ gdn_status gdn_conv_step(const gdn_conv_shape *shape, const void *x, const float
  * not tested.  N and P in {64, 128}; H a multiple of G, at most 1024; T * H < 2^27,
  * B * H < 2^23, B at most 65536 but for single tokens; strides at most 2^24.  Of bounds
  * that decrease, one below an earlier one counts as that one.
- * A value that is not finite reaches no other sequence and no other head's output,
- * and in y and hT the results that depend on it and no others; in the gradients it
- * may reach, within its sequence and head, the other results of its chunk of 128
- * tokens (float32: 64).
+ * A value that is not finite reaches the results that depend on it and no others; a
+ * step (dt) that is not may reach all gradients of its head in its sequence, and of
+ * the group's B and C there.
  *
  * gdn_ssm_forward: y, and hT the state behind each sequence (NULL: not written; may
  * be h0; a sequence without rows keeps its state).

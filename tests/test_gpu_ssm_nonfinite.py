@@ -6,7 +6,7 @@ import torch
 
 from gpu_util import log
 from test_gpu_attention import DT, NAN
-from test_gpu_ssm import forward, make
+from test_gpu_ssm import GRADS, backward, forward, make
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,81 @@ def test_several_values_in_a_block(dtype):
     y = forward(dict(s, x=t), CU)[0]
     torch.cuda.synchronize()
     check({"y": clean}, {"y": y}, {"y": may})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_gradients(dtype, heads, value):
+    """dy and C reach what lies before their token, x and B what lies behind: dx and dB of
+    the tokens up to it, dC of those from it on, and the steps on the way."""
+    H, G, N, P = heads
+    s = make(CU[-1], 3, *heads, DT[dtype])
+    run = lambda s: dict(zip(GRADS, backward(s, CU)))  # noqa: E731
+    clean = run(s)
+    lo, hi = CU[1], CU[2]
+    h, g, n, p = 1, 1 // (H // G), N - 5, P - 3
+    of = slice(g * (H // G), (g + 1) * (H // G))
+    for place in PLACES:
+        t = lo + place
+        for name in ("x", "dy", "B", "C"):
+            may, own = nothing(clean), slice(h, h + 1) if name in ("x", "dy") else of
+            got = run(spoiled(s, name, (t, h, p) if name in ("x", "dy") else (t, g, n), value))
+            may["ddt_bias"][own] = True
+            # nothing decays what the last token puts in: dg is of the tokens behind it
+            may["dA"][own] = name in ("dy", "C") or t < hi - 1
+            if name == "x":
+                may["dB"][t, g] = may["dC"][t:hi, g] = may["ddt"][t:hi, h] = may["dD"][h] = True
+            elif name == "dy":
+                may["dx"][lo:t + 1, h, p] = may["dB"][lo:t + 1, g] = may["dC"][t, g] = may["ddt"][lo:t + 1, h] = True
+                may["dh0"][1, h, :, p] = may["dD"][h] = True
+            elif name == "B":
+                may["dx"][t, of] = may["dC"][t:hi, g, n] = may["ddt"][t:hi, of] = True
+            else:
+                may["dx"][lo:t + 1, of] = may["dB"][lo:t + 1, g, n] = may["ddt"][lo:t + 1, of] = may["dh0"][1, of, n] = True
+            torch.cuda.synchronize()
+            log(f"gradients {dtype} {heads} {value} in {name} at {place}")
+            check(clean, got, may)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_states_that_are_not_finite(dtype):
+    """h0 reaches dC and the steps of all its sequence, dhT dx, dB, dh0 and the steps."""
+    s = make(CU[-1], 3, 4, 2, 64, 64, DT[dtype])
+    run = lambda s: dict(zip(GRADS, backward(s, CU)))  # noqa: E731
+    clean = run(s)
+    at = slice(CU[1], CU[2])
+    for name in ("h0", "dhT"):
+        may = nothing(clean)
+        may["ddt"][at, 3] = may["dA"][3] = may["ddt_bias"][3] = True
+        if name == "h0":
+            may["dC"][at, 1, 9] = True
+        else:
+            may["dx"][at, 3, 7] = may["dB"][at, 1, 9] = may["dh0"][1, 3, 9, 7] = True
+        got = run(spoiled(s, name, (1, 3, 9, 7), NAN))
+        torch.cuda.synchronize()
+        check(clean, got, may)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("place", [0, 100, 299])
+def test_steps_that_are_not_finite_stay_in_their_sequence_and_head(dtype, place):
+    """In the gradients: of the head in its sequence, and of its group there."""
+    H, G = 4, 2
+    s = make(CU[-1], 3, H, G, 64, 64, DT[dtype])
+    clean = backward(s, CU)
+    got = backward(spoiled(s, "dt", (CU[1] + place, 1), NAN), CU)
+    torch.cuda.synchronize()
+    at = slice(CU[1], CU[2])
+    for k, a, b in zip(GRADS, clean, got):
+        same = torch.ones(a.shape, dtype=torch.bool, device="cuda")
+        if k in ("dx", "ddt"):
+            same[at, 1] = False
+        elif k in ("dB", "dC"):
+            same[at, 0] = False
+        elif k == "dh0":
+            same[1, 1] = False
+        else:
+            same[1] = False
+        assert torch.equal(a[same], b[same]), k
+        assert k in ("dB", "dC", "dD") or not torch.isfinite(b[~same]).all(), k
