@@ -28,7 +28,7 @@
 // workgroups share a compute unit and one computes while the other loads.  A t has
 // the s before it and an s the t behind it, so the parts' waves complement one
 // another on a SIMD.  Each sum is formed within a lane and its other half, in one
-// order.  32768 tokens of 6 heads of 128, N = 128: 206 us.
+// order.  32768 tokens of 6 heads of 128, N = 128: 193 to 197 us.
 //
 // Masked pairs (s behind t within a block of 32) must not let an infinity or a NaN
 // through: their factors are selected away, and where G or Z of a block has such a value

@@ -8,7 +8,7 @@
 // and its registers are the s: the decay, the causal limit and delta are applied
 // there, and the result is the next product's operand as it stands.  That product
 // gives y^T, so that a lane stores neighbouring values of its token.  32768 tokens of 6
-// heads of 128, N = 128: 54 us.  No unit is full (matrix units 12 %): a wave's loads,
+// heads of 128, N = 128: 55 us.  No unit is full (matrix units 13 %): a wave's loads,
 // products and the vector work between them follow one another, and two workgroups share
 // a compute unit.
 //
